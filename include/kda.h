@@ -357,6 +357,130 @@ int kda_bwd(const void *q, const void *k, const void *v, const void *g, const vo
             float *dbeta, float *dgate, float *d_initial_state, void *workspace,
             size_t workspace_bytes, kda_stream_t stream);
 
+/* ------------------------------------ linear attention, one decay per head
+ * The same layer family with the forget gate of one number per head instead
+ * of one per key channel, and a plain write (no delta rule): per (sequence n,
+ * head h) a state S in R^{dk x dv} (fp32), and for every token t
+ *   S <- exp(g_t) S + k_t v_t^T,   o_t = S^T (scale q_t).
+ *
+ * Layouts as above (packed, contiguous), with
+ *   q, k      [total_tokens][Hk][dk]: Hk key heads, H % Hk == 0; head h reads
+ *             q and k of head h / (H / Hk)
+ *   v, out    [total_tokens][H][dv]
+ *   g         [total_tokens][H], or [H] with KDA_LIN_DECAY_PER_HEAD: the
+ *             log-decay, g <= 0.  There is no floor; -inf forgets everything.
+ *   states    [num_seqs][H][dk][dv] fp32
+ * dk, dv in {64, 128}; dtype BF16 or F32, shared by q, k, v, g, out and the
+ * gradients (states are fp32).  Inputs must be finite (g may be -inf).
+ * Alignment: q, k, v, out, states, workspace 16 bytes, g its element size.
+ *
+ * Tokens outside every sequence (behind cu_seqlens[num_seqs], when the host
+ * copy is not given) are neither read nor written; device offsets that are
+ * not monotone are clamped into [0, total_tokens] and give undefined values.
+ */
+#define KDA_LIN_DECAY_PER_HEAD 1 /* g is [H] (and dg [H]): the same decay at every token */
+
+/* Bytes of workspace kda_lin_chunk_fwd needs on the current CUDA device (the
+ * plan depends on its SM count); 0 for invalid sizes. */
+size_t kda_lin_chunk_fwd_workspace_size(int32_t total_tokens, int32_t num_seqs, int32_t H,
+                                        int32_t Hk, int32_t dk, int32_t dv, kda_dtype dtype);
+
+/*
+ * Prefill over packed sequences.
+ *   cu_seqlens, cu_seqlens_host, num_seqs, total_tokens, scale: as
+ *                   kda_chunk_fwd.
+ *   flags           0 or KDA_LIN_DECAY_PER_HEAD; other bits ->
+ *                   KDA_ERR_INVALID_ARG.
+ *   initial_state   NULL = zeros.
+ *   final_state     NULL = not written.  May alias initial_state exactly; no
+ *                   other aliasing of any two arguments is allowed.
+ *   workspace       >= kda_lin_chunk_fwd_workspace_size(...) bytes; calls that
+ *                   overlap on the GPU need one each.
+ * Results are deterministic.  Errors as kda_chunk_fwd.
+ */
+int kda_lin_chunk_fwd(const void *q, const void *k, const void *v, const void *g, void *out,
+                      const int32_t *cu_seqlens, const int32_t *cu_seqlens_host, int32_t num_seqs,
+                      int32_t total_tokens, int32_t H, int32_t Hk, int32_t dk, int32_t dv,
+                      kda_dtype dtype, float scale, int32_t flags, const float *initial_state,
+                      float *final_state, void *workspace, size_t workspace_bytes,
+                      kda_stream_t stream);
+
+/* One token per sequence: q, k [num_seqs][Hk][dk]; v, out [num_seqs][H][dv];
+ * g [num_seqs][H] or [H]; state [num_seqs][H][dk][dv] fp32, updated in place.
+ * No workspace. */
+int kda_lin_decode_step(const void *q, const void *k, const void *v, const void *g, void *out,
+                        float *state, int32_t num_seqs, int32_t H, int32_t Hk, int32_t dk,
+                        int32_t dv, kda_dtype dtype, float scale, int32_t flags,
+                        kda_stream_t stream);
+
+/*
+ * Gradients of kda_lin_chunk_fwd for L = sum dy (.) out + sum d_final_state
+ * (.) final_state.  dq, dk_out [total_tokens][Hk][dk] (summed over the heads
+ * that share a key head), dv_out [total_tokens][H][dv], dg [total_tokens][H]
+ * or [H], all in dtype, rounded once (they feed the backward of the layers
+ * before, which take dtype; kda_bwd returns fp32); d_initial_state
+ * [num_seqs][H][dk][dv] fp32 or NULL.  initial_state and d_final_state may be
+ * NULL (zeros).  No aliasing.  Deterministic.
+ */
+size_t kda_lin_bwd_workspace_size(int32_t total_tokens, int32_t num_seqs, int32_t H, int32_t Hk,
+                                  int32_t dk, int32_t dv);
+int kda_lin_bwd(const void *q, const void *k, const void *v, const void *g, const void *dy,
+                const int32_t *cu_seqlens, const int32_t *cu_seqlens_host, int32_t num_seqs,
+                int32_t total_tokens, int32_t H, int32_t Hk, int32_t dk, int32_t dv,
+                kda_dtype dtype, float scale, int32_t flags, const float *initial_state,
+                const float *d_final_state, void *dq, void *dk_out, void *dv_out, void *dg,
+                float *d_initial_state, void *workspace, size_t workspace_bytes,
+                kda_stream_t stream);
+
+/* ------------------------------------------------- norms around a block
+ * The norm of a block's output fused with its gate and the scaled residual,
+ * and the next block's norm (a KDA layer's per-head output norm with its
+ * sigmoid gate is the case rows = tokens * H, D = dv, no residual):
+ *   yn = y * rsqrt(mean(y^2) + eps) * post_weight   (KDA_NORM_POST, else yn = y)
+ *   out    = residual + res_scale * (act(gate) * yn)
+ *   normed = out * rsqrt(mean(out^2) + eps) * pre_weight   (KDA_NORM_PRE)
+ * per row of D elements.  act is the identity, the logistic function
+ * (KDA_NORM_GATE_SIGMOID) or z * logistic(z) (KDA_NORM_GATE_SILU).  Row
+ * statistics are fp32 and normed is taken from the unrounded out.
+ *
+ *   y, gate, residual  [rows][D] in dtype, elements of a row contiguous, rows
+ *                      *_stride elements apart (>= D); gate and residual may
+ *                      be NULL.
+ *   post_weight, pre_weight  [D] in dtype or NULL (ones); only with their flag.
+ *   out, normed        [rows][D] contiguous; normed exactly when KDA_NORM_PRE.
+ *                      Each may replace y, gate or residual exactly (same
+ *                      address, stride D); no other overlap.
+ * 1 <= D <= 16384.  Pointers are aligned to their element size (16-byte
+ * aligned rows are faster).
+ */
+#define KDA_NORM_POST 1
+#define KDA_NORM_PRE 2
+#define KDA_NORM_GATE_SIGMOID 4
+#define KDA_NORM_GATE_SILU 8
+
+int kda_block_norm(const void *y, int64_t y_stride, const void *post_weight, const void *gate,
+                   int64_t gate_stride, const void *residual, int64_t residual_stride,
+                   const void *pre_weight, void *out, void *normed, int64_t rows, int32_t D,
+                   kda_dtype dtype, float res_scale, float eps, int32_t flags,
+                   kda_stream_t stream);
+
+/*
+ * Its gradient, from the same inputs.  dout, dnormed [rows][D] contiguous,
+ * either NULL = zeros (dnormed only with KDA_NORM_PRE); dy, dgate, dresidual
+ * [rows][D] contiguous in dtype (dgate, dresidual NULL = not wanted);
+ * dpost_weight, dpre_weight [D] fp32, NULL = not wanted.  workspace
+ * (16-byte aligned, >= kda_block_norm_bwd_workspace_size bytes) is needed when
+ * a weight gradient is wanted.  No aliasing.  Deterministic.
+ */
+size_t kda_block_norm_bwd_workspace_size(int64_t rows, int32_t D, kda_dtype dtype);
+int kda_block_norm_bwd(const void *dout, const void *dnormed, const void *y, int64_t y_stride,
+                       const void *post_weight, const void *gate, int64_t gate_stride,
+                       const void *residual, int64_t residual_stride, const void *pre_weight,
+                       void *dy, void *dgate, void *dresidual, float *dpost_weight,
+                       float *dpre_weight, int64_t rows, int32_t D, kda_dtype dtype,
+                       float res_scale, float eps, int32_t flags, void *workspace,
+                       size_t workspace_bytes, kda_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

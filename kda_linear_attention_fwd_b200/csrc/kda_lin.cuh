@@ -1,0 +1,67 @@
+// Linear attention with one decay per head: shared definitions.
+//
+// Per (sequence n, head h), S in R^{dk x dv} (fp32):
+//   S_t = exp(g_t) S_{t-1} + k_t v_t^T,   o_t = S_t^T (scale q_t),
+// g_t <= 0 one number per token and head (or per head).  q and k have Hk
+// heads, head h reads head h / (H / Hk).
+//
+// Windows: the packed token axis is cut into W equal windows of `win` tokens,
+// and one CTA runs the tokens of one (window, head), sequence after sequence,
+// so the load is even whatever the sequence lengths are and no table has to be
+// made on the device.  The state that enters a window in the middle of a
+// sequence comes from the windows before it: a window maps it as
+// S -> gamma S + Z (the decay is one number per head, so the transition is
+// one number), every window's (gamma, Z) is made in parallel by a summary
+// pass, and a scan over the windows turns Z into the incoming states.
+//
+// Reverse passes (the gradient) run the same recurrence from the last token
+// to the first: the state is dL/dS_t, which step t reaches with the decay of
+// token t + 1.  There "init" is dL/d(final state) and "final" dL/d(initial
+// state), which also takes the decay of the sequence's first token.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace kda {
+namespace lin {
+
+// Log-decays below this leave nothing of an fp32 state (exp(-104) is 0 in
+// fp32), so clamping there changes no result; it keeps sums of -inf finite.
+constexpr float kMinG = -110.f;
+
+// A window whose outgoing state nobody reads (no sequence crosses its end).
+constexpr float kNoCarry = -1.f;
+
+struct Params {
+    // one pass of the recurrence: state [DA][DB] += wr (x) val, out = state^T rd
+    const void *rd, *wr;    // [T][H / rd_div][DA], [T][H / wr_div][DA]
+    const void *val;        // [T][H / val_div][DB]
+    const void *ext;        // [T][H / ext_div][DB]: xdot_t = out_t . ext_t (gradient passes)
+    int rd_div, wr_div, val_div, ext_div;
+    float rd_scale, wr_scale;
+    const void *g;          // [T][H], or [H] when g_per_head
+    int g_per_head;
+    void *out;              // [T][H][DB], input type (or fp32 when out_f32)
+    int out_f32;
+    const int32_t *cu;
+    int num_seqs, T, H, W, win;
+    const float *init;      // [num_seqs][H] states or null; transposed ([DB][DA]) when init_t
+    float *final_state;     // same layout, or null
+    int init_t;
+    float *win_state;       // [W][H] states [DA][DB]: Z out of the summary, incoming states after the scan
+    int win_t;              // the pass reads them transposed
+    float *gamma;           // [W][H]
+    float *start_copy;      // [W][H] states or null.  When final_state is init, the summary keeps here the
+                            // initial state of the sequence that starts in the window and crosses its end:
+                            // its last window overwrites that state in the same launch
+    // gradient passes
+    float *xdot;            // [T][H]: q . dq, written by the dq pass, read by the dk pass
+    float *ckpt;            // [slots][H][DA][DB]: the state after each 64-token chunk
+    void *dg;               // [T][H], input type, or fp32 when g_per_head
+    int zero_first_dg;      // no initial state: d(first log-decay) is exactly 0
+};
+
+}  // namespace lin
+}  // namespace kda

@@ -1,0 +1,357 @@
+// C-ABI entry points of linear attention with one decay per head (declared in
+// include/kda.h): argument checks, the window plan and the launch sequences.
+// No allocation, no host synchronisation, no exceptions across the boundary.
+#include <algorithm>
+
+#include "../../include/kda.h"
+#include "kda_args.h"
+#include "kda_common.cuh"
+#include "kda_lin.cuh"
+
+namespace kda {
+namespace lin {
+
+cudaError_t launch_rec(const Params &p, int mode, bool is_bf16, int da, int db, cudaStream_t st);
+cudaError_t launch_scan(float *z, const float *gamma, int W, int H, int elems, bool rev, cudaStream_t st);
+cudaError_t launch_decode(bool bf16, int dk, int dv, const void *q, const void *k, const void *v, const void *g,
+                          void *out, float *state, long nh, int H, int rep, int g_per_head, float scale, int sms,
+                          cudaStream_t st);
+enum { kFwd, kSum, kSumR, kDq, kDk, kDv };  // launch_rec's modes
+
+// out[t][hk][i] = sum over r of in[t][hk * rep + r][i]: the gradient of a head
+// shared by rep heads, rounded once.  D a multiple of 4.
+template <typename T>
+__global__ void __launch_bounds__(256) head_sum_kernel(const float4 *in, T *out, long n4, int rep, int d4) {
+    for (long i = (long)blockIdx.x * 256 + threadIdx.x; i < n4; i += (long)gridDim.x * 256) {
+        const long th = i / d4, c = i % d4;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int r = 0; r < rep; ++r) {
+            const float4 x = __ldcs(in + (th * rep + r) * d4 + c);
+            a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
+        }
+        st(out + 4 * i, a.x); st(out + 4 * i + 1, a.y); st(out + 4 * i + 2, a.z); st(out + 4 * i + 3, a.w);
+    }
+}
+
+// Column sums of x [T][H] in two steps whose order is fixed: per block of
+// kSumRows rows, then over the blocks.
+constexpr int kSumRows = 512;
+__global__ void __launch_bounds__(256) token_sum_kernel(const float *x, float *part, int T, int H) {
+    __shared__ float s[8][33];
+    const int hx = threadIdx.x & 31, ry = threadIdx.x >> 5, h = blockIdx.y * 32 + hx;
+    const int t0 = blockIdx.x * kSumRows, t1 = min(T, t0 + kSumRows);
+    float a = 0.f;
+    if (h < H)
+        for (int t = t0 + ry; t < t1; t += 8) a += x[(size_t)t * H + h];
+    s[ry][hx] = a;
+    __syncthreads();
+    if (ry == 0 && h < H) {
+#pragma unroll
+        for (int i = 1; i < 8; ++i) a += s[i][hx];
+        part[(size_t)blockIdx.x * H + h] = a;
+    }
+}
+template <typename T>
+__global__ void __launch_bounds__(256) part_sum_kernel(const float *part, T *out, int parts, int H) {
+    __shared__ float s[8][33];
+    const int hx = threadIdx.x & 31, ry = threadIdx.x >> 5, h = blockIdx.x * 32 + hx;
+    float a = 0.f;
+    if (h < H)
+        for (int i = ry; i < parts; i += 8) a += part[(size_t)i * H + h];
+    s[ry][hx] = a;
+    __syncthreads();
+    if (ry == 0 && h < H) {
+#pragma unroll
+        for (int i = 1; i < 8; ++i) a += s[i][hx];
+        st(out + h, a);
+    }
+}
+
+}  // namespace lin
+}  // namespace kda
+
+namespace {
+
+using kda::is_aligned;
+using kda::lin::Params;
+
+int sm_count() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
+        cudaGetLastError();
+        n = 148;
+    }
+    return n;
+}
+
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+struct Windows {
+    int win, W;
+};
+// Windows of a multiple of 64 tokens, as many as fill two CTAs per SM once.
+// A call with more than one window also runs the summary pass (about 0.6 of
+// the time of the main one) and the scan, so short calls stay in one.
+Windows choose_windows(int T, int H) {
+    const long slots = 2L * sm_count();
+    const long target = std::max(1L, slots / H);
+    long win = ((T + target - 1) / target + 63) / 64 * 64;
+    win = std::max(win, 64L);
+    if (1.6 * win + 40 >= T) win = std::max((T + 63L) / 64 * 64, 64L);
+    return {(int)win, std::max(1, (int)((T + win - 1) / win))};
+}
+
+struct FwdLayout {
+    size_t gamma, z, start, total;
+};
+FwdLayout fwd_layout(const Windows &wd, int H, int dk, int dv) {
+    FwdLayout L;
+    const size_t states = (size_t)wd.W * H * dk * dv * sizeof(float);
+    size_t o = 0;
+    L.gamma = o; o = align256(o + (size_t)wd.W * H * sizeof(float));
+    L.z = o;     o = align256(o + states);
+    L.start = o; o = align256(o + states);
+    L.total = o;
+    return L;
+}
+
+struct BwdLayout {
+    size_t gamma_f, gamma_r, zf, zr, xdot, ckpt, dgt, part, dq, dk, total;
+};
+BwdLayout bwd_layout(const Windows &wd, int T, int N, int H, int Hk, int dk, int dv) {
+    BwdLayout L;
+    const size_t states = (size_t)wd.W * H * dk * dv * sizeof(float), th = (size_t)T * H * sizeof(float);
+    size_t o = 0;
+    L.gamma_f = o; o = align256(o + (size_t)wd.W * H * sizeof(float));
+    L.gamma_r = o; o = align256(o + (size_t)wd.W * H * sizeof(float));
+    L.zf = o;      o = align256(o + states);
+    L.zr = o;      o = align256(o + states);
+    L.xdot = o;    o = align256(o + th);
+    L.ckpt = o;    o = align256(o + ((size_t)T / 64 + N + 1) * H * dk * dv * sizeof(float));
+    L.dgt = o;     o = align256(o + th);
+    L.part = o;    o = align256(o + ((size_t)T / kda::lin::kSumRows + 1) * H * sizeof(float));
+    L.dq = o;      o = align256(o + (H == Hk ? 0 : th * dk));
+    L.dk = o;      o = align256(o + (H == Hk ? 0 : th * dk));
+    L.total = o;
+    return L;
+}
+
+int check_sizes(int32_t num_seqs, int32_t T, int32_t H, int32_t Hk, int32_t dk, int32_t dv, kda_dtype dtype,
+                int32_t flags) {
+    const int rc = kda::check_prefill_sizes(num_seqs, T, H, dk, dv, dtype);
+    if (rc != KDA_OK) return rc;
+    if (Hk < 1 || H % Hk != 0 || (flags & ~KDA_LIN_DECAY_PER_HEAD)) return KDA_ERR_INVALID_ARG;
+    if (H > (1 << 20)) return KDA_ERR_UNSUPPORTED;
+    return KDA_OK;
+}
+
+bool overlap(const void *a, const void *b, size_t bytes) {
+    return a && b && (const char *)a < (const char *)b + bytes && (const char *)b < (const char *)a + bytes;
+}
+
+// the checks that the packed calls share; `a16` must be 16-byte aligned
+int check_packed(const int32_t *cu, const int32_t *cu_host, int32_t num_seqs, int32_t T, const void *g, size_t esz,
+                 const void *const *a16, int n16) {
+    if (!cu) return KDA_ERR_INVALID_ARG;
+    for (int i = 0; i < n16; ++i)
+        if (a16[i] && !is_aligned(a16[i], 16)) return KDA_ERR_ALIGNMENT;
+    if (!is_aligned(g, esz) || !is_aligned(cu, 4)) return KDA_ERR_ALIGNMENT;
+    if (cu_host) {
+        if (cu_host[0] != 0 || cu_host[num_seqs] != T) return KDA_ERR_INVALID_ARG;
+        for (int n = 0; n < num_seqs; ++n)
+            if (cu_host[n + 1] < cu_host[n]) return KDA_ERR_INVALID_ARG;
+    }
+    return KDA_OK;
+}
+
+template <typename F> bool ok(F e) { return e == cudaSuccess; }
+
+}  // namespace
+
+extern "C" {
+
+size_t kda_lin_chunk_fwd_workspace_size(int32_t total_tokens, int32_t num_seqs, int32_t H, int32_t Hk, int32_t dk,
+                                        int32_t dv, kda_dtype dtype) {
+    if (check_sizes(num_seqs, total_tokens, H, Hk, dk, dv, dtype, 0) != KDA_OK) return 0;
+    return fwd_layout(choose_windows(total_tokens, H), H, dk, dv).total;
+}
+
+int kda_lin_chunk_fwd(const void *q, const void *k, const void *v, const void *g, void *out, const int32_t *cu_seqlens,
+                      const int32_t *cu_seqlens_host, int32_t num_seqs, int32_t total_tokens, int32_t H, int32_t Hk,
+                      int32_t dk, int32_t dv, kda_dtype dtype, float scale, int32_t flags, const float *initial_state,
+                      float *final_state, void *workspace, size_t workspace_bytes, kda_stream_t stream) {
+    cudaStream_t st = (cudaStream_t)stream;
+    int rc = check_sizes(num_seqs, total_tokens, H, Hk, dk, dv, dtype, flags);
+    if (rc != KDA_OK) return rc;
+    if (num_seqs == 0) return total_tokens == 0 ? KDA_OK : KDA_ERR_INVALID_ARG;
+    if (total_tokens > 0 && (!q || !k || !v || !g || !out)) return KDA_ERR_INVALID_ARG;
+    const bool bf16 = dtype == KDA_DTYPE_BF16;
+    const void *a16[] = {q, k, v, out, initial_state, final_state, workspace};
+    rc = check_packed(cu_seqlens, cu_seqlens_host, num_seqs, total_tokens, g, bf16 ? 2 : 4, a16, 7);
+    if (rc != KDA_OK) return rc;
+    const bool in_place = initial_state && initial_state == final_state;
+    if (!in_place && overlap(initial_state, final_state, (size_t)num_seqs * H * dk * dv * sizeof(float)))
+        return KDA_ERR_INVALID_ARG;
+    const Windows wd = choose_windows(total_tokens, H);
+    const FwdLayout L = fwd_layout(wd, H, dk, dv);
+    if (!workspace || workspace_bytes < L.total) return KDA_ERR_WORKSPACE;
+    char *ws = (char *)workspace;
+
+    Params p{};
+    p.rd = q; p.wr = k; p.val = v; p.g = g; p.out = out;
+    p.rd_div = p.wr_div = H / Hk;
+    p.val_div = p.ext_div = 1;
+    p.rd_scale = scale;
+    p.wr_scale = 1.f;
+    p.g_per_head = flags & KDA_LIN_DECAY_PER_HEAD;
+    p.cu = cu_seqlens;
+    p.num_seqs = num_seqs; p.T = total_tokens; p.H = H; p.W = wd.W; p.win = wd.win;
+    p.init = initial_state;
+    p.final_state = final_state;
+    p.gamma = (float *)(ws + L.gamma);
+    p.win_state = (float *)(ws + L.z);
+    p.start_copy = in_place && wd.W > 1 ? (float *)(ws + L.start) : nullptr;
+    if (wd.W > 1) {
+        if (!ok(kda::lin::launch_rec(p, kda::lin::kSum, bf16, dk, dv, st))) return KDA_ERR_CUDA;
+        if (!ok(kda::lin::launch_scan(p.win_state, p.gamma, wd.W, H, dk * dv, false, st))) return KDA_ERR_CUDA;
+    }
+    return ok(kda::lin::launch_rec(p, kda::lin::kFwd, bf16, dk, dv, st)) ? KDA_OK : KDA_ERR_CUDA;
+}
+
+int kda_lin_decode_step(const void *q, const void *k, const void *v, const void *g, void *out, float *state,
+                        int32_t num_seqs, int32_t H, int32_t Hk, int32_t dk, int32_t dv, kda_dtype dtype, float scale,
+                        int32_t flags, kda_stream_t stream) {
+    const int rc = check_sizes(num_seqs, 0, H, Hk, dk, dv, dtype, flags);
+    if (rc != KDA_OK) return rc;
+    if (num_seqs == 0) return KDA_OK;
+    if (!q || !k || !v || !g || !out || !state) return KDA_ERR_INVALID_ARG;
+    const bool bf16 = dtype == KDA_DTYPE_BF16;
+    const void *a16[] = {q, k, v, out, state};
+    for (const void *p : a16)
+        if (!is_aligned(p, 16)) return KDA_ERR_ALIGNMENT;
+    if (!is_aligned(g, bf16 ? 2 : 4)) return KDA_ERR_ALIGNMENT;
+    const long nh = (long)num_seqs * H;
+    if (nh > 0x7fffffffL) return KDA_ERR_UNSUPPORTED;
+    return ok(kda::lin::launch_decode(bf16, dk, dv, q, k, v, g, out, state, nh, H, H / Hk,
+                                      flags & KDA_LIN_DECAY_PER_HEAD, scale, sm_count(), (cudaStream_t)stream))
+               ? KDA_OK
+               : KDA_ERR_CUDA;
+}
+
+size_t kda_lin_bwd_workspace_size(int32_t total_tokens, int32_t num_seqs, int32_t H, int32_t Hk, int32_t dk,
+                                  int32_t dv) {
+    if (check_sizes(num_seqs, total_tokens, H, Hk, dk, dv, KDA_DTYPE_F32, 0) != KDA_OK) return 0;
+    return bwd_layout(choose_windows(total_tokens, H), total_tokens, num_seqs, H, Hk, dk, dv).total;
+}
+
+int kda_lin_bwd(const void *q, const void *k, const void *v, const void *g, const void *dy, const int32_t *cu_seqlens,
+                const int32_t *cu_seqlens_host, int32_t num_seqs, int32_t total_tokens, int32_t H, int32_t Hk,
+                int32_t dk, int32_t dv, kda_dtype dtype, float scale, int32_t flags, const float *initial_state,
+                const float *d_final_state, void *dq, void *dk_out, void *dv_out, void *dg, float *d_initial_state,
+                void *workspace, size_t workspace_bytes, kda_stream_t stream) {
+    using namespace kda::lin;
+    cudaStream_t st = (cudaStream_t)stream;
+    int rc = check_sizes(num_seqs, total_tokens, H, Hk, dk, dv, dtype, flags);
+    if (rc != KDA_OK) return rc;
+    if (num_seqs == 0) return total_tokens == 0 ? KDA_OK : KDA_ERR_INVALID_ARG;
+    if (total_tokens > 0 && (!q || !k || !v || !g || !dy || !dq || !dk_out || !dv_out || !dg)) return KDA_ERR_INVALID_ARG;
+    const bool bf16 = dtype == KDA_DTYPE_BF16;
+    const size_t esz = bf16 ? 2 : 4;
+    const void *a16[] = {q, k, v, dy, initial_state, d_final_state, dq, dk_out, dv_out, d_initial_state, workspace};
+    rc = check_packed(cu_seqlens, cu_seqlens_host, num_seqs, total_tokens, g, esz, a16, 11);
+    if (rc != KDA_OK) return rc;
+    if (!is_aligned(dg, esz)) return KDA_ERR_ALIGNMENT;
+    const size_t state_bytes = (size_t)num_seqs * H * dk * dv * sizeof(float);
+    if (overlap(initial_state, d_initial_state, state_bytes) || overlap(d_final_state, d_initial_state, state_bytes))
+        return KDA_ERR_INVALID_ARG;
+    const Windows wd = choose_windows(total_tokens, H);
+    const BwdLayout L = bwd_layout(wd, total_tokens, num_seqs, H, Hk, dk, dv);
+    if (!workspace || workspace_bytes < L.total) return KDA_ERR_WORKSPACE;
+    char *ws = (char *)workspace;
+    const int rep = H / Hk, per_head = flags & KDA_LIN_DECAY_PER_HEAD;
+
+    Params c{};
+    c.g = g;
+    c.g_per_head = per_head;
+    c.cu = cu_seqlens;
+    c.num_seqs = num_seqs; c.T = total_tokens; c.H = H; c.W = wd.W; c.win = wd.win;
+    c.xdot = (float *)(ws + L.xdot);
+    c.ckpt = (float *)(ws + L.ckpt);
+    c.dg = per_head ? (void *)(ws + L.dgt) : dg;
+    c.zero_first_dg = initial_state == nullptr;
+    c.out_f32 = rep > 1;
+
+    // dq: read dy, write v, value k; state [dv][dk]
+    Params a = c;
+    a.rd = dy; a.wr = v; a.val = k; a.ext = q;
+    a.rd_div = a.wr_div = 1;
+    a.val_div = a.ext_div = rep;
+    a.rd_scale = scale;
+    a.wr_scale = 1.f;
+    a.out = rep > 1 ? (void *)(ws + L.dq) : dq;
+    a.init = initial_state;
+    a.init_t = 1;
+    a.win_state = (float *)(ws + L.zf);
+    a.gamma = (float *)(ws + L.gamma_f);
+    // dk, reversed: read v, write dy, value q; state [dv][dk]
+    Params b = c;
+    b.rd = v; b.wr = dy; b.val = q; b.ext = k;
+    b.rd_div = b.wr_div = 1;
+    b.val_div = b.ext_div = rep;
+    b.rd_scale = 1.f;
+    b.wr_scale = scale;
+    b.out = rep > 1 ? (void *)(ws + L.dk) : dk_out;
+    b.init = d_final_state;
+    b.init_t = 1;
+    b.win_state = (float *)(ws + L.zr);
+    b.gamma = (float *)(ws + L.gamma_r);
+    // dv, reversed: read k, write q, value dy; state [dk][dv]
+    Params d = c;
+    d.rd = k; d.wr = q; d.val = dy;
+    d.rd_div = d.wr_div = rep;
+    d.val_div = d.ext_div = 1;
+    d.rd_scale = 1.f;
+    d.wr_scale = scale;
+    d.out = dv_out;
+    d.out_f32 = 0;
+    d.init = d_final_state;
+    d.final_state = d_initial_state;
+    d.win_state = b.win_state;
+    d.win_t = 1;
+    d.gamma = b.gamma;
+
+    if (wd.W > 1) {
+        if (!ok(launch_rec(a, kSum, bf16, dv, dk, st)) || !ok(launch_rec(b, kSumR, bf16, dv, dk, st)) ||
+            !ok(launch_scan(a.win_state, a.gamma, wd.W, H, dk * dv, false, st)) ||
+            !ok(launch_scan(b.win_state, b.gamma, wd.W, H, dk * dv, true, st)))
+            return KDA_ERR_CUDA;
+    }
+    if (!ok(launch_rec(a, kDq, bf16, dv, dk, st)) || !ok(launch_rec(b, kDk, bf16, dv, dk, st)) ||
+        !ok(launch_rec(d, kDv, bf16, dk, dv, st)))
+        return KDA_ERR_CUDA;
+    if (total_tokens == 0) {
+        if (per_head && dg && !ok(cudaMemsetAsync(dg, 0, (size_t)H * esz, st))) return KDA_ERR_CUDA;
+        return KDA_OK;
+    }
+    if (rep > 1) {
+        const long n4 = (long)total_tokens * Hk * dk / 4;
+        const unsigned blocks = (unsigned)std::min<long>((n4 + 255) / 256, 8L * 148);
+        for (int i = 0; i < 2; ++i) {
+            const float4 *in = (const float4 *)(ws + (i ? L.dk : L.dq));
+            void *out = i ? dk_out : dq;
+            if (bf16) head_sum_kernel<<<blocks, 256, 0, st>>>(in, (__nv_bfloat16 *)out, n4, rep, dk / 4);
+            else head_sum_kernel<<<blocks, 256, 0, st>>>(in, (float *)out, n4, rep, dk / 4);
+        }
+    }
+    if (per_head) {
+        const int parts = (total_tokens + kSumRows - 1) / kSumRows, hb = (H + 31) / 32;
+        float *part = (float *)(ws + L.part);
+        token_sum_kernel<<<dim3(parts, hb), 256, 0, st>>>((const float *)c.dg, part, total_tokens, H);
+        if (bf16) part_sum_kernel<<<hb, 256, 0, st>>>(part, (__nv_bfloat16 *)dg, parts, H);
+        else part_sum_kernel<<<hb, 256, 0, st>>>(part, (float *)dg, parts, H);
+    }
+    return ok(cudaGetLastError()) ? KDA_OK : KDA_ERR_CUDA;
+}
+
+}  // extern "C"

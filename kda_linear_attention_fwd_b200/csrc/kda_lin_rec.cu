@@ -1,0 +1,475 @@
+// Linear attention with one decay per head, token by token in fp32: the
+// forward, its window summaries and the gradient's three passes.
+//
+// The recurrence itself (kda_lin.cuh) costs two FMAs per state element and
+// token, so fp32 inputs, which the tensor cores could only take split into
+// several products, run it directly: the whole state of one head sits in the
+// registers of one CTA of 128 threads and every product is a plain fp32 FMA
+// (pairs, fma.rn.f32x2).  Two things keep it at two FMAs:
+//   * the decay is one number, so it is kept outside the state: the registers
+//     hold S / e^G with G the log-decay summed since the last renormalisation;
+//     a write adds k (v e^-G)^T and a read is scaled by e^G.  The state is
+//     renormalised (one multiply per element) every 16 tokens, and earlier
+//     when G falls below -20, so e^-G stays in range and G is always a short
+//     sum (its rounding is what limits the decay's accuracy);
+//   * a warp's 32 lanes are RG row groups x CGW column groups, each thread
+//     holding RT rows x 4 columns, so the vectors come from shared memory as
+//     broadcast 16-byte reads (17 reads for 128 paired FMAs at 128 x 128) and
+//     o needs 3 shuffles per token.
+// Tokens arrive 16 at a time by cp.async, one block ahead.
+//
+// The gradient in the same form (B_t = dL/dS_t, L = sum o . do + <dS_T, S_T>):
+//   B_t = exp(g_{t+1}) B_{t+1} + scale q_t do_t^T
+//   dq_t = scale S_t do_t,  dk_t = B_t v_t,  dv_t = B_t^T k_t,
+//   dS_0 = exp(g_1) B_1,    dg_t = <exp(g_t) S_{t-1}, B_t>.
+// dq is this recurrence with the roles (read do, write v, value k), dk the
+// reversed one with (read v, write do, value q), dv with (read k, write q,
+// value do), so one kernel makes all three.  dg uses
+//   <exp(g_t) S_{t-1}, B_t> = <S_e, exp(g_{e+1}) B_{e+1}>
+//                             + sum_{t<=s<=e} (q_s . dq_s - k_s . dk_s),
+// e being the last token of t's 64-token chunk: the dq pass leaves S_e of
+// every chunk in the workspace and the dk pass takes the product with its own
+// state there, so the sums that cancel are at most 64 tokens long.
+#include "kda_common.cuh"
+#include "kda_lin.cuh"
+#include "kda_sm100.cuh"
+
+namespace kda {
+namespace lin {
+
+using namespace sm100;
+
+constexpr int kThreads = 128;
+constexpr int kSub = 16;    // tokens per staged block
+constexpr int kCkpt = 64;   // tokens per chunk of the gradient's dg sums
+
+enum Mode { FWD, SUM, SUMR, DQ, DK, DV };  // SUMR: the reversed summary
+
+template <int M> struct ModeOf {
+    static constexpr bool rev = M == SUMR || M == DK || M == DV;
+    static constexpr bool sum = M == SUM || M == SUMR;
+    static constexpr bool out = !sum;
+    static constexpr bool xd = M == DQ || M == DK;
+};
+
+template <typename T, int DA, int DB, int M>
+struct Stage {  // one block of 16 tokens in the input type
+    T wr[kSub][DA];
+    T val[kSub][DB];
+    T rd[ModeOf<M>::out ? kSub : 1][ModeOf<M>::out ? DA : 8];
+    T ext[ModeOf<M>::xd ? kSub : 1][ModeOf<M>::xd ? DB : 8];
+};
+template <typename T, int DA, int DB, int M>
+struct Smem {
+    alignas(16) Stage<T, DA, DB, M> st[2];
+    float g[2][kSub];
+    float xp[kCkpt][4];  // per token and warp: partial out . ext
+    float xq[kCkpt];
+    float fdot[4];
+};
+
+KDA_DEVICE float4 ld4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
+KDA_DEVICE float4 ld4(const bf16 *p) {
+    const uint2 u = *reinterpret_cast<const uint2 *>(p);
+    const float2 a = unpack_bf16(u.x), b = unpack_bf16(u.y);
+    return make_float4(a.x, a.y, b.x, b.y);
+}
+
+template <typename T, int DA, int DB, int M>
+__global__ void __launch_bounds__(kThreads, 3) rec_kernel(const Params p) {
+    using MO = ModeOf<M>;
+    constexpr int CGW = DB / 16;        // column groups (of 4) per warp
+    constexpr int RG = 32 / CGW;        // row groups
+    constexpr int RT = DA / RG;         // rows per thread
+    constexpr int NQ = RT / 4;          // in quads: quad i is rows 4 (i RG + rg) .. + 3
+    static_assert(NQ >= 1 && CGW * 4 * 4 == DB, "tile shape");
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    Smem<T, DA, DB, M> &sm = *reinterpret_cast<Smem<T, DA, DB, M> *>(smem_raw);
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rg = lane / CGW;
+    const int col0 = (warp * CGW + lane % CGW) * 4;
+    const int h = blockIdx.x, w = blockIdx.y;
+    const int H = p.H, N = p.num_seqs;
+    const int t0 = w * p.win, t1 = min(p.T, t0 + p.win);
+    const int hr = MO::out ? h / p.rd_div : 0, Hr = MO::out ? H / p.rd_div : 1;
+    const int hw = h / p.wr_div, Hw = H / p.wr_div;
+    const int hv = h / p.val_div, Hv = H / p.val_div;
+    const int he = MO::xd ? h / p.ext_div : 0, He = MO::xd ? H / p.ext_div : 1;
+    const T *rd = (const T *)p.rd, *wr = (const T *)p.wr, *val = (const T *)p.val, *ext = (const T *)p.ext;
+
+    float2 s[NQ][2][4];  // quad, row pair, column: S / e^G
+
+    auto row_of = [&](int i, int r) { return 4 * (i * RG + rg) + r; };
+    // state element access of a [DA][DB] matrix, or its transpose
+    auto load_state = [&](const float *base, bool transposed) {
+#pragma unroll
+        for (int i = 0; i < NQ; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                float x[4] = {0.f, 0.f, 0.f, 0.f};
+                if (base && !transposed) {
+                    const float4 v4 = *reinterpret_cast<const float4 *>(base + (size_t)row_of(i, r) * DB + col0);
+                    x[0] = v4.x; x[1] = v4.y; x[2] = v4.z; x[3] = v4.w;
+                } else if (base) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) x[c] = base[(size_t)(col0 + c) * DA + row_of(i, r)];
+                }
+#pragma unroll
+                for (int c = 0; c < 4; ++c) (r & 1 ? s[i][r >> 1][c].y : s[i][r >> 1][c].x) = x[c];
+            }
+    };
+    auto store_state = [&](float *base, bool transposed, float f) {
+#pragma unroll
+        for (int i = 0; i < NQ; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                float x[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) x[c] = f * (r & 1 ? s[i][r >> 1][c].y : s[i][r >> 1][c].x);
+                if (!transposed) {
+                    *reinterpret_cast<float4 *>(base + (size_t)row_of(i, r) * DB + col0) = make_float4(x[0], x[1], x[2], x[3]);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) base[(size_t)(col0 + c) * DA + row_of(i, r)] = x[c];
+                }
+            }
+    };
+    auto scale_state = [&](float f) {
+        const float2 f2 = make_float2(f, f);
+#pragma unroll
+        for (int i = 0; i < NQ; ++i)
+#pragma unroll
+            for (int pr = 0; pr < 2; ++pr)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) s[i][pr][c] = f2mul(s[i][pr][c], f2);
+    };
+    auto load_g = [&](int t) -> float {
+        const size_t at = p.g_per_head ? (size_t)h : (size_t)t * H + h;
+        return fmaxf(ld((const T *)p.g + at), kMinG);
+    };
+
+    // tokens [a, b) of sequence n, whose true range is [qa, qb)
+    float gamma = 1.f;
+    auto run_segment = [&](int n, int a, int b, int qa, int qb) {
+        const int len = b - a;
+        const int nsub = (len + kSub - 1) / kSub;
+        auto stage = [&](int sb, int buf) {
+            const int base = a + sb * kSub, rows = min(kSub, b - base);
+            Stage<T, DA, DB, M> &S = sm.st[buf];
+            auto copy = [&](T *dst, const T *src, int D, int Hx, int hx) {
+                const int per = D * (int)sizeof(T) / 16;
+                for (int x = tid; x < rows * per; x += kThreads) {
+                    const int r = x / per, c = x % per;
+                    cp_async16((char *)(dst + r * D) + c * 16,
+                               (const char *)(src + ((size_t)(base + r) * Hx + hx) * D) + c * 16, true);
+                }
+            };
+            copy(&S.wr[0][0], wr, DA, Hw, hw);
+            copy(&S.val[0][0], val, DB, Hv, hv);
+            if constexpr (MO::out) copy(&S.rd[0][0], rd, DA, Hr, hr);
+            if constexpr (MO::xd) copy(&S.ext[0][0], ext, DB, He, he);
+            if (tid < rows) {
+                const int t = base + tid;
+                if (MO::rev)
+                    sm.g[buf][tid] = t + 1 < qb ? load_g(t + 1) : 0.f;
+                else
+                    sm.g[buf][tid] = load_g(t);
+            }
+            cp_async_commit();
+        };
+        if (nsub > 0) stage(MO::rev ? nsub - 1 : 0, 0);
+        for (int it = 0; it < nsub; ++it) {
+            const int sb = MO::rev ? nsub - 1 - it : it, buf = it & 1;
+            if (it + 1 < nsub) {
+                stage(MO::rev ? sb - 1 : sb + 1, buf ^ 1);
+                cp_async_wait<1>();
+            } else {
+                cp_async_wait<0>();
+            }
+            __syncthreads();
+            const Stage<T, DA, DB, M> &S = sm.st[buf];
+            const int base = a + sb * kSub, rows = min(kSub, b - base);
+            const int chunk = sb / (kCkpt / kSub);
+            const int in_chunk = (sb % (kCkpt / kSub)) * kSub;
+            const int chunk_len = min(kCkpt, len - chunk * kCkpt);
+            const size_t slot = (size_t)((a + chunk * kCkpt) / kCkpt + n) * H + h;
+            if constexpr (M == DK) {
+                if (in_chunk + rows == chunk_len) {  // the chunk's last token comes first
+                    const float *ck = p.ckpt + slot * (DA * DB);
+                    float d = 0.f;
+#pragma unroll
+                    for (int i = 0; i < NQ; ++i)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const float4 v4 = *reinterpret_cast<const float4 *>(ck + (size_t)row_of(i, r) * DB + col0);
+                            const float x[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) d += x[c] * (r & 1 ? s[i][r >> 1][c].y : s[i][r >> 1][c].x);
+                        }
+                    d = warp_sum(d) * __expf(sm.g[buf][rows - 1]);
+                    if (lane == 0) sm.fdot[warp] = d;
+                    if (tid < chunk_len) sm.xq[tid] = p.xdot[(size_t)(a + chunk * kCkpt + tid) * H + h];
+                }
+            }
+            float G = 0.f;
+#pragma unroll 1
+            for (int jj = 0; jj < rows; ++jj) {
+                const int j = MO::rev ? rows - 1 - jj : jj;
+                G += sm.g[buf][j];
+                if (G < -20.f) {  // the same branch in every thread
+                    const float f = expf(G);
+                    scale_state(f);
+                    gamma *= f;
+                    G = 0.f;
+                }
+                const float wf = __expf(-G) * p.wr_scale;
+                const float4 v4 = ld4(&S.val[j][col0]);
+                const float vs[4] = {v4.x * wf, v4.y * wf, v4.z * wf, v4.w * wf};
+                float2 o[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) o[c] = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int i = 0; i < NQ; ++i) {
+                    const float4 k4 = ld4(&S.wr[j][row_of(i, 0)]);
+                    const float2 k2[2] = {make_float2(k4.x, k4.y), make_float2(k4.z, k4.w)};
+#pragma unroll
+                    for (int pr = 0; pr < 2; ++pr)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) s[i][pr][c] = f2fma(k2[pr], make_float2(vs[c], vs[c]), s[i][pr][c]);
+                    if constexpr (MO::out) {
+                        const float4 q4 = ld4(&S.rd[j][row_of(i, 0)]);
+                        const float2 q2[2] = {make_float2(q4.x, q4.y), make_float2(q4.z, q4.w)};
+#pragma unroll
+                        for (int pr = 0; pr < 2; ++pr)
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) o[c] = f2fma(q2[pr], s[i][pr][c], o[c]);
+                    }
+                }
+                if constexpr (MO::out) {
+                    // sum over the row groups, one column left per lane
+                    float x[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) x[c] = o[c].x + o[c].y;
+                    const bool hi = lane & 16, mid = lane & 8;
+                    float y0 = (hi ? x[2] : x[0]) + __shfl_xor_sync(0xffffffffu, hi ? x[0] : x[2], 16);
+                    float y1 = (hi ? x[3] : x[1]) + __shfl_xor_sync(0xffffffffu, hi ? x[1] : x[3], 16);
+                    float z = (mid ? y1 : y0) + __shfl_xor_sync(0xffffffffu, mid ? y0 : y1, 8);
+                    bool keep = true;
+                    if constexpr (RG == 8) {
+                        z += __shfl_xor_sync(0xffffffffu, z, 4);
+                        keep = !(lane & 4);
+                    }
+                    z *= __expf(G) * p.rd_scale;
+                    const int col = col0 + (hi ? 2 : 0) + (mid ? 1 : 0);
+                    const size_t at = ((size_t)(base + j) * H + h) * DB + col;
+                    if (keep) {
+                        if (p.out_f32) ((float *)p.out)[at] = z;
+                        else st((T *)p.out + at, z);
+                    }
+                    if constexpr (MO::xd) {
+                        const float x1 = warp_sum(keep ? z * ld(&S.ext[j][col]) : 0.f);
+                        if (lane == 0) sm.xp[in_chunk + j][warp] = x1;
+                    }
+                }
+            }
+            if (G != 0.f) {  // renormalise
+                const float f = expf(G);
+                scale_state(f);
+                gamma *= f;
+            }
+            if constexpr (M == DQ) {
+                if (in_chunk + rows == chunk_len) store_state(p.ckpt + slot * (DA * DB), false, 1.f);
+            }
+            __syncthreads();
+            if constexpr (M == DQ) {
+                if (tid < rows) {
+                    const float *x = sm.xp[in_chunk + tid];
+                    p.xdot[(size_t)(base + tid) * H + h] = (x[0] + x[1]) + (x[2] + x[3]);
+                }
+            }
+            if constexpr (M == DK) {
+                if (in_chunk == 0 && warp == 0) {  // the chunk is done: suffix sums of its 64 tokens
+                    const float F = (sm.fdot[0] + sm.fdot[1]) + (sm.fdot[2] + sm.fdot[3]);
+                    float d[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int j = 2 * lane + e;
+                        const float *x = sm.xp[j];
+                        d[e] = j < chunk_len ? sm.xq[j] - ((x[0] + x[1]) + (x[2] + x[3])) : 0.f;
+                    }
+                    float tot = d[0] + d[1];  // inclusive suffix scan over the lanes
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const float y = __shfl_down_sync(0xffffffffu, tot, o);
+                        if (lane + o < 32) tot += y;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int j = 2 * lane + e, t = a + chunk * kCkpt + j;
+                        float dg = F + (e ? tot - d[0] : tot);
+                        if (p.zero_first_dg && t == qa) dg = 0.f;
+                        if (j < chunk_len) {
+                            if (p.g_per_head) ((float *)p.dg)[(size_t)t * H + h] = dg;
+                            else st((T *)p.dg + (size_t)t * H + h, dg);
+                        }
+                    }
+                }
+            }
+        }
+        __syncthreads();
+    };
+
+    auto seq_state = [&](int n) -> size_t { return ((size_t)n * H + h) * (DA * DB); };
+    const size_t win_at = ((size_t)w * H + h) * (DA * DB);
+
+    // first sequence that starts at or behind t0
+    int lo = 0, hi_ = N;
+    while (lo < hi_) {
+        const int mid = (lo + hi_) >> 1;
+        if (p.cu[mid] < t0) lo = mid + 1;
+        else hi_ = mid;
+    }
+    // sequence n's tokens inside the window
+    auto seg_a = [&](int n) { return min(max(p.cu[n], t0), t1); };
+    auto seg_b = [&](int n, int a) { return max(a, min(p.cu[n + 1], t1)); };
+
+    if constexpr (MO::sum) {
+        // the sequence that crosses the window's outgoing edge, if any
+        int n = -1;
+        if (M == SUM) {
+            if (t1 < p.T) {  // the last sequence that starts before t1
+                int l = lo, u = N;
+                while (l < u) {
+                    const int mid = (l + u) >> 1;
+                    if (p.cu[mid] < t1) l = mid + 1;
+                    else u = mid;
+                }
+                n = l - 1;
+                if (n >= 0 && p.cu[n + 1] <= t1) n = -1;
+            }
+        } else {
+            n = t0 > 0 ? lo - 1 : -1;
+            if (n >= 0 && p.cu[n + 1] <= t0) n = -1;
+        }
+        if (n < 0) {
+            if (tid == 0) p.gamma[(size_t)w * H + h] = kNoCarry;
+            return;
+        }
+        const int a = seg_a(n), b = seg_b(n, a);
+        const bool whole = M == SUM ? p.cu[n] >= t0 : p.cu[n + 1] <= t1;  // starts (ends) in this window
+        load_state(whole && p.init ? p.init + seq_state(n) : nullptr, p.init_t);
+        if (whole && p.start_copy) store_state(p.start_copy + win_at, false, 1.f);
+        run_segment(n, a, b, p.cu[n], min(p.cu[n + 1], p.T));
+        store_state(p.win_state + win_at, false, 1.f);
+        if (tid == 0) p.gamma[(size_t)w * H + h] = whole ? 0.f : gamma;
+    } else {
+        // the sequences of this window: the one that continues into it, then
+        // those that start in it (the last window also takes the empty ones
+        // at the very end)
+        const int first = lo > 0 && lo <= N && p.cu[lo] > t0 ? lo - 1 : lo;
+        int end = lo;
+        if (w == p.W - 1) {
+            end = N;
+        } else {
+            int u = N;
+            while (end < u) {
+                const int mid = (end + u) >> 1;
+                if (p.cu[mid] < t1) end = mid + 1;
+                else u = mid;
+            }
+        }
+        for (int i = first; i < end; ++i) {
+            const int n = MO::rev ? end - 1 - (i - first) : i;
+            const int a = seg_a(n), b = seg_b(n, a);
+            const bool from_win = MO::rev ? p.cu[n + 1] > t1 : n < lo;
+            const bool ends = MO::rev ? n >= lo : p.cu[n + 1] <= t1;
+            if (from_win)
+                load_state(p.win_state + win_at, p.win_t);
+            else if (p.start_copy && p.cu[n + 1] > t1)  // its final state may replace its initial one by now
+                load_state(p.start_copy + win_at, false);
+            else
+                load_state(p.init ? p.init + seq_state(n) : nullptr, p.init_t);
+            run_segment(n, a, b, p.cu[n], min(p.cu[n + 1], p.T));
+            if (ends && p.final_state) {
+                const float f = MO::rev && b > a ? expf(load_g(a)) : 1.f;
+                store_state(p.final_state + seq_state(n), p.init_t, f);
+            }
+        }
+    }
+}
+
+// The states entering the windows, in place of the windows' Z:
+// S_in(w + 1) = gamma_w S_in(w) + Z_w (reversed: S_in(w - 1)).  One thread per
+// four state elements, the next kAhead windows' Z in flight.
+constexpr int kAhead = 8;
+__global__ void __launch_bounds__(128) scan_kernel(float4 *z, const float *gamma, int W, int H, int quads, int rev) {
+    const int e = blockIdx.x * 128 + threadIdx.x, h = blockIdx.y;
+    if (e >= quads) return;
+    float4 carry = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int w0 = 0; w0 < W; w0 += kAhead) {
+        float4 zz[kAhead];
+        float gm[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            if (w0 + i < W) {
+                const int w = rev ? W - 1 - (w0 + i) : w0 + i;
+                gm[i] = gamma[(size_t)w * H + h];
+                zz[i] = z[((size_t)w * H + h) * quads + e];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            if (w0 + i < W) {
+                const int w = rev ? W - 1 - (w0 + i) : w0 + i;
+                z[((size_t)w * H + h) * quads + e] = carry;
+                if (gm[i] < 0.f) {
+                    carry = make_float4(0.f, 0.f, 0.f, 0.f);
+                } else {
+                    carry.x = fmaf(gm[i], carry.x, zz[i].x);
+                    carry.y = fmaf(gm[i], carry.y, zz[i].y);
+                    carry.z = fmaf(gm[i], carry.z, zz[i].z);
+                    carry.w = fmaf(gm[i], carry.w, zz[i].w);
+                }
+            }
+        }
+    }
+}
+
+cudaError_t launch_scan(float *z, const float *gamma, int W, int H, int elems, bool rev, cudaStream_t st) {
+    const int quads = elems / 4;
+    scan_kernel<<<dim3((quads + 127) / 128, H), 128, 0, st>>>((float4 *)z, gamma, W, H, quads, rev);
+    return cudaGetLastError();
+}
+
+template <typename T, int DA, int DB, int M>
+static cudaError_t launch_rec_t(const Params &p, cudaStream_t st) {
+    constexpr int bytes = (int)sizeof(Smem<T, DA, DB, M>);
+    cudaError_t e = cudaFuncSetAttribute(rec_kernel<T, DA, DB, M>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    rec_kernel<T, DA, DB, M><<<dim3(p.H, p.W), kThreads, bytes, st>>>(p);
+    return cudaGetLastError();
+}
+template <typename T, int M>
+static cudaError_t launch_rec_d(const Params &p, int da, int db, cudaStream_t st) {
+    if (da == 128) return db == 128 ? launch_rec_t<T, 128, 128, M>(p, st) : launch_rec_t<T, 128, 64, M>(p, st);
+    return db == 128 ? launch_rec_t<T, 64, 128, M>(p, st) : launch_rec_t<T, 64, 64, M>(p, st);
+}
+template <int M>
+static cudaError_t launch_rec_m(const Params &p, bool is_bf16, int da, int db, cudaStream_t st) {
+    return is_bf16 ? launch_rec_d<bf16, M>(p, da, db, st) : launch_rec_d<float, M>(p, da, db, st);
+}
+// mode: 0 forward, 1 summary, 2 reversed summary, 3 dq, 4 dk (and dg), 5 dv (and dS0)
+cudaError_t launch_rec(const Params &p, int mode, bool is_bf16, int da, int db, cudaStream_t st) {
+    switch (mode) {
+        case FWD: return launch_rec_m<FWD>(p, is_bf16, da, db, st);
+        case SUM: return launch_rec_m<SUM>(p, is_bf16, da, db, st);
+        case SUMR: return launch_rec_m<SUMR>(p, is_bf16, da, db, st);
+        case DQ: return launch_rec_m<DQ>(p, is_bf16, da, db, st);
+        case DK: return launch_rec_m<DK>(p, is_bf16, da, db, st);
+        default: return launch_rec_m<DV>(p, is_bf16, da, db, st);
+    }
+}
+
+}  // namespace lin
+}  // namespace kda

@@ -1,0 +1,537 @@
+// The norms before and after a block, fused with the block's gate and the
+// scaled residual, and their gradient (kda_block_norm, kda_block_norm_bwd):
+//
+//   yn = y * iy,  iy = rsqrt(mean(y^2) + eps)        (post norm; else yn = y)
+//   u  = act(gate) * yn * w_post
+//   r  = x + c u                                     (no residual: r = c u)
+//   h  = r * ir * w_pre,  ir = rsqrt(mean(r^2) + eps)  (pre norm of the next block)
+//
+// and for given dr, dh, with m = dh w_pre, rn = r ir:
+//   dR = dr + ir (m - rn mean(m rn)),   dx = dR,   du = c dR
+//   dgate = du yn w_post act'(gate),    dn = du act(gate) w_post
+//   dy = iy (dn - yn mean(dn yn))                    (no post norm: dy = dn)
+//   dw_post = sum_rows du act(gate) yn, dw_pre = sum_rows dh rn
+//
+// Everything is one pass over the rows: each input is read once into
+// registers in its own type, the row statistics are fp32, h is taken from the
+// unrounded r, and the outputs are rounded once.  The floor is that traffic.
+//
+// A row belongs to TPR threads (a power of two; up to 32 of them inside a
+// warp, more as whole warps), each holding NV vectors of VEC elements; a CTA
+// of 256 threads (or of TPR, when a row takes more) holds 256 / TPR rows.
+// VEC is 16 bytes when D, the strides and the addresses allow it and one
+// element otherwise.  The gradient runs a fixed number of CTAs over the rows
+// so that each thread keeps the sums of its columns of dw in registers; the
+// CTAs' partial sums are added in a second, small launch in a fixed order.
+#include <algorithm>
+#include <type_traits>
+
+#include "../../include/kda.h"
+#include "kda_args.h"
+#include "kda_common.cuh"
+
+namespace kda {
+namespace norm {
+
+constexpr int kThreads = 256;
+constexpr int kMaxD = 16384;
+
+struct Params {
+    const void *y, *gate, *x, *w_post, *w_pre;
+    long y_ld, gate_ld, x_ld;
+    void *out, *normed;
+    // gradient
+    const void *dr, *dh;
+    void *dy, *dgate, *dx;
+    float *part;      // [gridDim][2][D]
+    int want_post, want_pre;
+    long rows;
+    int D, tpr, flags;
+    float c, eps;
+};
+
+template <typename T, int VEC> struct Vec { T e[VEC]; };
+template <typename T, int VEC> struct alignas(16) Vec16 { T e[VEC]; };
+template <typename T, int VEC>
+using VecT = typename std::conditional<VEC == 1, Vec<T, 1>, Vec16<T, VEC>>::type;
+
+template <typename T, int VEC>
+KDA_DEVICE VecT<T, VEC> load_vec(const void *base, long at) {
+    return *reinterpret_cast<const VecT<T, VEC> *>((const T *)base + at);
+}
+template <typename T, int VEC>
+KDA_DEVICE void store_vec(void *base, long at, const float (&v)[VEC]) {
+    VecT<T, VEC> o;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) st(&o.e[e], v[e]);
+    *reinterpret_cast<VecT<T, VEC> *>((T *)base + at) = o;
+}
+
+// Sum of N values over the TPR threads of a row (every thread gets it).
+template <int N>
+KDA_DEVICE void row_sum(float (&v)[N], int tpr, float (*red)[N]) {
+    for (int o = min(tpr, 32) >> 1; o > 0; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+    if (tpr > 32) {
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        __syncthreads();  // earlier readers of red are done
+        if (lane == 0)
+#pragma unroll
+            for (int i = 0; i < N; ++i) red[warp][i] = v[i];
+        __syncthreads();
+        const int nw = tpr >> 5, first = warp / nw * nw;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            float a = 0.f;
+            for (int j = 0; j < nw; ++j) a += red[first + j][i];
+            v[i] = a;
+        }
+    }
+}
+
+KDA_DEVICE float act_of(float z, int flags) {
+    if (flags & (KDA_NORM_GATE_SIGMOID | KDA_NORM_GATE_SILU)) {
+        const float s = sigmoid_f(z);
+        return (flags & KDA_NORM_GATE_SILU) ? z * s : s;
+    }
+    return z;
+}
+KDA_DEVICE float act_slope(float z, int flags) {
+    if (flags & (KDA_NORM_GATE_SIGMOID | KDA_NORM_GATE_SILU)) {
+        const float s = sigmoid_f(z);
+        return (flags & KDA_NORM_GATE_SILU) ? s * (1.f + z * (1.f - s)) : s * (1.f - s);
+    }
+    return 1.f;
+}
+
+template <typename T, int VEC, int NV, int MT>
+__global__ void __launch_bounds__(MT) fwd_kernel(const Params p) {
+    __shared__ float red[32][1];
+    const int tpr = p.tpr, t = threadIdx.x & (tpr - 1);
+    const long row = (long)blockIdx.x * (blockDim.x / tpr) + threadIdx.x / tpr;
+    const bool live = row < p.rows;
+    const bool post = p.flags & KDA_NORM_POST, pre = p.flags & KDA_NORM_PRE;
+    const float inv_d = 1.f / p.D;
+    VecT<T, VEC> y[NV], z[NV], x[NV];
+    float u[NV][VEC];
+    float ss[1] = {0.f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * tpr + t) * VEC;
+        if (live && c < p.D) {
+            y[i] = load_vec<T, VEC>(p.y, row * p.y_ld + c);
+            if (p.gate) z[i] = load_vec<T, VEC>(p.gate, row * p.gate_ld + c);
+            if (p.x) x[i] = load_vec<T, VEC>(p.x, row * p.x_ld + c);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const bool in = live && (i * tpr + t) * VEC < p.D;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            u[i][e] = in ? ld(&y[i].e[e]) : 0.f;
+            ss[0] = fmaf(u[i][e], u[i][e], ss[0]);
+        }
+    }
+    float iy = 1.f;
+    if (post) {
+        row_sum(ss, tpr, red);
+        iy = rsqrtf(fmaf(ss[0], inv_d, p.eps));
+    }
+    float rr[1] = {0.f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * tpr + t) * VEC;
+        if (live && c < p.D) {
+            VecT<T, VEC> wv;
+            if (p.w_post) wv = load_vec<T, VEC>(p.w_post, c);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                float a = u[i][e] * iy;
+                if (p.w_post) a *= ld(&wv.e[e]);
+                if (p.gate) a *= act_of(ld(&z[i].e[e]), p.flags);
+                a = p.x ? fmaf(a, p.c, ld(&x[i].e[e])) : a * p.c;
+                u[i][e] = a;
+                rr[0] = fmaf(a, a, rr[0]);
+            }
+            store_vec<T, VEC>(p.out, row * p.D + c, u[i]);
+        }
+    }
+    if (!pre) return;
+    row_sum(rr, tpr, red);
+    const float ir = rsqrtf(fmaf(rr[0], inv_d, p.eps));
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * tpr + t) * VEC;
+        if (live && c < p.D) {
+            VecT<T, VEC> wv;
+            if (p.w_pre) wv = load_vec<T, VEC>(p.w_pre, c);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) u[i][e] *= p.w_pre ? ir * ld(&wv.e[e]) : ir;
+            store_vec<T, VEC>(p.normed, row * p.D + c, u[i]);
+        }
+    }
+}
+
+template <typename T, int VEC, int NV, int MT>
+__global__ void __launch_bounds__(MT) bwd_kernel(const Params p) {
+    __shared__ float red[32][2];
+    __shared__ float red1[32][1];
+    extern __shared__ float colsum[];  // [2][D], when a CTA holds more than one row
+    const int tpr = p.tpr, t = threadIdx.x & (tpr - 1);
+    const int per = blockDim.x / tpr, sub = threadIdx.x / tpr;
+    const bool post = p.flags & KDA_NORM_POST, pre = p.flags & KDA_NORM_PRE;
+    const bool need_r = pre && p.dh;
+    const float inv_d = 1.f / p.D;
+    float gpost[NV][VEC], gpre[NV][VEC];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) gpost[i][e] = gpre[i][e] = 0.f;
+
+    for (long row0 = (long)blockIdx.x * per; row0 < p.rows; row0 += (long)gridDim.x * per) {
+        const long row = row0 + sub;
+        const bool live = row < p.rows;
+        VecT<T, VEC> y[NV], z[NV], x[NV], dr[NV], dh[NV];
+        float a1[1] = {0.f};
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * tpr + t) * VEC;
+            if (live && c < p.D) {
+                y[i] = load_vec<T, VEC>(p.y, row * p.y_ld + c);
+                if (p.gate) z[i] = load_vec<T, VEC>(p.gate, row * p.gate_ld + c);
+                if (p.x && need_r) x[i] = load_vec<T, VEC>(p.x, row * p.x_ld + c);
+                if (p.dr) dr[i] = load_vec<T, VEC>(p.dr, row * p.D + c);
+                if (need_r) dh[i] = load_vec<T, VEC>(p.dh, row * p.D + c);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (live && (i * tpr + t) * VEC < p.D)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    const float v = ld(&y[i].e[e]);
+                    a1[0] = fmaf(v, v, a1[0]);
+                }
+        float iy = 1.f;
+        if (post) {
+            row_sum(a1, tpr, red1);
+            iy = rsqrtf(fmaf(a1[0], inv_d, p.eps));
+        }
+        float ir = 0.f, mean_r = 0.f;
+        if (need_r) {
+            float s2[2] = {0.f, 0.f};  // sum r^2, sum dh w_pre r
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = (i * tpr + t) * VEC;
+                if (live && c < p.D) {
+                    VecT<T, VEC> wa, wb;
+                    if (p.w_post) wa = load_vec<T, VEC>(p.w_post, c);
+                    if (p.w_pre) wb = load_vec<T, VEC>(p.w_pre, c);
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) {
+                        float a = ld(&y[i].e[e]) * iy;
+                        if (p.w_post) a *= ld(&wa.e[e]);
+                        if (p.gate) a *= act_of(ld(&z[i].e[e]), p.flags);
+                        a = p.x ? fmaf(a, p.c, ld(&x[i].e[e])) : a * p.c;
+                        const float m = ld(&dh[i].e[e]) * (p.w_pre ? ld(&wb.e[e]) : 1.f);
+                        s2[0] = fmaf(a, a, s2[0]);
+                        s2[1] = fmaf(m, a, s2[1]);
+                    }
+                }
+            }
+            row_sum(s2, tpr, red);
+            ir = rsqrtf(fmaf(s2[0], inv_d, p.eps));
+            mean_r = s2[1] * ir * inv_d;
+        }
+        float dn[NV][VEC];
+        float a3[1] = {0.f};
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * tpr + t) * VEC;
+            if (live && c < p.D) {
+                VecT<T, VEC> wa, wb;
+                if (p.w_post) wa = load_vec<T, VEC>(p.w_post, c);
+                if (need_r && p.w_pre) wb = load_vec<T, VEC>(p.w_pre, c);
+                float dR[VEC], dz[VEC];
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    const float yn = ld(&y[i].e[e]) * iy;
+                    const float w = p.w_post ? ld(&wa.e[e]) : 1.f;
+                    const float zz = p.gate ? ld(&z[i].e[e]) : 1.f;
+                    const float act = p.gate ? act_of(zz, p.flags) : 1.f;
+                    float d = p.dr ? ld(&dr[i].e[e]) : 0.f;
+                    if (need_r) {
+                        const float u = yn * w * act;
+                        const float rn = (p.x ? fmaf(u, p.c, ld(&x[i].e[e])) : u * p.c) * ir;
+                        const float dhe = ld(&dh[i].e[e]);
+                        const float m = p.w_pre ? dhe * ld(&wb.e[e]) : dhe;
+                        d += ir * (m - rn * mean_r);
+                        gpre[i][e] = fmaf(dhe, rn, gpre[i][e]);
+                    }
+                    dR[e] = d;
+                    const float du = d * p.c;
+                    if (p.gate) dz[e] = du * yn * w * act_slope(zz, p.flags);
+                    const float da = du * act;
+                    gpost[i][e] = fmaf(da, yn, gpost[i][e]);
+                    dn[i][e] = da * w;
+                    a3[0] = fmaf(dn[i][e], yn, a3[0]);
+                }
+                if (p.dx) store_vec<T, VEC>(p.dx, row * p.D + c, dR);
+                if (p.dgate) store_vec<T, VEC>(p.dgate, row * p.D + c, dz);
+            }
+        }
+        float mean_y = 0.f;
+        if (post) {
+            row_sum(a3, tpr, red1);
+            mean_y = a3[0] * inv_d;
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * tpr + t) * VEC;
+            if (live && c < p.D) {
+                if (post)
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) dn[i][e] = iy * (dn[i][e] - ld(&y[i].e[e]) * iy * mean_y);
+                store_vec<T, VEC>(p.dy, row * p.D + c, dn[i]);
+            }
+        }
+    }
+    if (!p.want_post && !p.want_pre) return;
+    // this CTA's column sums: over its row groups in order, then to the workspace
+    float *dst = p.part + (size_t)blockIdx.x * 2 * p.D;
+    if (per > 1) {
+        for (int s = 0; s < per; ++s) {
+            __syncthreads();
+            if (sub == s) {
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    const int c = (i * tpr + t) * VEC;
+                    if (c < p.D)
+#pragma unroll
+                        for (int e = 0; e < VEC; ++e) {
+                            colsum[c + e] = (s ? colsum[c + e] : 0.f) + gpost[i][e];
+                            colsum[p.D + c + e] = (s ? colsum[p.D + c + e] : 0.f) + gpre[i][e];
+                        }
+                }
+            }
+        }
+        __syncthreads();
+        for (int c = threadIdx.x; c < 2 * p.D; c += blockDim.x) dst[c] = colsum[c];
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * tpr + t) * VEC;
+            if (c < p.D)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    dst[c + e] = gpost[i][e];
+                    dst[p.D + c + e] = gpre[i][e];
+                }
+        }
+    }
+}
+
+// dw[c] = sum over the CTAs' partial sums, in order: 32 columns x 8 parts per CTA.
+__global__ void __launch_bounds__(256) weight_sum_kernel(const float *part, int parts, int D, float *dpost, float *dpre) {
+    __shared__ float s[8][33];
+    const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5, c = blockIdx.x * 32 + cx;
+    float *out = blockIdx.y ? dpre : dpost;
+    if (!out) return;
+    float a = 0.f;
+    if (c < D)
+        for (int i = ry; i < parts; i += 8) a += part[(size_t)i * 2 * D + (size_t)blockIdx.y * D + c];
+    s[ry][cx] = a;
+    __syncthreads();
+    if (ry == 0 && c < D) {
+#pragma unroll
+        for (int i = 1; i < 8; ++i) a += s[i][cx];
+        out[c] = a;
+    }
+}
+
+struct Shape {
+    int vec, nv, tpr, threads, per;
+};
+// Threads per row: each holds at most 2 vectors while 512 threads are enough
+// (the loads of a row are then all in flight at once), 4 or, for single
+// elements, 16 behind that.
+Shape choose_shape(int D, int vec) {
+    static constexpr int most[5][2] = {{2, 256}, {2, 512}, {4, 512}, {4, 1024}, {16, 1024}};
+    const int vecs = (D + vec - 1) / vec;
+    int i = 0;
+    while (i < 4 && most[i][0] * most[i][1] < vecs) ++i;
+    Shape s;
+    s.vec = vec;
+    s.nv = most[i][0];
+    s.tpr = 1;
+    while (s.tpr * s.nv < vecs) s.tpr *= 2;
+    if (vecs == 1) s.nv = 1;
+    s.threads = std::max(kThreads, s.tpr);
+    s.per = s.threads / s.tpr;
+    return s;
+}
+
+template <typename T, int VEC, int NV, int MT>
+cudaError_t launch_nv(const Params &p, const Shape &s, bool bwd, unsigned grid, cudaStream_t st) {
+    if (bwd) {
+        const size_t bytes = s.per > 1 ? (size_t)2 * p.D * sizeof(float) : 0;
+        bwd_kernel<T, VEC, NV, MT><<<grid, s.threads, bytes, st>>>(p);
+    } else {
+        fwd_kernel<T, VEC, NV, MT><<<grid, s.threads, 0, st>>>(p);
+    }
+    return cudaGetLastError();
+}
+template <typename T, int VEC>
+cudaError_t launch_vec(const Params &p, const Shape &s, bool bwd, unsigned grid, cudaStream_t st) {
+    if (s.nv == 1) return launch_nv<T, VEC, 1, 256>(p, s, bwd, grid, st);
+    if (s.nv == 2 && s.threads == 256) return launch_nv<T, VEC, 2, 256>(p, s, bwd, grid, st);
+    if (s.nv == 2) return launch_nv<T, VEC, 2, 512>(p, s, bwd, grid, st);
+    if (s.nv == 4 && s.threads == 512) return launch_nv<T, VEC, 4, 512>(p, s, bwd, grid, st);
+    if (s.nv == 4) return launch_nv<T, VEC, 4, 1024>(p, s, bwd, grid, st);
+    // 16 x 1024 = kMaxD: only single elements come here
+    if constexpr (VEC == 1) return launch_nv<T, 1, 16, 1024>(p, s, bwd, grid, st);
+    return cudaErrorInvalidValue;
+}
+template <typename T>
+cudaError_t launch_t(const Params &p, const Shape &s, bool bwd, unsigned grid, cudaStream_t st) {
+    if (s.vec == 1) return launch_vec<T, 1>(p, s, bwd, grid, st);
+    return launch_vec<T, 16 / (int)sizeof(T)>(p, s, bwd, grid, st);
+}
+
+}  // namespace norm
+}  // namespace kda
+
+namespace {
+
+using kda::is_aligned;
+using kda::norm::Params;
+using kda::norm::Shape;
+
+int sm_count() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
+        cudaGetLastError();
+        n = 148;
+    }
+    return n;
+}
+
+int check_shape(int64_t rows, int32_t D, kda_dtype dtype, int32_t flags, float eps) {
+    const int all = KDA_NORM_POST | KDA_NORM_PRE | KDA_NORM_GATE_SIGMOID | KDA_NORM_GATE_SILU;
+    const int acts = KDA_NORM_GATE_SIGMOID | KDA_NORM_GATE_SILU;
+    if (rows < 0 || D < 1 || (flags & ~all) || (flags & acts) == acts || !(eps >= 0.f)) return KDA_ERR_INVALID_ARG;
+    if (dtype != KDA_DTYPE_F32 && dtype != KDA_DTYPE_BF16) return KDA_ERR_UNSUPPORTED;
+    if (D > kda::norm::kMaxD || rows > (1LL << 40) / D) return KDA_ERR_UNSUPPORTED;
+    return KDA_OK;
+}
+
+// 16-byte vectors when every row of every buffer allows them
+int vec_of(const Params &p, const void *const *ptrs, int n, size_t esz) {
+    const int vec = (int)(16 / esz);
+    if (p.D % vec || p.y_ld % vec || (p.gate && p.gate_ld % vec) || (p.x && p.x_ld % vec)) return 1;
+    for (int i = 0; i < n; ++i)
+        if (ptrs[i] && !is_aligned(ptrs[i], 16)) return 1;
+    return vec;
+}
+int check_elems(const void *const *ptrs, int n, size_t esz) {
+    for (int i = 0; i < n; ++i)
+        if (ptrs[i] && !is_aligned(ptrs[i], esz)) return KDA_ERR_ALIGNMENT;
+    return KDA_OK;
+}
+
+int bwd_parts(int64_t rows, const Shape &s) {
+    const int64_t batches = (rows + s.per - 1) / s.per;
+    return (int)std::max<int64_t>(1, std::min<int64_t>(batches, (int64_t)sm_count() * (s.threads > 512 ? 1 : 1024 / s.threads)));
+}
+
+}  // namespace
+
+extern "C" {
+
+int kda_block_norm(const void *y, int64_t y_stride, const void *post_weight, const void *gate, int64_t gate_stride,
+                   const void *residual, int64_t residual_stride, const void *pre_weight, void *out, void *normed,
+                   int64_t rows, int32_t D, kda_dtype dtype, float res_scale, float eps, int32_t flags,
+                   kda_stream_t stream) {
+    int rc = check_shape(rows, D, dtype, flags, eps);
+    if (rc != KDA_OK) return rc;
+    if ((post_weight && !(flags & KDA_NORM_POST)) || (pre_weight && !(flags & KDA_NORM_PRE))) return KDA_ERR_INVALID_ARG;
+    if (rows == 0) return KDA_OK;
+    if ((normed != nullptr) != ((flags & KDA_NORM_PRE) != 0)) return KDA_ERR_INVALID_ARG;
+    if (!y || !out || y_stride < D || (gate && gate_stride < D) || (residual && residual_stride < D))
+        return KDA_ERR_INVALID_ARG;
+    const bool bf16 = dtype == KDA_DTYPE_BF16;
+    const void *ptrs[] = {y, gate, residual, post_weight, pre_weight, out, normed};
+    rc = check_elems(ptrs, 7, bf16 ? 2 : 4);
+    if (rc != KDA_OK) return rc;
+    Params p{};
+    p.y = y; p.gate = gate; p.x = residual; p.w_post = post_weight; p.w_pre = pre_weight;
+    p.y_ld = y_stride; p.gate_ld = gate_stride; p.x_ld = residual_stride;
+    p.out = out; p.normed = normed;
+    p.rows = rows; p.D = D; p.flags = flags; p.c = res_scale; p.eps = eps;
+    const Shape s = kda::norm::choose_shape(D, vec_of(p, ptrs, 7, bf16 ? 2 : 4));
+    p.tpr = s.tpr;
+    const int64_t grid = (rows + s.per - 1) / s.per;
+    if (grid > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
+    const cudaError_t e = bf16 ? kda::norm::launch_t<__nv_bfloat16>(p, s, false, (unsigned)grid, (cudaStream_t)stream)
+                               : kda::norm::launch_t<float>(p, s, false, (unsigned)grid, (cudaStream_t)stream);
+    return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+size_t kda_block_norm_bwd_workspace_size(int64_t rows, int32_t D, kda_dtype dtype) {
+    if (check_shape(rows, D, dtype, 0, 0.f) != KDA_OK) return 0;
+    // the most partial sums either vector width makes
+    const int wide = bwd_parts(rows, kda::norm::choose_shape(D, dtype == KDA_DTYPE_BF16 ? 8 : 4));
+    const int one = bwd_parts(rows, kda::norm::choose_shape(D, 1));
+    return (size_t)std::max(wide, one) * 2 * D * sizeof(float);
+}
+
+int kda_block_norm_bwd(const void *dout, const void *dnormed, const void *y, int64_t y_stride, const void *post_weight,
+                       const void *gate, int64_t gate_stride, const void *residual, int64_t residual_stride,
+                       const void *pre_weight, void *dy, void *dgate, void *dresidual, float *dpost_weight,
+                       float *dpre_weight, int64_t rows, int32_t D, kda_dtype dtype, float res_scale, float eps,
+                       int32_t flags, void *workspace, size_t workspace_bytes, kda_stream_t stream) {
+    cudaStream_t st = (cudaStream_t)stream;
+    int rc = check_shape(rows, D, dtype, flags, eps);
+    if (rc != KDA_OK) return rc;
+    if ((post_weight && !(flags & KDA_NORM_POST)) || (pre_weight && !(flags & KDA_NORM_PRE)) ||
+        (dpost_weight && !post_weight) || (dpre_weight && !pre_weight) || (dnormed && !(flags & KDA_NORM_PRE)) ||
+        (dgate && !gate) || (dresidual && !residual))
+        return KDA_ERR_INVALID_ARG;
+    const bool weights = dpost_weight || dpre_weight;
+    if (rows > 0 && (!y || !dy || (!dout && !dnormed) || y_stride < D || (gate && gate_stride < D) ||
+                     (residual && residual_stride < D)))
+        return KDA_ERR_INVALID_ARG;
+    const bool bf16 = dtype == KDA_DTYPE_BF16;
+    const void *ptrs[] = {y, gate, residual, post_weight, pre_weight, dout, dnormed, dy, dgate, dresidual};
+    rc = check_elems(ptrs, 10, bf16 ? 2 : 4);
+    if (rc != KDA_OK) return rc;
+    if (!is_aligned(dpost_weight, 4) || !is_aligned(dpre_weight, 4) || !is_aligned(workspace, 16)) return KDA_ERR_ALIGNMENT;
+    Params p{};
+    p.y = y; p.gate = gate; p.x = residual; p.w_post = post_weight; p.w_pre = pre_weight;
+    p.y_ld = y_stride; p.gate_ld = gate_stride; p.x_ld = residual_stride;
+    p.dr = dout; p.dh = dnormed; p.dy = dy; p.dgate = dgate; p.dx = dresidual;
+    p.rows = rows; p.D = D; p.flags = flags; p.c = res_scale; p.eps = eps;
+    p.want_post = dpost_weight != nullptr;
+    p.want_pre = dpre_weight != nullptr;
+    const Shape s = kda::norm::choose_shape(D, vec_of(p, ptrs, 10, bf16 ? 2 : 4));
+    p.tpr = s.tpr;
+    const int parts = bwd_parts(rows, s);
+    if (weights && (!workspace || workspace_bytes < (size_t)parts * 2 * D * sizeof(float))) return KDA_ERR_WORKSPACE;
+    p.part = (float *)workspace;
+    if (rows > 0) {
+        const cudaError_t e = bf16 ? kda::norm::launch_t<__nv_bfloat16>(p, s, true, (unsigned)parts, st)
+                                   : kda::norm::launch_t<float>(p, s, true, (unsigned)parts, st);
+        if (e != cudaSuccess) return KDA_ERR_CUDA;
+    }
+    if (weights) {
+        kda::norm::weight_sum_kernel<<<dim3((D + 31) / 32, 2), 256, 0, st>>>(p.part, rows > 0 ? parts : 0, D,
+                                                                            dpost_weight, dpre_weight);
+        if (cudaGetLastError() != cudaSuccess) return KDA_ERR_CUDA;
+    }
+    return KDA_OK;
+}
+
+}  // extern "C"

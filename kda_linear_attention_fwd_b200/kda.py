@@ -24,10 +24,16 @@ EXPORTS = ("kda_status_string", "kda_chunk_fwd_workspace_size", "kda_chunk_fwd_p
            "kda_chunk_fwd", "kda_decode_step", "kda_chunk_fwd_ex", "kda_decode_step_ex",
            "kda_chunk_fwd_summary", "kda_state_compose", "kda_bwd_workspace_size", "kda_bwd",
            "kda_chunk_fwd_check", "kda_build_checks_g", "kda_chunk_fwd_noalloc",
-           "kda_chunk_fwd_noalloc_check", "kda_chunk_fwd_sub_pieces")
+           "kda_chunk_fwd_noalloc_check", "kda_chunk_fwd_sub_pieces",
+           "kda_lin_chunk_fwd_workspace_size", "kda_lin_chunk_fwd", "kda_lin_decode_step",
+           "kda_lin_bwd_workspace_size", "kda_lin_bwd", "kda_block_norm",
+           "kda_block_norm_bwd_workspace_size", "kda_block_norm_bwd")
 
 # flags of the extended entry points (include/kda.h)
 FLAG_QK_L2NORM, FLAG_BETA_LOGITS, FLAG_GATE_LOGITS, FLAG_CLAMP_DECAY = 1, 2, 4, 8
+# flags of the operators with one decay per head and of the block norms
+LIN_DECAY_PER_HEAD = 1
+NORM_POST, NORM_PRE, NORM_GATE_SIGMOID, NORM_GATE_SILU = 1, 2, 4, 8
 
 _lib = None
 _lib_checked = None
@@ -103,6 +109,25 @@ def _open(path):
     lib.kda_chunk_fwd_noalloc.restype = ctypes.c_int
     lib.kda_chunk_fwd_noalloc_check.argtypes = [P]
     lib.kda_chunk_fwd_noalloc_check.restype = ctypes.c_int
+    i64 = ctypes.c_int64
+    lib.kda_lin_chunk_fwd_workspace_size.argtypes = [i32] * 6 + [ctypes.c_int]
+    lib.kda_lin_chunk_fwd_workspace_size.restype = sz
+    lib.kda_lin_chunk_fwd.argtypes = [P] * 7 + [i32] * 6 + [ctypes.c_int, f32, i32, P, P, P, sz, P]
+    lib.kda_lin_chunk_fwd.restype = ctypes.c_int
+    lib.kda_lin_decode_step.argtypes = [P] * 6 + [i32] * 5 + [ctypes.c_int, f32, i32, P]
+    lib.kda_lin_decode_step.restype = ctypes.c_int
+    lib.kda_lin_bwd_workspace_size.argtypes = [i32] * 6
+    lib.kda_lin_bwd_workspace_size.restype = sz
+    lib.kda_lin_bwd.argtypes = [P] * 7 + [i32] * 6 + [ctypes.c_int, f32, i32] + [P] * 8 + [sz, P]
+    lib.kda_lin_bwd.restype = ctypes.c_int
+    lib.kda_block_norm.argtypes = [P, i64, P, P, i64, P, i64, P, P, P, i64, i32, ctypes.c_int, f32,
+                                   f32, i32, P]
+    lib.kda_block_norm.restype = ctypes.c_int
+    lib.kda_block_norm_bwd_workspace_size.argtypes = [i64, i32, ctypes.c_int]
+    lib.kda_block_norm_bwd_workspace_size.restype = sz
+    lib.kda_block_norm_bwd.argtypes = [P, P, P, i64, P, P, i64, P, i64, P, P, P, P, P, P, i64, i32,
+                                       ctypes.c_int, f32, f32, i32, P, sz, P]
+    lib.kda_block_norm_bwd.restype = ctypes.c_int
     return lib
 
 
@@ -330,3 +355,258 @@ def chunk_fwd_check(workspace, stream=None, lib=None) -> int:
     lib = lib or load()
     return int(lib.kda_chunk_fwd_check(_ptr(workspace), workspace.numel() * workspace.element_size(),
                                        _stream(stream)))
+
+
+# ---------------------------------------------- linear attention, one decay per head
+_CODES = {torch.bfloat16: KDA_DTYPE_BF16, torch.float32: KDA_DTYPE_F32}
+
+
+class _on:
+    """The call's device and stream: the tensors' device is made current (the
+    library launches there), the stream defaults to that device's current one."""
+    __slots__ = ("dev", "prev")
+
+    def __init__(self, t):
+        self.dev = t.device.index
+
+    def __enter__(self):
+        self.prev = torch.cuda.current_device()
+        if self.prev != self.dev:
+            torch.cuda.set_device(self.dev)
+        return self
+
+    def __exit__(self, *exc):
+        if self.prev != self.dev:
+            torch.cuda.set_device(self.prev)
+
+    def stream(self, stream):
+        return torch._C._cuda_getCurrentRawStream(self.dev) if stream is None else stream.cuda_stream
+
+
+def _tensor(name, t, shape, dtype, like):
+    """Refuses a tensor the kernels could not read as it is."""
+    if t.dtype != dtype or t.shape != shape or t.device != like.device or not t.is_contiguous():
+        raise ValueError(f"{name}: want a contiguous {dtype} tensor of shape {tuple(shape)} on "
+                         f"{like.device}, got {t.dtype} {tuple(t.shape)} on {t.device}"
+                         f"{'' if t.is_contiguous() else ', not contiguous'}")
+    return t.data_ptr()
+
+
+def _opt(name, t, shape, dtype, like):
+    return None if t is None else _tensor(name, t, shape, dtype, like)
+
+
+def _code(t):
+    try:
+        return _CODES[t.dtype]
+    except KeyError:
+        raise TypeError(f"unsupported dtype {t.dtype}") from None
+
+
+def _space(workspace, need, like):
+    if workspace is None:
+        return torch.empty(max(need, 16), dtype=torch.uint8, device=like.device)
+    if workspace.device != like.device or not workspace.is_contiguous():
+        raise ValueError(f"workspace: want a contiguous tensor on {like.device}")
+    return workspace  # too small a one is refused by the library
+
+
+def _lin_shapes(q, k, v, g):
+    if not q.is_cuda:
+        raise ValueError("all tensors must be CUDA tensors")
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError("q, k are [tokens, Hk, dk], v is [tokens, H, dv]")
+    T, Hk, dk = q.shape
+    H, dv = v.shape[1], v.shape[2]
+    per_head = g.dim() == 1
+    dt = q.dtype
+    ptrs = (_tensor("q", q, q.shape, dt, q), _tensor("k", k, q.shape, dt, q),
+            _tensor("v", v, (T, H, dv), dt, q), _tensor("g", g, (H,) if per_head else (T, H), dt, q))
+    return T, H, Hk, dk, dv, LIN_DECAY_PER_HEAD if per_head else 0, _code(q), ptrs
+
+
+def _host_offsets(cu_seqlens_host, N):
+    if cu_seqlens_host is None:
+        return None
+    if len(cu_seqlens_host) != N + 1:
+        raise ValueError("cu_seqlens_host and cu_seqlens differ in length")
+    return (ctypes.c_int32 * (N + 1))(*cu_seqlens_host)
+
+
+def lin_workspace_size(total_tokens, num_seqs, H, Hk, dk, dv, dtype=torch.bfloat16) -> int:
+    return int(load().kda_lin_chunk_fwd_workspace_size(total_tokens, num_seqs, H, Hk, dk, dv,
+                                                       _CODES[dtype]))
+
+
+def lin_chunk_fwd(q, k, v, g, cu_seqlens, *, scale=1.0, initial_state=None, final_state=None,
+                  out=None, workspace=None, cu_seqlens_host=None, output_final_state=True,
+                  stream=None):
+    """Linear attention with one decay per head over packed sequences:
+    S <- exp(g) S + k v^T, o = S^T (scale q).  q, k [T, Hk, dk]; v [T, H, dv],
+    H a multiple of Hk; g [T, H], or [H] for the same decay at every token;
+    cu_seqlens int32 [N+1] (device).  Returns (out, final_state); final_state
+    may be initial_state itself."""
+    lib = load()
+    T, H, Hk, dk, dv, flags, code, ptrs = _lin_shapes(q, k, v, g)
+    N = cu_seqlens.shape[0] - 1
+    p_cu = _tensor("cu_seqlens", cu_seqlens, (N + 1,), torch.int32, q)
+    states = (N, H, dk, dv)
+    if out is None:
+        out = torch.empty_like(v)
+    if final_state is None and output_final_state:
+        final_state = torch.empty(states, dtype=torch.float32, device=q.device)
+    p_out = _tensor("out", out, v.shape, q.dtype, q)
+    p_s0 = _opt("initial_state", initial_state, states, torch.float32, q)
+    p_s1 = _opt("final_state", final_state, states, torch.float32, q)
+    host = _host_offsets(cu_seqlens_host, N)
+    with _on(q) as on:
+        ws = _space(workspace, 0 if workspace is not None else lib.kda_lin_chunk_fwd_workspace_size(
+            T, N, H, Hk, dk, dv, code), q)
+        st = lib.kda_lin_chunk_fwd(*ptrs, p_out, p_cu, host, N, T, H, Hk, dk, dv, code, scale, flags,
+                                   p_s0, p_s1, ws.data_ptr(), ws.numel() * ws.element_size(),
+                                   on.stream(stream))
+    _check("kda_lin_chunk_fwd", st)
+    return out, final_state
+
+
+def lin_decode_step(q, k, v, g, state, *, scale=1.0, out=None, stream=None):
+    """One token per sequence.  q, k [N, Hk, dk]; v [N, H, dv]; g [N, H] or
+    [H]; state [N, H, dk, dv] fp32, updated in place.  Returns out."""
+    lib = load()
+    N, H, Hk, dk, dv, flags, code, ptrs = _lin_shapes(q, k, v, g)
+    if out is None:
+        out = torch.empty_like(v)
+    p_out = _tensor("out", out, v.shape, q.dtype, q)
+    p_s = _tensor("state", state, (N, H, dk, dv), torch.float32, q)
+    with _on(q) as on:
+        st = lib.kda_lin_decode_step(*ptrs, p_out, p_s, N, H, Hk, dk, dv, code, scale, flags,
+                                     on.stream(stream))
+    _check("kda_lin_decode_step", st)
+    return out
+
+
+def lin_bwd_workspace_size(total_tokens, num_seqs, H, Hk, dk, dv) -> int:
+    return int(load().kda_lin_bwd_workspace_size(total_tokens, num_seqs, H, Hk, dk, dv))
+
+
+def lin_bwd(q, k, v, g, dy, cu_seqlens, *, scale=1.0, initial_state=None, d_final_state=None,
+            cu_seqlens_host=None, workspace=None, stream=None):
+    """Gradients of lin_chunk_fwd: a dict of dq, dk [T, Hk, dk], dv [T, H, dv],
+    dg (the shape of g), all in the inputs' dtype, and ds0 [N, H, dk, dv] fp32."""
+    lib = load()
+    T, H, Hk, dk, dv, flags, code, ptrs = _lin_shapes(q, k, v, g)
+    N = cu_seqlens.shape[0] - 1
+    p_cu = _tensor("cu_seqlens", cu_seqlens, (N + 1,), torch.int32, q)
+    p_dy = _tensor("dy", dy, v.shape, q.dtype, q)
+    states = (N, H, dk, dv)
+    p_s0 = _opt("initial_state", initial_state, states, torch.float32, q)
+    p_ds = _opt("d_final_state", d_final_state, states, torch.float32, q)
+    # tokens outside every sequence keep what is there: zeros only where the
+    # offsets are not known to cover every token
+    new = torch.empty_like if cu_seqlens_host is not None else torch.zeros_like
+    out = {"dq": new(q), "dk": new(k), "dv": new(v), "dg": new(g),
+           "ds0": torch.empty(states, dtype=torch.float32, device=q.device)}
+    host = _host_offsets(cu_seqlens_host, N)
+    with _on(q) as on:
+        ws = _space(workspace, 0 if workspace is not None else lib.kda_lin_bwd_workspace_size(
+            T, N, H, Hk, dk, dv), q)
+        st = lib.kda_lin_bwd(*ptrs, p_dy, p_cu, host, N, T, H, Hk, dk, dv, code, scale, flags, p_s0, p_ds,
+                             out["dq"].data_ptr(), out["dk"].data_ptr(), out["dv"].data_ptr(),
+                             out["dg"].data_ptr(), out["ds0"].data_ptr(), ws.data_ptr(),
+                             ws.numel() * ws.element_size(), on.stream(stream))
+    _check("kda_lin_bwd", st)
+    return out
+
+
+# ------------------------------------------------------------ norms around a block
+def _norm_rows(name, t, like):
+    """(address, row stride) of a tensor whose rows (last dimension) are contiguous."""
+    if t is None:
+        return None, 0
+    if t.dtype != like.dtype or t.shape != like.shape or t.device != like.device:
+        raise ValueError(f"{name}: want {like.dtype} {tuple(like.shape)} on {like.device}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    D = t.shape[-1]
+    if t.is_contiguous():
+        return t.data_ptr(), D
+    rows = t.flatten(0, -2) if t.dim() != 2 else t
+    if rows.data_ptr() != t.data_ptr() or rows.stride(1) != 1 or (rows.shape[0] > 1 and rows.stride(0) < D):
+        raise ValueError(f"{name}: rows must be contiguous and evenly spaced, got strides {t.stride()}")
+    return t.data_ptr(), max(rows.stride(0), D)
+
+
+def _norm_flags(post_norm, post_weight, pre_norm, pre_weight, gate, gate_logits, gate_silu):
+    if gate_logits and gate_silu:
+        raise ValueError("gate_logits and gate_silu exclude each other")
+    if (post_weight is not None and not post_norm) or (pre_weight is not None and not pre_norm):
+        raise ValueError("a weight without its norm")
+    return ((NORM_POST if post_norm else 0) | (NORM_PRE if pre_norm else 0) |
+            (NORM_GATE_SIGMOID if gate_logits and gate is not None else 0) |
+            (NORM_GATE_SILU if gate_silu and gate is not None else 0))
+
+
+def block_norm(y, *, post_norm=True, post_weight=None, gate=None, gate_logits=False, gate_silu=False,
+               residual=None, res_scale=1.0, pre_norm=False, pre_weight=None, eps=1e-6, out=None,
+               normed=None, stream=None):
+    """The norm of a block's output with its gate and the scaled residual, and
+    the next block's norm: u = act(gate) * rmsnorm(y) * post_weight, out =
+    residual + res_scale * u, normed = rmsnorm(out) * pre_weight, over the last
+    dimension of y [..., D].  Returns (out, normed); normed is None without
+    pre_norm.  out and normed may be y, gate or residual themselves."""
+    lib = load()
+    if not y.is_cuda:
+        raise ValueError("all tensors must be CUDA tensors")
+    D = y.shape[-1]
+    code, dt = _code(y), y.dtype
+    flags = _norm_flags(post_norm, post_weight, pre_norm, pre_weight, gate, gate_logits, gate_silu)
+    p_y, s_y = _norm_rows("y", y, y)
+    p_g, s_g = _norm_rows("gate", gate, y)
+    p_x, s_x = _norm_rows("residual", residual, y)
+    p_wp, p_wn = _opt("post_weight", post_weight, (D,), dt, y), _opt("pre_weight", pre_weight, (D,), dt, y)
+    if out is None:
+        out = torch.empty(y.shape, dtype=dt, device=y.device)
+    if normed is None and pre_norm:
+        normed = torch.empty(y.shape, dtype=dt, device=y.device)
+    p_out, p_n = _tensor("out", out, y.shape, dt, y), _opt("normed", normed, y.shape, dt, y)
+    with _on(y) as on:
+        st = lib.kda_block_norm(p_y, s_y, p_wp, p_g, s_g, p_x, s_x, p_wn, p_out, p_n,
+                                y.numel() // D if D else 0, D, code, res_scale, eps, flags, on.stream(stream))
+    _check("kda_block_norm", st)
+    return out, normed
+
+
+def block_norm_bwd(dout, dnormed, y, *, post_norm=True, post_weight=None, gate=None, gate_logits=False,
+                   gate_silu=False, residual=None, res_scale=1.0, pre_norm=False, pre_weight=None,
+                   eps=1e-6, workspace=None, stream=None):
+    """Gradients of block_norm for dout and dnormed (either None = zeros): a
+    dict of dy, dgate, dresidual in y's dtype and dpost_weight, dpre_weight [D]
+    fp32; None for what was not given."""
+    lib = load()
+    if not y.is_cuda:
+        raise ValueError("all tensors must be CUDA tensors")
+    D = y.shape[-1]
+    code, dt = _code(y), y.dtype
+    flags = _norm_flags(post_norm, post_weight, pre_norm, pre_weight, gate, gate_logits, gate_silu)
+    if dout is None and dnormed is None:
+        raise ValueError("dout and dnormed are both None")
+    p_y, s_y = _norm_rows("y", y, y)
+    p_g, s_g = _norm_rows("gate", gate, y)
+    p_x, s_x = _norm_rows("residual", residual, y)
+    p_wp, p_wn = _opt("post_weight", post_weight, (D,), dt, y), _opt("pre_weight", pre_weight, (D,), dt, y)
+    p_do, p_dn = _opt("dout", dout, y.shape, dt, y), _opt("dnormed", dnormed, y.shape, dt, y)
+    rows = y.numel() // D if D else 0
+
+    def like(t, shape=None, dtype=None):
+        return None if t is None else torch.empty(shape or t.shape, dtype=dtype or t.dtype, device=y.device)
+
+    got = {"dy": like(y), "dgate": like(gate), "dresidual": like(residual),
+           "dpost_weight": like(post_weight, (D,), torch.float32), "dpre_weight": like(pre_weight, (D,), torch.float32)}
+    with _on(y) as on:
+        need = lib.kda_block_norm_bwd_workspace_size(rows, D, code) if workspace is None else 0
+        ws = _space(workspace, need, y)
+        st = lib.kda_block_norm_bwd(p_do, p_dn, p_y, s_y, p_wp, p_g, s_g, p_x, s_x, p_wn,
+                                    *(None if t is None else t.data_ptr() for t in got.values()), rows, D, code,
+                                    res_scale, eps, flags, ws.data_ptr(), ws.numel() * ws.element_size(),
+                                    on.stream(stream))
+    _check("kda_block_norm_bwd", st)
+    return got

@@ -1,0 +1,349 @@
+"""Linear attention with one decay per head (kda_lin_chunk_fwd,
+kda_lin_decode_step, kda_lin_bwd) on the GPU against the fp64 oracle.
+
+Tolerances, as ||err||_2 / ||ref||_2:
+  fp32 results of fp32 inputs: 1e-5, i.e. 168 half steps of 2^-24; the longest
+    sums here have some 128 channels times the tokens in memory, whose
+    independent roundings add up as the root of their number.
+  fp32 states of bf16 inputs: 2e-5.  k v^T of bf16 values is exact in fp32;
+    a kernel that splits a decayed value into two bf16 parts leaves at most
+    2^-8 2^-8 = 2^-16 = 1.5e-5 of it.
+  bf16 results: 4e-3.  One rounding is off by at most 2^-8 of the value, in
+    the root mean square by at most 2^-8 / sqrt(3) = 2.3e-3; a result goes
+    through three independent ones (the products inside a chunk, the state as
+    an operand, the output): sqrt(3) 2.3e-3 = 3.9e-3.
+"""
+import numpy as np
+import pytest
+import torch
+
+from kda_linear_attention_fwd_b200 import kda
+from oracle import linear as O
+from parity import np32
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+TOL = {torch.bfloat16: 4e-3, torch.float32: 1e-5}
+
+
+def make(lengths, H, Hk, dk, dv, dtype, per_head=False, s0=True, seed=0):
+    gen = torch.Generator().manual_seed(seed)
+    T, N, dt = sum(lengths), len(lengths), DT[dtype]
+    randn = lambda *s: torch.randn(*s, generator=gen)  # noqa: E731
+    unit = lambda x: x / x.norm(dim=-1, keepdim=True)  # noqa: E731
+    bias = -6.0 * torch.arange(H) / max(H - 1, 1)   # memories of about one to 400 tokens
+    g = -torch.nn.functional.softplus(bias if per_head else bias + randn(T, H))
+    cu = [0]
+    for L in lengths:
+        cu.append(cu[-1] + L)
+    d = dict(q=unit(randn(T, Hk, dk)).to(dt), k=unit(randn(T, Hk, dk)).to(dt), v=randn(T, H, dv).to(dt), g=g.to(dt),
+             s0=0.1 * randn(N, H, dk, dv) if s0 else None, dy=randn(T, H, dv).to(dt), dsf=randn(N, H, dk, dv))
+    d = {k: None if x is None else x.cuda() for k, x in d.items()}
+    d["cu"], d["host"] = torch.tensor(cu, dtype=torch.int32, device="cuda"), cu
+    return d
+
+
+def near(got, want, tol, what):
+    a, e = np32(got).astype(np.float64), np.asarray(want, np.float64)
+    assert a.shape == e.shape, (what, a.shape, e.shape)
+    assert np.isfinite(a).all(), f"{what}: not finite"
+    off = np.linalg.norm(a - e) / max(np.linalg.norm(e), 1e-30) if e.size else 0.0
+    assert off <= tol, f"{what}: relative error {off:.2e} > {tol:.1e}"
+
+
+def fwd_both(d, scale=0.5, **kw):
+    out, fin = kda.lin_chunk_fwd(d["q"], d["k"], d["v"], d["g"], d["cu"], scale=scale, initial_state=d["s0"],
+                                 cu_seqlens_host=d["host"], **kw)
+    ref = O.forward(np32(d["q"]), np32(d["k"]), np32(d["v"]), np32(d["g"]), d["host"], scale=scale,
+                    initial_state=np32(d["s0"]))
+    return out, fin, ref
+
+
+SHAPES = [("bf16", 128, 128), ("bf16", 64, 128), ("bf16", 128, 64), ("bf16", 64, 64), ("f32", 128, 128),
+          ("f32", 64, 128), ("f32", 128, 64), ("f32", 64, 64)]
+LENGTHS = [(1,), (0, 5, 64, 0, 130), (127, 128, 129), (700, 1, 63, 65), (1111,), (0,)]
+
+
+@pytest.mark.parametrize("dtype,dk,dv", SHAPES)
+@pytest.mark.parametrize("lengths", LENGTHS, ids=str)
+def test_prefill_matches_oracle(cuda_lib, dtype, dk, dv, lengths):
+    seed = len(lengths) + sum(lengths)
+    d = make(lengths, 4, 2, dk, dv, dtype, per_head=seed % 2 == 0, s0=sum(lengths) != 1111, seed=seed)
+    out, fin, (o, S) = fwd_both(d)
+    near(out, o, TOL[d["q"].dtype], "out")
+    near(fin, S, 2e-5 if dtype == "bf16" else 1e-5, "final state")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("H,Hk", [(1, 1), (6, 2), (5, 5), (8, 1)])
+def test_prefill_head_layouts(cuda_lib, dtype, H, Hk):
+    d = make((200, 77), H, Hk, 64, 64, dtype, seed=H)
+    out, fin, (o, S) = fwd_both(d, scale=1.0)
+    near(out, o, TOL[d["q"].dtype], "out")
+    near(fin, S, 2e-5 if dtype == "bf16" else 1e-5, "final state")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_prefill_many_short_sequences(cuda_lib, dtype):
+    """Windows that hold dozens of sequences, empty ones among them."""
+    rng = np.random.default_rng(5)
+    d = make(tuple(int(x) for x in rng.integers(0, 9, 150)), 3, 3, 64, 128, dtype, seed=6)
+    out, fin, (o, S) = fwd_both(d)
+    near(out, o, TOL[d["q"].dtype], "out")
+    near(fin, S, 2e-5 if dtype == "bf16" else 1e-5, "final state")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_prefill_state_in_place(cuda_lib, dtype):
+    """final_state = initial_state, for sequences that cross several windows."""
+    d = make((900, 3, 0, 640), 2, 2, 128, 128, dtype, seed=7)
+    want, fin = kda.lin_chunk_fwd(d["q"], d["k"], d["v"], d["g"], d["cu"], initial_state=d["s0"])
+    for _ in range(3):
+        s = d["s0"].clone()
+        out, got = kda.lin_chunk_fwd(d["q"], d["k"], d["v"], d["g"], d["cu"], initial_state=s, final_state=s)
+        assert got is s and torch.equal(out, want) and torch.equal(s, fin)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_decays_of_every_size(cuda_lib, dtype):
+    """No decay at all, resets by -inf and by large finite values, and mixtures."""
+    d = make((300, 40), 4, 4, 128, 64, dtype, seed=8)
+    g = d["g"].float()
+    g[:, 0] = 0.0
+    g[::7, 1] = -float("inf")
+    g[5::11, 2] = -500.0
+    g[:, 3] *= 30.0
+    g[0, 1] = -float("inf")
+    d["g"] = g.to(d["g"].dtype)
+    out, fin, (o, S) = fwd_both(d)
+    near(out, o, TOL[d["q"].dtype], "out")
+    near(fin, S, 2e-5 if dtype == "bf16" else 1e-5, "final state")
+    got = kda.lin_bwd(d["q"], d["k"], d["v"], d["g"], d["dy"], d["cu"], initial_state=d["s0"])
+    ref = O.backward(np32(d["q"]), np32(d["k"]), np32(d["v"]), np32(d["g"]), d["host"], np32(d["dy"]),
+                     initial_state=np32(d["s0"]))
+    check_grads(got, ref, dtype)
+
+
+def test_long_context_memory(cuda_lib):
+    """A head that forgets almost nothing over 6000 tokens."""
+    d = make((6000,), 2, 1, 64, 64, "f32", s0=True, seed=9)
+    d["g"] = torch.full_like(d["g"], -1e-4)
+    out, fin, (o, S) = fwd_both(d)
+    near(out, o, 1e-5, "out")
+    near(fin, S, 1e-5, "final state")
+
+
+def test_continuing_from_a_state(cuda_lib):
+    """Two calls over the halves of a sequence give the whole sequence's result."""
+    d = make((500,), 4, 2, 128, 128, "f32", seed=10)
+    whole, fin = kda.lin_chunk_fwd(d["q"], d["k"], d["v"], d["g"], d["cu"], initial_state=d["s0"])
+    s, parts = d["s0"], []
+    for a, b in ((0, 211), (211, 500)):
+        cu = torch.tensor([0, b - a], dtype=torch.int32, device="cuda")
+        o, s = kda.lin_chunk_fwd(*(d[x][a:b].contiguous() for x in ("q", "k", "v", "g")), cu, initial_state=s)
+        parts.append(o)
+    near(torch.cat(parts), np32(whole), 1e-5, "out")
+    near(s, np32(fin), 1e-5, "final state")
+
+
+def test_rows_behind_the_last_sequence_are_left(cuda_lib):
+    d = make((100, 60), 2, 2, 64, 64, "bf16", seed=11)
+    cu = torch.tensor([0, 90, 120], dtype=torch.int32, device="cuda")
+    out = torch.full_like(d["v"], 7.0)
+    d["v"][120:] = float("nan")
+    d["k"][120:] = float("nan")
+    kda.lin_chunk_fwd(d["q"], d["k"], d["v"], d["g"], cu, out=out)
+    assert (out[120:] == 7.0).all() and torch.isfinite(out[:120]).all()
+
+
+@pytest.mark.parametrize("dtype,dk,dv", SHAPES)
+@pytest.mark.parametrize("N,H,Hk,per_head", [(1, 2, 1, True), (3, 5, 5, False), (160, 4, 2, False)])
+def test_decode_matches_oracle(cuda_lib, dtype, dk, dv, N, H, Hk, per_head):
+    d = make((1,) * N, H, Hk, dk, dv, dtype, per_head=per_head, seed=N)
+    s = d["s0"].clone()
+    ref, S = O.forward(np32(d["q"]), np32(d["k"]), np32(d["v"]), np32(d["g"]), d["host"], scale=0.5,
+                       initial_state=np32(d["s0"]))
+    out = kda.lin_decode_step(d["q"], d["k"], d["v"], d["g"], s, scale=0.5)
+    near(out, ref, TOL[d["q"].dtype], "out")
+    near(s, S, 1e-6, "state")
+
+
+def test_decode_steps_equal_prefill(cuda_lib):
+    d = make((40, 40, 40), 4, 2, 128, 128, "f32", seed=12)
+    want, fin = kda.lin_chunk_fwd(d["q"], d["k"], d["v"], d["g"], d["cu"], initial_state=d["s0"])
+    s = d["s0"].clone()
+    steps = {x: d[x].unflatten(0, (3, 40)).transpose(0, 1).contiguous() for x in ("q", "k", "v", "g")}
+    outs = [kda.lin_decode_step(steps["q"][t], steps["k"][t], steps["v"][t], steps["g"][t], s) for t in range(40)]
+    near(torch.stack(outs, 1).flatten(0, 1), np32(want), 1e-5, "out")
+    near(s, np32(fin), 1e-5, "state")
+
+
+def check_grads(got, ref, dtype):
+    for name in ("dq", "dk", "dv", "dg"):
+        assert got[name].dtype == DT[dtype]
+        near(got[name], ref[name], TOL[DT[dtype]], name)
+    near(got["ds0"], ref["ds0"], 2e-5 if dtype == "bf16" else 1e-5, "ds0")
+
+
+@pytest.mark.parametrize("dtype,dk,dv", SHAPES)
+@pytest.mark.parametrize("lengths", [(0, 5, 64, 130), (300, 1, 127), (777,)], ids=str)
+def test_gradients_match_oracle(cuda_lib, dtype, dk, dv, lengths):
+    seed = sum(lengths)
+    d = make(lengths, 4, 2 if seed % 2 else 4, dk, dv, dtype, per_head=len(lengths) == 3, s0=len(lengths) != 1, seed=seed)
+    got = kda.lin_bwd(d["q"], d["k"], d["v"], d["g"], d["dy"], d["cu"], scale=0.5, initial_state=d["s0"],
+                      d_final_state=d["dsf"] if len(lengths) > 1 else None, cu_seqlens_host=d["host"])
+    ref = O.backward(np32(d["q"]), np32(d["k"]), np32(d["v"]), np32(d["g"]), d["host"], np32(d["dy"]), scale=0.5,
+                     initial_state=np32(d["s0"]), d_final_state=np32(d["dsf"]) if len(lengths) > 1 else None)
+    check_grads(got, ref, dtype)
+
+
+def test_gradient_of_single_tokens_without_state(cuda_lib):
+    """dg of a first token is exactly zero when there is no state to decay."""
+    for dtype in DT:
+        d = make((1, 1, 1), 4, 2, 64, 64, dtype, s0=False, seed=13)
+        got = kda.lin_bwd(d["q"], d["k"], d["v"], d["g"], d["dy"], d["cu"], d_final_state=d["dsf"])
+        assert (got["dg"] == 0).all()
+        ref = O.backward(np32(d["q"]), np32(d["k"]), np32(d["v"]), np32(d["g"]), d["host"], np32(d["dy"]),
+                         d_final_state=np32(d["dsf"]))
+        near(got["dk"], ref["dk"], TOL[DT[dtype]], "dk")
+
+
+def test_gradient_is_the_derivative_of_the_forward(cuda_lib):
+    """Along a random direction, (L(x + e) - L(x - e)) / 2 against the gradient, both from the kernels."""
+    d = make((150, 41), 2, 1, 64, 64, "f32", seed=14)
+    got = kda.lin_bwd(d["q"], d["k"], d["v"], d["g"], d["dy"], d["cu"], scale=0.5, initial_state=d["s0"],
+                      d_final_state=d["dsf"])
+    gen = torch.Generator(device="cuda").manual_seed(15)
+
+    def loss(x):
+        o, fin = kda.lin_chunk_fwd(x["q"], x["k"], x["v"], x["g"], d["cu"], scale=0.5, initial_state=x["s0"])
+        return float((o.double() * d["dy"]).sum() + (fin.double() * d["dsf"]).sum())
+
+    for key, name in (("q", "dq"), ("k", "dk"), ("v", "dv"), ("g", "dg"), ("s0", "ds0")):
+        u = torch.randn(d[key].shape, generator=gen, device="cuda")
+        e = 1e-3 if key == "g" else 1e-2
+        slope = (loss({**d, key: d[key] + e * u}) - loss({**d, key: d[key] - e * u})) / (2 * e)
+        want = float((got[name].double() * u).sum())
+        # the loss is linear or nearly so in each input; its fp32 rounding over 2 e bounds the rest
+        size = float(got[name].double().norm() * u.double().norm())
+        assert abs(slope - want) <= 1e-3 * size, (key, slope, want)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_captured_and_replayed(cuda_lib, dtype):
+    """Forward, backward and a decode step in one graph, replayed on new values."""
+    d = make((333, 50), 4, 2, 128, 128, dtype, seed=16)
+    e = make((333, 50), 4, 2, 128, 128, dtype, seed=17)
+    cur = {k: x.clone() if torch.is_tensor(x) else x for k, x in d.items()}
+    state = cur["s0"].clone()
+
+    def work():
+        out, fin = kda.lin_chunk_fwd(cur["q"], cur["k"], cur["v"], cur["g"], cur["cu"], initial_state=cur["s0"])
+        got = kda.lin_bwd(cur["q"], cur["k"], cur["v"], cur["g"], cur["dy"], cur["cu"], initial_state=cur["s0"],
+                          cu_seqlens_host=cur["host"])
+        dec = kda.lin_decode_step(cur["q"][:2], cur["k"][:2], cur["v"][:2], cur["g"][:2], state)
+        return [out, fin, dec] + list(got.values())
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        work()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            outs = work()
+    for x in (e, d):
+        for k in ("q", "k", "v", "g", "s0", "dy"):
+            cur[k].copy_(x[k])
+        state.copy_(x["s0"])
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [o.clone() for o in outs]
+        state.copy_(x["s0"])
+        want = work()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+
+
+def test_two_streams_at_once(cuda_lib):
+    d = [make((900,), 4, 4, 128, 128, "bf16", seed=s) for s in (18, 19)]
+    want = [kda.lin_chunk_fwd(x["q"], x["k"], x["v"], x["g"], x["cu"])[0] for x in d]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in d]
+    for _ in range(4):
+        got = []
+        for x, s in zip(d, streams):
+            ws = torch.empty(kda.lin_workspace_size(900, 1, 4, 4, 128, 128), dtype=torch.uint8, device="cuda")
+            torch.cuda.synchronize()
+            got.append((kda.lin_chunk_fwd(x["q"], x["k"], x["v"], x["g"], x["cu"], workspace=ws, stream=s)[0], ws))
+        torch.cuda.synchronize()
+        for (a, _), b in zip(got, want):
+            assert torch.equal(a, b)
+
+
+def test_bindings_refuse_other_layouts(cuda_lib):
+    d = make((8,), 2, 2, 64, 64, "bf16", seed=20)
+    bad = dict(q=d["q"].transpose(0, 1).contiguous().transpose(0, 1), k=d["k"][:4], v=d["v"].float(), g=d["g"].cpu())
+    for name, t in bad.items():
+        args = {**{x: d[x] for x in ("q", "k", "v", "g")}, name: t}
+        with pytest.raises(ValueError):
+            kda.lin_chunk_fwd(*args.values(), d["cu"])
+    with pytest.raises(ValueError):
+        kda.lin_chunk_fwd(d["q"], d["k"], d["v"], d["g"], d["cu"].long())
+    with pytest.raises(TypeError):
+        kda.lin_chunk_fwd(*(d[x].half() for x in ("q", "k", "v", "g")), d["cu"])
+    with pytest.raises(ValueError):
+        kda.lin_chunk_fwd(d["q"], d["k"], d["v"], d["g"], d["cu"], cu_seqlens_host=[0, 4, 8])
+    with pytest.raises(kda.KdaError):
+        kda.lin_chunk_fwd(d["q"], d["k"], d["v"], d["g"], d["cu"], cu_seqlens_host=[0, 4])
+    with pytest.raises(ValueError):
+        kda.lin_decode_step(d["q"], d["k"], d["v"], d["g"], torch.zeros(8, 2, 64, 64, device="cuda").bfloat16())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_layer_of_them(cuda_lib, dtype):
+    """Linear attention, its per-head norm with the gate, and the residual with
+    the next norm, forward and backward as a training step runs them, against
+    fp64 autograd of the formulas on the same inputs."""
+    H, D = 4, 64
+    d = make((100, 29), H, 2, D, D, dtype, s0=False, seed=21)
+    gen = torch.Generator().manual_seed(22)
+    dt, T = DT[dtype], 129
+    gate, x, dr, dh = (torch.randn(T, H * D, generator=gen).to(dt).cuda() for _ in range(4))
+    w, wn = (1 + 0.1 * torch.randn(n, generator=gen).to(dt).cuda() for n in (D, H * D))
+
+    kw1 = dict(post_weight=w, gate=gate.view(T, H, D), gate_logits=True)
+    kw2 = dict(post_norm=False, residual=x, res_scale=0.5, pre_norm=True, pre_weight=wn)
+    o, _ = kda.lin_chunk_fwd(d["q"], d["k"], d["v"], d["g"], d["cu"], scale=0.5)
+    u, _ = kda.block_norm(o, **kw1)
+    r, h = kda.block_norm(u.view(T, H * D), **kw2)
+    b2 = kda.block_norm_bwd(dr, dh, u.view(T, H * D), **kw2)
+    b1 = kda.block_norm_bwd(b2["dy"].view(T, H, D), None, o, **kw1)
+    got = kda.lin_bwd(d["q"], d["k"], d["v"], d["g"], b1["dy"], d["cu"], scale=0.5)
+
+    names = ("q", "k", "v", "g")
+    leaf = {n: d[n].double().cpu().requires_grad_() for n in names}
+    leaf.update({n: t.double().cpu().requires_grad_() for n, t in dict(gate=gate, x=x, w=w, wn=wn).items()})
+    q, k = (leaf[n].repeat_interleave(2, 1) for n in ("q", "k"))
+    outs = []
+    for a, b in ((0, 100), (100, 129)):
+        G = leaf["g"][a:b].cumsum(0).T
+        low = torch.ones(b - a, b - a, dtype=torch.bool).tril()
+        Dm = torch.where(low, G[:, :, None] - G[:, None], -torch.inf).exp()
+        A = torch.einsum("thd,shd->hts", 0.5 * q[a:b], k[a:b]) * Dm
+        outs.append(torch.einsum("hts,shd->thd", A, leaf["v"][a:b]))
+    ro = torch.cat(outs)
+    rms = lambda t: t * torch.rsqrt(t.square().mean(-1, keepdim=True) + 1e-6)  # noqa: E731
+    ru = rms(ro) * leaf["w"] * leaf["gate"].view(T, H, D).sigmoid()
+    rr = leaf["x"] + 0.5 * ru.flatten(1)
+    rh = rms(rr) * leaf["wn"]
+    ref = dict(zip(leaf, torch.autograd.grad((rr, rh), list(leaf.values()), (dr.double().cpu(), dh.double().cpu()))))
+    # a bf16 chain rounds every tensor on the way (o, u, dy twice: each 2^-8 / sqrt(3) at
+    # most in the root mean square), on top of the single operator's 3.9e-3
+    tol = 4 * TOL[dt]
+    for name, t, e in (("r", r, rr), ("h", h, rh), ("dx", b2["dresidual"], ref["x"]), ("dwn", b2["dpre_weight"], ref["wn"]),
+                       ("dw", b1["dpost_weight"], ref["w"]), ("dgate", b1["dgate"].flatten(1), ref["gate"]),
+                       ("dq", got["dq"], ref["q"]), ("dk", got["dk"], ref["k"]), ("dv", got["dv"], ref["v"]),
+                       ("dg", got["dg"], ref["g"])):
+        near(t, e.detach().numpy(), tol, name)
