@@ -56,6 +56,7 @@ struct Params {
     float *start_copy;      // [W][H] states or null.  When final_state is init, the summary keeps here the
                             // initial state of the sequence that starts in the window and crosses its end:
                             // its last window overwrites that state in the same launch
+    int32_t *err;           // [3] words of the workspace's header: [2] bit 0 = a bounded wait gave up
     // gradient passes
     float *xdot;            // [T][H]: q . dq, written by the dq pass, read by the dk pass
     float *ckpt;            // [slots][H][DA][DB]: the state after each 64-token chunk

@@ -12,6 +12,7 @@ namespace kda {
 namespace lin {
 
 cudaError_t launch_rec(const Params &p, int mode, bool is_bf16, int da, int db, cudaStream_t st);
+cudaError_t launch_tc(const Params &p, int mode, int da, int db, cudaStream_t st);
 cudaError_t launch_scan(float *z, const float *gamma, int W, int H, int elems, bool rev, cudaStream_t st);
 cudaError_t launch_decode(bool bf16, int dk, int dv, const void *q, const void *k, const void *v, const void *g,
                           void *out, float *state, long nh, int H, int rep, int g_per_head, float scale, int sms,
@@ -93,7 +94,12 @@ struct Windows {
 // Windows of a multiple of 64 tokens, as many as fill two CTAs per SM once.
 // A call with more than one window also runs the summary pass (about 0.6 of
 // the time of the main one) and the scan, so short calls stay in one.
-Windows choose_windows(int T, int H) {
+Windows choose_windows(int T, int H, bool tc) {
+    if (tc) {  // one CTA per SM, windows of whole 128-token chunks
+        const long target = std::max(1L, (long)sm_count() / H);
+        const long win = std::max(128L, ((T + target - 1) / target + 127) / 128 * 128);
+        return {(int)win, std::max(1, (int)((T + win - 1) / win))};
+    }
     const long slots = 2L * sm_count();
     const long target = std::max(1L, slots / H);
     long win = ((T + target - 1) / target + 63) / 64 * 64;
@@ -102,13 +108,17 @@ Windows choose_windows(int T, int H) {
     return {(int)win, std::max(1, (int)((T + win - 1) / win))};
 }
 
+// bf16 on the tensor cores, fp32 token by token
+bool use_tc(kda_dtype dtype, int T) { return dtype == KDA_DTYPE_BF16 && T > 0; }
+
 struct FwdLayout {
-    size_t gamma, z, start, total;
+    size_t header, gamma, z, start, total;
 };
 FwdLayout fwd_layout(const Windows &wd, int H, int dk, int dv) {
     FwdLayout L;
     const size_t states = (size_t)wd.W * H * dk * dv * sizeof(float);
     size_t o = 0;
+    L.header = o; o = align256(o + 64 * sizeof(int32_t));
     L.gamma = o; o = align256(o + (size_t)wd.W * H * sizeof(float));
     L.z = o;     o = align256(o + states);
     L.start = o; o = align256(o + states);
@@ -174,7 +184,7 @@ extern "C" {
 size_t kda_lin_chunk_fwd_workspace_size(int32_t total_tokens, int32_t num_seqs, int32_t H, int32_t Hk, int32_t dk,
                                         int32_t dv, kda_dtype dtype) {
     if (check_sizes(num_seqs, total_tokens, H, Hk, dk, dv, dtype, 0) != KDA_OK) return 0;
-    return fwd_layout(choose_windows(total_tokens, H), H, dk, dv).total;
+    return fwd_layout(choose_windows(total_tokens, H, use_tc(dtype, total_tokens)), H, dk, dv).total;
 }
 
 int kda_lin_chunk_fwd(const void *q, const void *k, const void *v, const void *g, void *out, const int32_t *cu_seqlens,
@@ -193,7 +203,8 @@ int kda_lin_chunk_fwd(const void *q, const void *k, const void *v, const void *g
     const bool in_place = initial_state && initial_state == final_state;
     if (!in_place && overlap(initial_state, final_state, (size_t)num_seqs * H * dk * dv * sizeof(float)))
         return KDA_ERR_INVALID_ARG;
-    const Windows wd = choose_windows(total_tokens, H);
+    const bool tc = use_tc(dtype, total_tokens);
+    const Windows wd = choose_windows(total_tokens, H, tc);
     const FwdLayout L = fwd_layout(wd, H, dk, dv);
     if (!workspace || workspace_bytes < L.total) return KDA_ERR_WORKSPACE;
     char *ws = (char *)workspace;
@@ -212,11 +223,15 @@ int kda_lin_chunk_fwd(const void *q, const void *k, const void *v, const void *g
     p.gamma = (float *)(ws + L.gamma);
     p.win_state = (float *)(ws + L.z);
     p.start_copy = in_place && wd.W > 1 ? (float *)(ws + L.start) : nullptr;
+    p.err = (int32_t *)(ws + L.header);
+    auto pass = [&](int mode) {
+        return ok(tc ? kda::lin::launch_tc(p, mode, dk, dv, st) : kda::lin::launch_rec(p, mode, bf16, dk, dv, st));
+    };
     if (wd.W > 1) {
-        if (!ok(kda::lin::launch_rec(p, kda::lin::kSum, bf16, dk, dv, st))) return KDA_ERR_CUDA;
+        if (!pass(kda::lin::kSum)) return KDA_ERR_CUDA;
         if (!ok(kda::lin::launch_scan(p.win_state, p.gamma, wd.W, H, dk * dv, false, st))) return KDA_ERR_CUDA;
     }
-    return ok(kda::lin::launch_rec(p, kda::lin::kFwd, bf16, dk, dv, st)) ? KDA_OK : KDA_ERR_CUDA;
+    return pass(kda::lin::kFwd) ? KDA_OK : KDA_ERR_CUDA;
 }
 
 int kda_lin_decode_step(const void *q, const void *k, const void *v, const void *g, void *out, float *state,
@@ -242,7 +257,7 @@ int kda_lin_decode_step(const void *q, const void *k, const void *v, const void 
 size_t kda_lin_bwd_workspace_size(int32_t total_tokens, int32_t num_seqs, int32_t H, int32_t Hk, int32_t dk,
                                   int32_t dv) {
     if (check_sizes(num_seqs, total_tokens, H, Hk, dk, dv, KDA_DTYPE_F32, 0) != KDA_OK) return 0;
-    return bwd_layout(choose_windows(total_tokens, H), total_tokens, num_seqs, H, Hk, dk, dv).total;
+    return bwd_layout(choose_windows(total_tokens, H, false), total_tokens, num_seqs, H, Hk, dk, dv).total;
 }
 
 int kda_lin_bwd(const void *q, const void *k, const void *v, const void *g, const void *dy, const int32_t *cu_seqlens,
@@ -265,7 +280,7 @@ int kda_lin_bwd(const void *q, const void *k, const void *v, const void *g, cons
     const size_t state_bytes = (size_t)num_seqs * H * dk * dv * sizeof(float);
     if (overlap(initial_state, d_initial_state, state_bytes) || overlap(d_final_state, d_initial_state, state_bytes))
         return KDA_ERR_INVALID_ARG;
-    const Windows wd = choose_windows(total_tokens, H);
+    const Windows wd = choose_windows(total_tokens, H, false);
     const BwdLayout L = bwd_layout(wd, total_tokens, num_seqs, H, Hk, dk, dv);
     if (!workspace || workspace_bytes < L.total) return KDA_ERR_WORKSPACE;
     char *ws = (char *)workspace;

@@ -1,0 +1,742 @@
+// Linear attention with one decay per head on the 5th-generation tensor
+// cores: bf16 inputs, chunks of 128 tokens.
+//
+// One CTA runs the tokens of one (window, head) (kda_lin.cuh), chunk after
+// chunk.  With c_t the log-decay summed from the chunk's first token to t,
+// D[t][s] = exp(c_t - c_s) for s <= t and w_s = exp(c_last - c_s), a chunk is
+//   A   = R W^T                  R: the read vectors (q), W: the write vectors (k)
+//   P   = scale D (.) A          fp32 from TMEM, rounded to bf16 once, back to TMEM
+//   O1  = R S                    S: bf16 copy of the state entering the chunk
+//   O   = scale exp(c_t) O1 + P V
+//   S   = exp(c_last) S + W^T (w V)
+// The state stays in TMEM in fp32 for the whole window.  w V is split into two
+// bf16 parts (hi + lo, 2^-16 of the value), so the state that is carried and
+// returned has fp32-like accuracy; only the copy that R reads is one bf16.
+// Reversed passes (the gradient) keep the tokens in their rows and flip the
+// triangle: c_t is then summed from the chunk's last token back to t.
+//
+// The decays are never formed as exp(-c): between two 32-token blocks they
+// factor into exp(c_t - c_block end) * exp(c_block end - c_s), both at most 1,
+// one exponential per row and block; only the diagonal blocks need one per
+// element.
+//
+// What bounds it: at 128 x 128 a chunk moves 128 KB through HBM, 3.0 us of one
+// SM's share at 6.5 TB/s, against five 128^3 products (about 2600 tensor-pipe
+// cycles, 1.4 us).  So the chunk's serial chains have to stay hidden: every
+// step has its own warpgroup, one chunk apart at most, joined by mbarriers:
+//   warps  0- 3  P    the decayed products           (TMEM lane = token)
+//   warps  4- 7  S    the state: scaled in TMEM, bf16 copy to shared memory
+//   warps  8-11  V    w V as hi and lo halves, 64 tokens at a time
+//   warps 12-15  O    the outputs                    (TMEM lane = token)
+//   warp  16     TMA  tiles of 128 tokens x 64 channels, 128-byte swizzle
+//   warp  17     MMA  issues every product
+// Shared memory (128 x 128): W and V tiles twice (128 KB), R, the hi/lo halves
+// and the state copy (32 KB each).
+//
+// Every wait is bounded (2 s): one that gives up marks the workspace's error
+// word and the CTA, whose remaining waits then return at once; the loads and
+// products in flight are waited for before TMEM is released.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include "kda_common.cuh"
+#include "kda_lin.cuh"
+#include "kda_sm100.cuh"
+
+namespace kda {
+namespace lin {
+namespace tc {
+
+using namespace sm100;
+
+constexpr int kC = 128;             // tokens per chunk
+constexpr int kBox = 64 * kC * 2;   // bytes of one TMA box: 64 channels x 128 tokens
+constexpr int kWarps = 18;
+constexpr int kThreads = 32 * kWarps;
+constexpr float kLog2e = 1.4426950408889634f;
+
+enum Mode { FWD, SUM, SUMR, DQ, DK, DV };
+
+struct Maps {
+    CUtensorMap rd, wr, val;
+};
+
+template <int DA, int DB, int M>
+struct Cfg {
+    static constexpr bool rev = M == SUMR || M == DK || M == DV;
+    static constexpr bool sum = M == SUM || M == SUMR;
+    static constexpr bool out = !sum;
+    static constexpr int stages = sum ? 3 : 2;
+    static constexpr int wr_bytes = DA / 64 * kBox, val_bytes = DB / 64 * kBox;
+    static constexpr int stage_bytes = wr_bytes + val_bytes;
+    static constexpr int rd_bytes = out ? wr_bytes : 0;
+    static constexpr int vb_part = DB / 64 * (64 * 64 * 2);  // 64 tokens of hi or lo
+    static constexpr int sb_bytes = out ? DB / 64 * (DA * 128) : 0;
+    static constexpr int off_rd = stages * stage_bytes;
+    static constexpr int off_vb = off_rd + rd_bytes;
+    static constexpr int off_sb = off_vb + 2 * vb_part;
+    static constexpr int off_ctl = off_sb + sb_bytes;
+    // TMEM columns
+    static constexpr uint32_t col_s = 0, col_a = 128, col_o1 = 256, col_o2 = 384;
+    static constexpr uint32_t cols = out ? 512 : 128;
+};
+
+struct Ctl {
+    unsigned long long full[3], free[3];  // the stages of W and V
+    unsigned long long rd_full, rd_free;  // R; rd_free also releases the state copy
+    unsigned long long a_full;            // A is in TMEM
+    unsigned long long p_full;            // P is in TMEM
+    unsigned long long s_full;            // the scaled state and its copy are in place
+    unsigned long long vb_full, vb_free;  // the hi/lo half
+    unsigned long long kv_done;           // the state has this chunk's writes
+    unsigned long long pv_done;           // O1 and O2 are complete
+    unsigned long long o_free;            // O1 and O2 have been read
+    unsigned long long clean;             // rows behind a short chunk's end are zero
+    unsigned long long end;
+    int dead;
+    uint32_t tmem;
+    alignas(16) float pc[2][kC], pe[2][kC];
+    float pt[2][4];                         // P: c within the 32-token block, exp(to the block's far end); block sums
+    float vw[kC], vt[2][4];                // V: w_s, block sums
+    float ot[2][4];                        // O: block sums
+};
+
+// 32 bytes of one row: one whole sector when the address allows it
+KDA_DEVICE void st_global32(void *p, const uint32_t (&r)[8], bool aligned32) {
+    if (!aligned32) {
+        reinterpret_cast<uint4 *>(p)[0] = make_uint4(r[0], r[1], r[2], r[3]);
+        reinterpret_cast<uint4 *>(p)[1] = make_uint4(r[4], r[5], r[6], r[7]);
+        return;
+    }
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+                 "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+KDA_DEVICE float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// inclusive scans over the lanes of a warp
+KDA_DEVICE float scan_up(float x, int lane) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const float y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    return x;
+}
+KDA_DEVICE float scan_down(float x, int lane) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const float y = __shfl_down_sync(0xffffffffu, x, o);
+        if (lane + o < 32) x += y;
+    }
+    return x;
+}
+
+template <int DA, int DB, int M>
+__global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__ Params p,
+                                                         const __grid_constant__ Maps maps) {
+    using C = Cfg<DA, DB, M>;
+    extern __shared__ __align__(1024) unsigned char sm[];  // the swizzle's period
+    Ctl &ctl = *reinterpret_cast<Ctl *>(sm + C::off_ctl);
+    const uint32_t sbase = smem_u32(sm);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, role = warp >> 2;
+    const int h = blockIdx.x, w = blockIdx.y, H = p.H, N = p.num_seqs;
+    const int t0 = w * p.win, t1 = min(p.T, t0 + p.win);
+    volatile int *dead = &ctl.dead;
+
+    if (h == 0 && w == 0 && tid < 3 && p.err) p.err[tid] = 0;
+
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ctl.tmem)),
+                     "r"(C::cols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    if (tid == 32) {
+        for (int i = 0; i < 3; ++i) {
+            mbar_init(smem_u32(&ctl.full[i]), 1);
+            mbar_init(smem_u32(&ctl.free[i]), 1);
+        }
+        unsigned long long *one[] = {&ctl.rd_full, &ctl.rd_free, &ctl.a_full, &ctl.vb_free, &ctl.kv_done, &ctl.pv_done, &ctl.end};
+        unsigned long long *wg[] = {&ctl.p_full, &ctl.s_full, &ctl.vb_full, &ctl.o_free, &ctl.clean};
+        for (auto *b : one) mbar_init(smem_u32(b), 1);
+        for (auto *b : wg) mbar_init(smem_u32(b), 128);
+        ctl.dead = (sbase & 1023u) != 0;  // never: the tiles would be read wrongly
+        if (ctl.dead && p.err) atomicOr(p.err + 2, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = ctl.tmem;
+
+    auto wait = [&](unsigned long long &bar, uint32_t parity) {
+        if (*dead) return;
+        if (!mbar_wait(smem_u32(&bar), parity)) {
+            *dead = 1;
+            if (p.err) atomicOr(p.err + 2, 1);
+        }
+    };
+    auto arrive = [&](unsigned long long &bar) { mbar_arrive(smem_u32(&bar)); };
+    auto load_g = [&](int t) -> float {  // in powers of two
+        const size_t at = p.g_per_head ? (size_t)h : (size_t)t * H + h;
+        return fmaxf(__bfloat162float(((const bf16 *)p.g)[at]), kMinG) * kLog2e;
+    };
+    // the decay that row `row` of the chunk of `rows` tokens at `base` multiplies the running state with
+    auto row_g = [&](int base, int rows, int row, int qb) -> float {
+        if (row >= rows) return 0.f;
+        const int t = base + row;
+        if (C::rev) return t + 1 < qb ? load_g(t + 1) : 0.f;
+        return load_g(t);
+    };
+
+    // first sequence that starts at or behind x
+    auto lower = [&](int x) {
+        int lo = 0, hi = N;
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (p.cu[mid] < x) lo = mid + 1;
+            else hi = mid;
+        }
+        return lo;
+    };
+    const int lo = lower(t0);
+    int first, end;
+    if (C::sum) {  // the sequence that crosses the window's outgoing edge, if any
+        int n;
+        if (!C::rev) {
+            n = t1 < p.T ? lower(t1) - 1 : -1;
+            if (n >= 0 && p.cu[n + 1] <= t1) n = -1;
+        } else {
+            n = t0 > 0 ? lo - 1 : -1;
+            if (n >= 0 && p.cu[n + 1] <= t0) n = -1;
+        }
+        first = n < 0 ? 0 : n;
+        end = n < 0 ? 0 : n + 1;
+        if (n < 0 && tid == 0) p.gamma[(size_t)w * H + h] = kNoCarry;
+    } else {
+        first = lo > 0 && p.cu[lo] > t0 ? lo - 1 : lo;
+        end = w == p.W - 1 ? N : lower(t1);
+    }
+
+    // f(n, a, b, qb): tokens [a, b) of sequence n, which ends at qb, in the order of the pass
+    auto segments = [&](auto f) {
+        for (int i = first; i < end; ++i) {
+            const int n = C::rev ? end - 1 - (i - first) : i;
+            const int qa = p.cu[n], qb = min(p.cu[n + 1], p.T);
+            const int a = min(max(qa, t0), t1), b = max(a, min(qb, t1));
+            f(n, a, b, qa, qb);
+        }
+    };
+    // f(base, rows): its chunks
+    auto chunks = [&](int a, int b, auto f) {
+        const int nch = (b - a + kC - 1) / kC;
+        for (int i = 0; i < nch; ++i) {
+            const int base = a + (C::rev ? nch - 1 - i : i) * kC;
+            f(base, min(kC, b - base), i, nch);
+        }
+    };
+    auto next_base = [&](int base) { return C::rev ? base - kC : base + kC; };
+
+    int it = 0;  // chunks done by this role
+    if (role == 0) {
+        // --------------------------------------------------------------- P
+        if (C::out) {
+            const int row = tid;  // 32 * warp + lane
+            const uint32_t ta = tmem + ((uint32_t)(32 * warp) << 16) + C::col_a;
+            const float sc = p.rd_scale * p.wr_scale;
+            segments([&](int n, int a, int b, int qa, int qb) {
+                float gx = 0.f;
+                chunks(a, b, [&](int base, int rows, int i, int nch) {
+                    if (i == 0) gx = row_g(base, rows, row, qb);
+                    const int pb = it & 1;
+                    const float c = C::rev ? scan_down(gx, lane) : scan_up(gx, lane);
+                    const float tot = __shfl_sync(0xffffffffu, c, C::rev ? 0 : 31);
+                    ctl.pc[pb][row] = c;
+                    ctl.pe[pb][row] = exp2f(tot - c);
+                    if (lane == 0) ctl.pt[pb][warp] = tot;
+                    if (i + 1 < nch) gx = row_g(next_base(base), min(kC, b - next_base(base)), row, qb);
+                    bar_sync(1, 128);
+                    wait(ctl.a_full, it & 1);
+                    tc_fence_after();
+                    // block by block upwards: P's block lies in columns 16 blk .. + 15, which hold products of
+                    // block blk / 2, read by then or not needed by this warp
+#pragma unroll 1
+                    for (int blk = 0; blk < 4; ++blk) {
+                        uint32_t pk[16];
+                        if (C::rev ? blk < warp : blk > warp) {
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) pk[e] = 0u;
+                        } else {
+                            uint32_t r[32];
+                            tmem_ld32_wait(ta + 32 * blk, r);
+                            if (blk == warp) {
+#pragma unroll
+                                for (int e4 = 0; e4 < 8; ++e4) {
+                                    const float4 cs = *reinterpret_cast<const float4 *>(&ctl.pc[pb][32 * blk + 4 * e4]);
+                                    const float cc[4] = {cs.x, cs.y, cs.z, cs.w};
+                                    float v[4];
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) {
+                                        const int s = 4 * e4 + e;
+                                        const bool on = C::rev ? s >= lane : s <= lane;
+                                        v[e] = on ? __uint_as_float(r[s]) * (exp2_fast(c - cc[e]) * sc) : 0.f;
+                                    }
+                                    pk[2 * e4] = pack_bf16(v[0], v[1]);
+                                    pk[2 * e4 + 1] = pack_bf16(v[2], v[3]);
+                                }
+                            } else {
+                                float far = c;  // + the blocks between
+                                for (int j = min(blk, warp) + 1; j < max(blk, warp); ++j) far += ctl.pt[pb][j];
+                                const float f = exp2f(far) * sc;
+                                const float2 f2 = make_float2(f, f);
+#pragma unroll
+                                for (int e4 = 0; e4 < 8; ++e4) {
+                                    const float4 es = *reinterpret_cast<const float4 *>(&ctl.pe[pb][32 * blk + 4 * e4]);
+                                    pk[2 * e4] = pack_bf16(f2mul(f2mul(make_float2(es.x, es.y), f2),
+                                                                 make_float2(__uint_as_float(r[4 * e4]), __uint_as_float(r[4 * e4 + 1]))));
+                                    pk[2 * e4 + 1] = pack_bf16(f2mul(f2mul(make_float2(es.z, es.w), f2),
+                                                                     make_float2(__uint_as_float(r[4 * e4 + 2]), __uint_as_float(r[4 * e4 + 3]))));
+                                }
+                            }
+                        }
+                        tmem_st16(ta + 16 * blk, pk);
+                    }
+                    tc_wait_st();
+                    tc_fence_before();
+                    arrive(ctl.p_full);
+                    ++it;
+                });
+            });
+        }
+    } else if (role == 1) {
+        // --------------------------------------------------------------- S
+        const int row = tid - 128, wl = warp & 3;
+        const uint32_t ts = tmem + ((uint32_t)(32 * wl) << 16) + C::col_s;
+        const bool mine = row < DA;
+        float gamma = 1.f;
+        segments([&](int n, int a, int b, int qa, int qb) {
+            const bool from_win = C::rev ? p.cu[n + 1] > t1 : n < lo;
+            const bool ends = C::rev ? n >= lo : p.cu[n + 1] <= t1;
+            const size_t win_at = ((size_t)w * H + h) * (DA * DB), seq_at = ((size_t)n * H + h) * (DA * DB);
+            const float *src;
+            bool src_t = false;
+            if (C::sum) {
+                src = from_win ? nullptr : p.init ? p.init + seq_at : nullptr;
+                src_t = p.init_t;
+            } else if (from_win) {
+                src = p.win_state + win_at;
+                src_t = p.win_t;
+            } else if (p.start_copy && p.cu[n + 1] > t1) {
+                src = p.start_copy + win_at;
+            } else {
+                src = p.init ? p.init + seq_at : nullptr;
+                src_t = p.init_t;
+            }
+            // 32 columns of this thread's row of the state before the chunk
+            auto load32 = [&](int cb, bool from_src, uint32_t (&r)[32]) {
+                if (!from_src) {
+                    tmem_ld32_wait(ts + 32 * cb, r);
+                } else if (!src || !mine) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) r[e] = 0u;
+                } else if (!src_t) {
+#pragma unroll
+                    for (int e4 = 0; e4 < 8; ++e4) {
+                        const uint4 v = *reinterpret_cast<const uint4 *>(src + (size_t)row * DB + 32 * cb + 4 * e4);
+                        r[4 * e4] = v.x; r[4 * e4 + 1] = v.y; r[4 * e4 + 2] = v.z; r[4 * e4 + 3] = v.w;
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(src[(size_t)(32 * cb + e) * DA + row]);
+                }
+            };
+            float gx[4] = {0.f, 0.f, 0.f, 0.f};
+            chunks(a, b, [&](int base, int rows, int i, int nch) {
+                if (i == 0)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) gx[x] = row_g(base, rows, 32 * x + lane, qb);
+                const float f = exp2f(warp_sum((gx[0] + gx[1]) + (gx[2] + gx[3])));
+                gamma *= f;
+                if (i + 1 < nch)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) gx[x] = row_g(next_base(base), min(kC, b - next_base(base)), 32 * x + lane, qb);
+                if (i > 0) {
+                    wait(ctl.kv_done, (it - 1) & 1);
+                    tc_fence_after();
+                }
+                if (mine) {
+#pragma unroll 1
+                    for (int cb = 0; cb < DB / 32; ++cb) {
+                        uint32_t r[32];
+                        load32(cb, i == 0, r);
+                        if (C::sum && i == 0 && p.start_copy && !from_win) {
+                            float *dst = p.start_copy + win_at + (size_t)row * DB + 32 * cb;
+#pragma unroll
+                            for (int e4 = 0; e4 < 8; ++e4)
+                                reinterpret_cast<uint4 *>(dst)[e4] = make_uint4(r[4 * e4], r[4 * e4 + 1], r[4 * e4 + 2], r[4 * e4 + 3]);
+                        }
+                        if (C::out) {  // the copy that R reads: [DA rows][64 channels] boxes, 128-byte swizzle
+                            unsigned char *box = sm + C::off_sb + (cb >> 1) * (DA * 128) + row * 128;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                uint4 v;
+                                v.x = pack_bf16(__uint_as_float(r[8 * e]), __uint_as_float(r[8 * e + 1]));
+                                v.y = pack_bf16(__uint_as_float(r[8 * e + 2]), __uint_as_float(r[8 * e + 3]));
+                                v.z = pack_bf16(__uint_as_float(r[8 * e + 4]), __uint_as_float(r[8 * e + 5]));
+                                v.w = pack_bf16(__uint_as_float(r[8 * e + 6]), __uint_as_float(r[8 * e + 7]));
+                                *reinterpret_cast<uint4 *>(box + ((((cb & 1) * 4 + e) ^ (row & 7)) << 4)) = v;
+                            }
+                        }
+                        const float2 f2 = make_float2(f, f);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const float2 v = f2mul(make_float2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])), f2);
+                            r[2 * e] = __float_as_uint(v.x);
+                            r[2 * e + 1] = __float_as_uint(v.y);
+                        }
+                        tmem_st32(ts + 32 * cb, r);
+                    }
+                    tc_wait_st();
+                }
+                if (C::out) fence_async_smem();
+                tc_fence_before();
+                arrive(ctl.s_full);
+                ++it;
+            });
+            // the state behind the segment
+            float *dst = C::sum ? p.win_state + win_at : ends && p.final_state ? p.final_state + seq_at : nullptr;
+            const bool dst_t = !C::sum && p.init_t;
+            if (b > a) {
+                wait(ctl.kv_done, (it - 1) & 1);
+                tc_fence_after();
+            }
+            if (dst && mine) {
+                const float f = !C::sum && C::rev && b > a ? exp2f(load_g(a)) : 1.f;
+#pragma unroll 1
+                for (int cb = 0; cb < DB / 32; ++cb) {
+                    uint32_t r[32];
+                    load32(cb, b == a, r);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
+                    if (!dst_t) {
+#pragma unroll
+                        for (int e4 = 0; e4 < 8; ++e4)
+                            *reinterpret_cast<uint4 *>(dst + (size_t)row * DB + 32 * cb + 4 * e4) =
+                                make_uint4(r[4 * e4], r[4 * e4 + 1], r[4 * e4 + 2], r[4 * e4 + 3]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) dst[(size_t)(32 * cb + e) * DA + row] = __uint_as_float(r[e]);
+                    }
+                }
+            }
+            if (C::sum && row == 0) p.gamma[(size_t)w * H + h] = from_win ? gamma : 0.f;
+        });
+        tc_fence_before();
+    } else if (role == 2) {
+        // --------------------------------------------------------------- V
+        const int vt = tid - 256, wl = warp & 3;
+        const int vrow = vt & 63, vhalf = vt >> 6;
+        int halves = 0;
+        segments([&](int n, int a, int b, int qa, int qb) {
+            float gx = 0.f;
+            chunks(a, b, [&](int base, int rows, int i, int nch) {
+                if (i == 0) gx = row_g(base, rows, vt, qb);
+                const int pb = it & 1, st = it % C::stages;
+                // the decays behind this row, in the order of the pass
+                const float inc = C::rev ? scan_up(gx, lane) : scan_down(gx, lane);
+                float exc = C::rev ? __shfl_up_sync(0xffffffffu, inc, 1) : __shfl_down_sync(0xffffffffu, inc, 1);
+                if (lane == (C::rev ? 0 : 31)) exc = 0.f;
+                if (lane == (C::rev ? 31 : 0)) ctl.vt[pb][wl] = inc;
+                if (i + 1 < nch) gx = row_g(next_base(base), min(kC, b - next_base(base)), vt, qb);
+                bar_sync(2, 128);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (C::rev ? j < wl : j > wl) exc += ctl.vt[pb][j];
+                ctl.vw[vt] = exp2f(exc) * p.wr_scale;
+                wait(ctl.full[st], (it / C::stages) & 1);
+                unsigned char *tw = sm + st * C::stage_bytes, *tv = tw + C::wr_bytes;
+                if (rows < kC) {
+                    // the MMA warp has passed the short chunk before this one
+                    if (halves > 0) wait(ctl.vb_free, (halves - 1) & 1);
+                    // rows behind the end hold other tokens: zero, whatever they are
+                    if (vt >= rows) {
+                        const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+                        for (int c = 0; c < (DA + DB) / 8; ++c)
+                            *reinterpret_cast<uint4 *>(tw + (c >> 3) * kBox + vt * 128 + (c & 7) * 16) = z;
+                    }
+                    fence_async_smem();
+                    arrive(ctl.clean);
+                }
+                bar_sync(2, 128);  // vw, and the zeros
+                for (int hh = 0; hh < (rows > 64 ? 2 : 1); ++hh) {
+                    if (halves > 0) wait(ctl.vb_free, (halves - 1) & 1);
+                    const float f = ctl.vw[64 * hh + vrow];
+                    constexpr int CH = DB / 16;  // 16-byte pieces of this thread: its half of the channels
+#pragma unroll
+                    for (int c0 = 0; c0 < CH; ++c0) {
+                        const int c = vhalf * CH + c0, box = c >> 3, cc = c & 7, r = 64 * hh + vrow;
+                        const uint4 x = *reinterpret_cast<const uint4 *>(tv + box * kBox + r * 128 + ((cc ^ (r & 7)) << 4));
+                        const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+                        uint32_t hi[4], lw[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 v = f2mul(unpack_bf16(xs[e]), make_float2(f, f));
+                            hi[e] = pack_bf16(v);
+                            const float2 k2 = unpack_bf16(hi[e]);
+                            lw[e] = pack_bf16(v.x - k2.x, v.y - k2.y);
+                        }
+                        unsigned char *dst = sm + C::off_vb + box * 8192 + vrow * 128 + ((cc ^ (vrow & 7)) << 4);
+                        *reinterpret_cast<uint4 *>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        *reinterpret_cast<uint4 *>(dst + C::vb_part) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+                    }
+                    fence_async_smem();
+                    arrive(ctl.vb_full);
+                    ++halves;
+                }
+                ++it;
+            });
+        });
+    } else if (role == 3) {
+        // --------------------------------------------------------------- O
+        if (C::out) {
+            const int row = tid - 384, wl = warp & 3;
+            const uint32_t lane_off = (uint32_t)(32 * wl) << 16;
+            const bool al32 = ((uintptr_t)p.out & 31) == 0;
+            const uint32_t to1 = tmem + lane_off + C::col_o1, to2 = tmem + lane_off + C::col_o2;
+            segments([&](int n, int a, int b, int qa, int qb) {
+                float gx = 0.f;
+                chunks(a, b, [&](int base, int rows, int i, int nch) {
+                    if (i == 0) gx = row_g(base, rows, row, qb);
+                    const int pb = it & 1;
+                    float c = C::rev ? scan_down(gx, lane) : scan_up(gx, lane);
+                    if (lane == (C::rev ? 0 : 31)) ctl.ot[pb][wl] = c;
+                    if (i + 1 < nch) gx = row_g(next_base(base), min(kC, b - next_base(base)), row, qb);
+                    bar_sync(3, 128);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (C::rev ? j > wl : j < wl) c += ctl.ot[pb][j];
+                    const float f = exp2f(c) * p.rd_scale;
+                    wait(ctl.pv_done, it & 1);
+                    tc_fence_after();
+                    bf16 *dst = (bf16 *)p.out + ((size_t)(base + row) * H + h) * DB;
+#pragma unroll 1
+                    for (int cb = 0; cb < DB / 32; ++cb) {
+                        uint32_t x[32], y[32];
+                        tmem_ld32(to1 + 32 * cb, x);
+                        tmem_ld32_wait(to2 + 32 * cb, y);
+                        if (cb == DB / 32 - 1) {
+                            tc_fence_before();
+                            arrive(ctl.o_free);
+                        }
+                        if (row < rows) {
+#pragma unroll
+                            for (int q = 0; q < 2; ++q) {
+                                uint32_t v[8];
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) {
+                                    const int k = 16 * q + 2 * e;
+                                    v[e] = pack_bf16(f2fma(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])),
+                                                           make_float2(f, f),
+                                                           make_float2(__uint_as_float(y[k]), __uint_as_float(y[k + 1]))));
+                                }
+                                st_global32(dst + 32 * cb + 16 * q, v, al32);
+                            }
+                        }
+                    }
+                    ++it;
+                });
+            });
+        }
+    } else if (warp == 16) {
+        // --------------------------------------------------------------- TMA
+        const int hr = C::out ? h / p.rd_div : 0, hw = h / p.wr_div, hv = h / p.val_div;
+        segments([&](int n, int a, int b, int qa, int qb) {
+            chunks(a, b, [&](int base, int rows, int i, int nch) {
+                const int st = it % C::stages;
+                if (it >= C::stages) wait(ctl.free[st], (it / C::stages - 1) & 1);
+                if (elect_one_sync() && !*dead) {
+                    const uint32_t bar = smem_u32(&ctl.full[st]), dst = sbase + st * C::stage_bytes;
+                    mbar_arrive_expect_tx(bar, C::stage_bytes);
+#pragma unroll
+                    for (int x = 0; x < DA / 64; ++x) tma_load_3d(dst + x * kBox, &maps.wr, 64 * x, hw, base, bar);
+#pragma unroll
+                    for (int x = 0; x < DB / 64; ++x)
+                        tma_load_3d(dst + C::wr_bytes + x * kBox, &maps.val, 64 * x, hv, base, bar);
+                }
+                __syncwarp();
+                if (C::out) {
+                    if (it > 0) wait(ctl.rd_free, (it - 1) & 1);
+                    if (elect_one_sync() && !*dead) {
+                        const uint32_t bar = smem_u32(&ctl.rd_full);
+                        mbar_arrive_expect_tx(bar, C::rd_bytes);
+#pragma unroll
+                        for (int x = 0; x < DA / 64; ++x) {
+                            tma_load_3d(sbase + C::off_rd + x * kBox, &maps.rd, 64 * x, hr, base, bar);
+                            if (i + 1 < nch) tma_prefetch_3d(&maps.rd, 64 * x, hr, next_base(base));
+                        }
+                    }
+                    __syncwarp();
+                }
+                ++it;
+            });
+        });
+        if (*dead) {  // loads in flight land before the CTA ends (bounded)
+            for (int x = max(0, it - C::stages); x < it; ++x)
+                mbar_wait(smem_u32(&ctl.full[x % C::stages]), (x / C::stages) & 1);
+            if (C::out && it > 0) mbar_wait(smem_u32(&ctl.rd_full), (it - 1) & 1);
+        }
+    } else {
+        // --------------------------------------------------------------- MMA
+        constexpr uint32_t ID_A = idesc_bf16(128, 128, 0, 0);  // R (K-major) x W (K-major)
+        constexpr uint32_t ID_O1 = idesc_bf16(128, DB, 0, 1);  // R (K-major) x S (MN-major)
+        constexpr uint32_t ID_KV = idesc_bf16(128, DB, 1, 1);  // W^T (MN-major) x w V (MN-major)
+        constexpr uint32_t ID_PV = idesc_bf16(128, DB, 0, 1);  // P (TMEM) x V (MN-major)
+        int halves = 0, cleans = 0;
+        segments([&](int n, int a, int b, int qa, int qb) {
+            chunks(a, b, [&](int base, int rows, int i, int nch) {
+                const int st = it % C::stages;
+                const uint32_t tw = sbase + st * C::stage_bytes, tv = tw + C::wr_bytes, tr = sbase + C::off_rd;
+                wait(ctl.full[st], (it / C::stages) & 1);
+                if (C::out) wait(ctl.rd_full, it & 1);
+                if (rows < kC) {
+                    wait(ctl.clean, cleans & 1);
+                    ++cleans;
+                }
+                if (C::out) {
+                    if (it > 0) wait(ctl.pv_done, (it - 1) & 1);  // P's columns are A's
+                    tc_fence_after();
+                    if (elect_one_sync() && !*dead) {
+#pragma unroll
+                        for (int kk = 0; kk < DA / 16; ++kk) {
+                            const uint32_t off = (kk >> 2) * kBox + (kk & 3) * 32;
+                            tc_mma_ss(tmem + C::col_a, sdesc_sw128(tr + off, 16, 1024), sdesc_sw128(tw + off, 16, 1024), ID_A,
+                                      kk > 0);
+                        }
+                        tc_commit(smem_u32(&ctl.a_full));
+                    }
+                    __syncwarp();
+                }
+                wait(ctl.s_full, it & 1);
+                if (C::out) {
+                    if (it > 0) wait(ctl.o_free, (it - 1) & 1);
+                    tc_fence_after();
+                    if (elect_one_sync() && !*dead) {
+#pragma unroll
+                        for (int kk = 0; kk < DA / 16; ++kk)
+                            tc_mma_ss(tmem + C::col_o1, sdesc_sw128(tr + (kk >> 2) * kBox + (kk & 3) * 32, 16, 1024),
+                                      sdesc_sw128(sbase + C::off_sb + 2048 * kk, DA * 128, 1024), ID_O1, kk > 0);
+                        tc_commit(smem_u32(&ctl.rd_free));
+                    }
+                    __syncwarp();
+                }
+                const int nh = rows > 64 ? 2 : 1;
+                for (int hh = 0; hh < nh; ++hh) {
+                    wait(ctl.vb_full, halves & 1);
+                    tc_fence_after();
+                    if (elect_one_sync() && !*dead) {
+                        const uint32_t vb = sbase + C::off_vb;
+#pragma unroll
+                        for (int part = 0; part < 2; ++part)
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                tc_mma_ss(tmem + C::col_s, sdesc_sw128(tw + 8192 * hh + 2048 * kk, kBox, 1024),
+                                          sdesc_sw128(vb + part * C::vb_part + 2048 * kk, 8192, 1024), ID_KV, 1u);
+                        tc_commit(smem_u32(&ctl.vb_free));
+                        if (hh == nh - 1) {
+                            tc_commit(smem_u32(&ctl.kv_done));
+                            if (C::sum) tc_commit(smem_u32(&ctl.free[st]));
+                        }
+                    }
+                    __syncwarp();
+                    ++halves;
+                }
+                if (C::out) {
+                    wait(ctl.p_full, it & 1);
+                    tc_fence_after();
+                    if (elect_one_sync() && !*dead) {
+                        const int steps = (rows + 15) / 16;
+                        for (int kk = 0; kk < steps; ++kk)
+                            tc_mma_ts(tmem + C::col_o2, tmem + C::col_a + 8 * kk, sdesc_sw128(tv + 2048 * kk, kBox, 1024), ID_PV,
+                                      kk > 0);
+                        tc_commit(smem_u32(&ctl.pv_done));
+                        tc_commit(smem_u32(&ctl.free[st]));
+                    }
+                    __syncwarp();
+                }
+                ++it;
+            });
+        });
+        if (*dead) {  // the products in flight end before TMEM is released (bounded)
+            if (elect_one_sync()) tc_commit(smem_u32(&ctl.end));
+            __syncwarp();
+            mbar_wait(smem_u32(&ctl.end), 0);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::cols) : "memory");
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            return (PFN_cuTensorMapEncodeTiled_v12000) nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    }();
+    return fn;
+}
+
+// [T][Hx][D] bf16 as (channel, head, token); box 64 x 1 x 128.
+bool encode(CUtensorMap *m, const void *base, int T, int Hx, int D) {
+    const PFN_cuTensorMapEncodeTiled_v12000 enc = encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)Hx, (cuuint64_t)T};
+    const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)Hx * D * 2};
+    const cuuint32_t box[3] = {64, 1, kC};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int DA, int DB, int M>
+cudaError_t launch_t(const Params &p, cudaStream_t st) {
+    using C = Cfg<DA, DB, M>;
+    constexpr int bytes = C::off_ctl + (int)sizeof(Ctl);
+    static_assert(bytes <= 232448, "shared memory");
+    Maps maps;
+    if (!encode(&maps.wr, p.wr, p.T, p.H / p.wr_div, DA) || !encode(&maps.val, p.val, p.T, p.H / p.val_div, DB) ||
+        !encode(&maps.rd, C::out ? p.rd : p.wr, p.T, C::out ? p.H / p.rd_div : p.H / p.wr_div, DA))
+        return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(tc_kernel<DA, DB, M>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    tc_kernel<DA, DB, M><<<dim3(p.H, p.W), kThreads, bytes, st>>>(p, maps);
+    return cudaGetLastError();
+}
+template <int M>
+cudaError_t launch_m(const Params &p, int da, int db, cudaStream_t st) {
+    if (da == 128) return db == 128 ? launch_t<128, 128, M>(p, st) : launch_t<128, 64, M>(p, st);
+    return db == 128 ? launch_t<64, 128, M>(p, st) : launch_t<64, 64, M>(p, st);
+}
+
+}  // namespace tc
+
+// The bf16 passes (same modes as launch_rec); T > 0.
+cudaError_t launch_tc(const Params &p, int mode, int da, int db, cudaStream_t st) {
+    switch (mode) {
+        case tc::FWD: return tc::launch_m<tc::FWD>(p, da, db, st);
+        default: return tc::launch_m<tc::SUM>(p, da, db, st);
+    }
+}
+
+}  // namespace lin
+}  // namespace kda
