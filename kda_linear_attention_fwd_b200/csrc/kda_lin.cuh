@@ -59,7 +59,9 @@ struct Params {
     int32_t *err;           // [3] words of the workspace's header: [2] bit 0 = a bounded wait gave up
     // gradient passes
     float *xdot;            // [T][H]: q . dq, written by the dq pass, read by the dk pass
-    float *ckpt;            // [slots][H][DA][DB]: the state after each 64-token chunk
+    void *ckpt;             // [slots][H][DA][DB]: fp32 passes, the state after each 64-token chunk (fp32);
+                            // bf16 passes, the state before each 128-token chunk (bf16)
+    float *xstate, *across; // bf16 passes, [T][H]: see kda_lin_tc.cu
     void *dg;               // [T][H], input type, or fp32 when g_per_head
     int zero_first_dg;      // no initial state: d(first log-decay) is exactly 0
 };

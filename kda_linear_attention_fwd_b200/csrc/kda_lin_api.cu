@@ -19,11 +19,20 @@ cudaError_t launch_decode(bool bf16, int dk, int dv, const void *q, const void *
                           cudaStream_t st);
 enum { kFwd, kSum, kSumR, kDq, kDk, kDv };  // launch_rec's modes
 
+// The tokens of a packed call that lie in a sequence: [cu[0], cu[num_seqs]).
+struct Tokens {
+    const int32_t *cu;
+    int num_seqs, T;
+    KDA_DEVICE long first() const { return min(max(cu[0], 0), T); }
+    KDA_DEVICE long last() const { return min(max(cu[num_seqs], 0), T); }
+};
+
 // out[t][hk][i] = sum over r of in[t][hk * rep + r][i]: the gradient of a head
 // shared by rep heads, rounded once.  D a multiple of 4.
 template <typename T>
-__global__ void __launch_bounds__(256) head_sum_kernel(const float4 *in, T *out, long n4, int rep, int d4) {
-    for (long i = (long)blockIdx.x * 256 + threadIdx.x; i < n4; i += (long)gridDim.x * 256) {
+__global__ void __launch_bounds__(256) head_sum_kernel(const float4 *in, T *out, const Tokens tk, int Hk, int rep, int d4) {
+    const long row4 = (long)Hk * d4;
+    for (long i = tk.first() * row4 + (long)blockIdx.x * 256 + threadIdx.x; i < tk.last() * row4; i += (long)gridDim.x * 256) {
         const long th = i / d4, c = i % d4;
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int r = 0; r < rep; ++r) {
@@ -34,16 +43,23 @@ __global__ void __launch_bounds__(256) head_sum_kernel(const float4 *in, T *out,
     }
 }
 
-// Column sums of x [T][H] in two steps whose order is fixed: per block of
+// out = x + y, rounded
+template <typename T>
+__global__ void __launch_bounds__(256) add_kernel(const float *x, const float *y, T *out, const Tokens tk, int H) {
+    for (long i = tk.first() * H + (long)blockIdx.x * 256 + threadIdx.x; i < tk.last() * H; i += (long)gridDim.x * 256)
+        st(out + i, x[i] + y[i]);
+}
+
+// Column sums of x (+ y) [T][H] in two steps whose order is fixed: per block of
 // kSumRows rows, then over the blocks.
 constexpr int kSumRows = 512;
-__global__ void __launch_bounds__(256) token_sum_kernel(const float *x, float *part, int T, int H) {
+__global__ void __launch_bounds__(256) token_sum_kernel(const float *x, const float *y, float *part, const Tokens tk, int H) {
     __shared__ float s[8][33];
     const int hx = threadIdx.x & 31, ry = threadIdx.x >> 5, h = blockIdx.y * 32 + hx;
-    const int t0 = blockIdx.x * kSumRows, t1 = min(T, t0 + kSumRows);
+    const long b0 = (long)blockIdx.x * kSumRows, t0 = max(b0, tk.first()), t1 = min(b0 + kSumRows, tk.last());
     float a = 0.f;
     if (h < H)
-        for (int t = t0 + ry; t < t1; t += 8) a += x[(size_t)t * H + h];
+        for (long t = t0 + ry; t < t1; t += 8) a += x[t * H + h] + (y ? y[t * H + h] : 0.f);
     s[ry][hx] = a;
     __syncthreads();
     if (ry == 0 && h < H) {
@@ -127,19 +143,22 @@ FwdLayout fwd_layout(const Windows &wd, int H, int dk, int dv) {
 }
 
 struct BwdLayout {
-    size_t gamma_f, gamma_r, zf, zr, xdot, ckpt, dgt, part, dq, dk, total;
+    size_t header, gamma_f, gamma_r, zf, zr, xdot, xstate, across, ckpt, part, dq, dk, total;
 };
-BwdLayout bwd_layout(const Windows &wd, int T, int N, int H, int Hk, int dk, int dv) {
+BwdLayout bwd_layout(const Windows &wd, bool tc, int T, int N, int H, int Hk, int dk, int dv) {
     BwdLayout L;
     const size_t states = (size_t)wd.W * H * dk * dv * sizeof(float), th = (size_t)T * H * sizeof(float);
+    const size_t ckpt = tc ? ((size_t)T / 128 + N + 1) * sizeof(__nv_bfloat16) : ((size_t)T / 64 + N + 1) * sizeof(float);
     size_t o = 0;
+    L.header = o;  o = align256(o + 64 * sizeof(int32_t));
     L.gamma_f = o; o = align256(o + (size_t)wd.W * H * sizeof(float));
     L.gamma_r = o; o = align256(o + (size_t)wd.W * H * sizeof(float));
     L.zf = o;      o = align256(o + states);
     L.zr = o;      o = align256(o + states);
     L.xdot = o;    o = align256(o + th);
-    L.ckpt = o;    o = align256(o + ((size_t)T / 64 + N + 1) * H * dk * dv * sizeof(float));
-    L.dgt = o;     o = align256(o + th);
+    L.xstate = o;  o = align256(o + th);
+    L.across = o;  o = align256(o + (tc ? th : 0));
+    L.ckpt = o;    o = align256(o + ckpt * H * dk * dv);
     L.part = o;    o = align256(o + ((size_t)T / kda::lin::kSumRows + 1) * H * sizeof(float));
     L.dq = o;      o = align256(o + (H == Hk ? 0 : th * dk));
     L.dk = o;      o = align256(o + (H == Hk ? 0 : th * dk));
@@ -257,7 +276,11 @@ int kda_lin_decode_step(const void *q, const void *k, const void *v, const void 
 size_t kda_lin_bwd_workspace_size(int32_t total_tokens, int32_t num_seqs, int32_t H, int32_t Hk, int32_t dk,
                                   int32_t dv) {
     if (check_sizes(num_seqs, total_tokens, H, Hk, dk, dv, KDA_DTYPE_F32, 0) != KDA_OK) return 0;
-    return bwd_layout(choose_windows(total_tokens, H, false), total_tokens, num_seqs, H, Hk, dk, dv).total;
+    // enough for either element type
+    size_t total = 0;
+    for (bool tc : {false, true})
+        total = std::max(total, bwd_layout(choose_windows(total_tokens, H, tc), tc, total_tokens, num_seqs, H, Hk, dk, dv).total);
+    return total;
 }
 
 int kda_lin_bwd(const void *q, const void *k, const void *v, const void *g, const void *dy, const int32_t *cu_seqlens,
@@ -280,9 +303,11 @@ int kda_lin_bwd(const void *q, const void *k, const void *v, const void *g, cons
     const size_t state_bytes = (size_t)num_seqs * H * dk * dv * sizeof(float);
     if (overlap(initial_state, d_initial_state, state_bytes) || overlap(d_final_state, d_initial_state, state_bytes))
         return KDA_ERR_INVALID_ARG;
-    const Windows wd = choose_windows(total_tokens, H, false);
-    const BwdLayout L = bwd_layout(wd, total_tokens, num_seqs, H, Hk, dk, dv);
-    if (!workspace || workspace_bytes < L.total) return KDA_ERR_WORKSPACE;
+    const bool tc = use_tc(dtype, total_tokens);
+    const Windows wd = choose_windows(total_tokens, H, tc);
+    const BwdLayout L = bwd_layout(wd, tc, total_tokens, num_seqs, H, Hk, dk, dv);
+    if (!workspace || workspace_bytes < kda_lin_bwd_workspace_size(total_tokens, num_seqs, H, Hk, dk, dv))
+        return KDA_ERR_WORKSPACE;
     char *ws = (char *)workspace;
     const int rep = H / Hk, per_head = flags & KDA_LIN_DECAY_PER_HEAD;
 
@@ -292,8 +317,11 @@ int kda_lin_bwd(const void *q, const void *k, const void *v, const void *g, cons
     c.cu = cu_seqlens;
     c.num_seqs = num_seqs; c.T = total_tokens; c.H = H; c.W = wd.W; c.win = wd.win;
     c.xdot = (float *)(ws + L.xdot);
-    c.ckpt = (float *)(ws + L.ckpt);
-    c.dg = per_head ? (void *)(ws + L.dgt) : dg;
+    c.xstate = (float *)(ws + L.xstate);
+    c.across = (float *)(ws + L.across);
+    c.err = (int32_t *)(ws + L.header);
+    c.ckpt = ws + L.ckpt;
+    c.dg = per_head ? (void *)(ws + L.xstate) : dg;
     c.zero_first_dg = initial_state == nullptr;
     c.out_f32 = rep > 1;
 
@@ -336,35 +364,40 @@ int kda_lin_bwd(const void *q, const void *k, const void *v, const void *g, cons
     d.win_t = 1;
     d.gamma = b.gamma;
 
-    if (wd.W > 1) {
-        if (!ok(launch_rec(a, kSum, bf16, dv, dk, st)) || !ok(launch_rec(b, kSumR, bf16, dv, dk, st)) ||
-            !ok(launch_scan(a.win_state, a.gamma, wd.W, H, dk * dv, false, st)) ||
-            !ok(launch_scan(b.win_state, b.gamma, wd.W, H, dk * dv, true, st)))
-            return KDA_ERR_CUDA;
-    }
-    if (!ok(launch_rec(a, kDq, bf16, dv, dk, st)) || !ok(launch_rec(b, kDk, bf16, dv, dk, st)) ||
-        !ok(launch_rec(d, kDv, bf16, dk, dv, st)))
+    auto pass = [&](const Params &p, int mode, int da, int db) {
+        return ok(tc ? launch_tc(p, mode, da, db, st) : launch_rec(p, mode, bf16, da, db, st));
+    };
+    if (wd.W > 1 && (!pass(a, kSum, dv, dk) || !pass(b, kSumR, dv, dk) ||
+                     !ok(launch_scan(a.win_state, a.gamma, wd.W, H, dk * dv, false, st)) ||
+                     !ok(launch_scan(b.win_state, b.gamma, wd.W, H, dk * dv, true, st))))
         return KDA_ERR_CUDA;
+    if (!pass(a, kDq, dv, dk) || !pass(b, kDk, dv, dk) || !pass(d, kDv, dk, dv)) return KDA_ERR_CUDA;
     if (total_tokens == 0) {
         if (per_head && dg && !ok(cudaMemsetAsync(dg, 0, (size_t)H * esz, st))) return KDA_ERR_CUDA;
         return KDA_OK;
     }
+    const Tokens tk{cu_seqlens, num_seqs, total_tokens};
     if (rep > 1) {
         const long n4 = (long)total_tokens * Hk * dk / 4;
         const unsigned blocks = (unsigned)std::min<long>((n4 + 255) / 256, 8L * 148);
         for (int i = 0; i < 2; ++i) {
             const float4 *in = (const float4 *)(ws + (i ? L.dk : L.dq));
             void *out = i ? dk_out : dq;
-            if (bf16) head_sum_kernel<<<blocks, 256, 0, st>>>(in, (__nv_bfloat16 *)out, n4, rep, dk / 4);
-            else head_sum_kernel<<<blocks, 256, 0, st>>>(in, (float *)out, n4, rep, dk / 4);
+            if (bf16) head_sum_kernel<<<blocks, 256, 0, st>>>(in, (__nv_bfloat16 *)out, tk, Hk, rep, dk / 4);
+            else head_sum_kernel<<<blocks, 256, 0, st>>>(in, (float *)out, tk, Hk, rep, dk / 4);
         }
     }
     if (per_head) {
         const int parts = (total_tokens + kSumRows - 1) / kSumRows, hb = (H + 31) / 32;
         float *part = (float *)(ws + L.part);
-        token_sum_kernel<<<dim3(parts, hb), 256, 0, st>>>((const float *)c.dg, part, total_tokens, H);
+        token_sum_kernel<<<dim3(parts, hb), 256, 0, st>>>(c.xstate, tc ? c.across : nullptr, part, tk, H);
         if (bf16) part_sum_kernel<<<hb, 256, 0, st>>>(part, (__nv_bfloat16 *)dg, parts, H);
         else part_sum_kernel<<<hb, 256, 0, st>>>(part, (float *)dg, parts, H);
+    }
+    if (tc && !per_head) {
+        const long n = (long)total_tokens * H;
+        add_kernel<<<(unsigned)std::min<long>((n + 255) / 256, 8L * 148), 256, 0, st>>>(c.xstate, c.across,
+                                                                                       (__nv_bfloat16 *)dg, tk, H);
     }
     return ok(cudaGetLastError()) ? KDA_OK : KDA_ERR_CUDA;
 }

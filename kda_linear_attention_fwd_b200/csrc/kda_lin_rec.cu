@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 3) rec_kernel(const Params p) {
             const size_t slot = (size_t)((a + chunk * kCkpt) / kCkpt + n) * H + h;
             if constexpr (M == DK) {
                 if (in_chunk + rows == chunk_len) {  // the chunk's last token comes first
-                    const float *ck = p.ckpt + slot * (DA * DB);
+                    const float *ck = (const float *)p.ckpt + slot * (DA * DB);
                     float d = 0.f;
 #pragma unroll
                     for (int i = 0; i < NQ; ++i)
@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 3) rec_kernel(const Params p) {
                 gamma *= f;
             }
             if constexpr (M == DQ) {
-                if (in_chunk + rows == chunk_len) store_state(p.ckpt + slot * (DA * DB), false, 1.f);
+                if (in_chunk + rows == chunk_len) store_state((float *)p.ckpt + slot * (DA * DB), false, 1.f);
             }
             __syncthreads();
             if constexpr (M == DQ) {

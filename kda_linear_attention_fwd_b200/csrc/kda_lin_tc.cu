@@ -33,6 +33,20 @@
 // Shared memory (128 x 128): W and V tiles twice (128 KB), R, the hi/lo halves
 // and the state copy (32 KB each).
 //
+// The gradient (kda_lin_rec.cu has the formulas) is three such passes: dq
+// (read do, write v, value k), dk and dv reversed.  Its dg_t is the sum of
+// d(log weight) over all pairs u < t <= s of an earlier and a later token.
+// Summing q . dq - k . dk would cancel to nothing for short memories, at
+// bf16 accuracy, so the pairs are added up as they are, without differences
+// of rounded numbers:
+//   both in the chunk          the dq pass has X = (q k^T) (.) P in fp32 (Q K^T is
+//                              one more product) and takes row sums less column sums
+//   u before the chunk         q . (the state's part of dq)      (dq pass)
+//   s behind the chunk         k . (the state's part of dk)      (dk pass)
+//   u before and s behind      exp(chunk) <S_in, B_in>: the dq pass leaves a bf16 copy
+//                              of the state that enters every chunk in the workspace
+// all four linear in the bf16 operands' roundings.
+//
 // Every wait is bounded (2 s): one that gives up marks the workspace's error
 // word and the CTA, whose remaining waits then return at once; the loads and
 // products in flight are waited for before TMEM is released.
@@ -58,7 +72,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 enum Mode { FWD, SUM, SUMR, DQ, DK, DV };
 
 struct Maps {
-    CUtensorMap rd, wr, val;
+    CUtensorMap rd, wr, val, ext;
 };
 
 template <int DA, int DB, int M>
@@ -66,7 +80,7 @@ struct Cfg {
     static constexpr bool rev = M == SUMR || M == DK || M == DV;
     static constexpr bool sum = M == SUM || M == SUMR;
     static constexpr bool out = !sum;
-    static constexpr int stages = sum ? 3 : 2;
+    static constexpr int stages = sum ? 3 : M == DQ ? 1 : 2;
     static constexpr int wr_bytes = DA / 64 * kBox, val_bytes = DB / 64 * kBox;
     static constexpr int stage_bytes = wr_bytes + val_bytes;
     static constexpr int rd_bytes = out ? wr_bytes : 0;
@@ -75,7 +89,10 @@ struct Cfg {
     static constexpr int off_rd = stages * stage_bytes;
     static constexpr int off_vb = off_rd + rd_bytes;
     static constexpr int off_sb = off_vb + 2 * vb_part;
-    static constexpr int off_ctl = off_sb + sb_bytes;
+    static constexpr int off_ext = off_sb + sb_bytes;
+    static constexpr int ext_bytes = M == DQ ? DB / 64 * kBox : 0;
+    static constexpr int off_xc = off_ext + ext_bytes;  // DQ: column sums of X, per warp
+    static constexpr int off_ctl = off_xc + (M == DQ ? 4 * kC * 4 : 0);
     // TMEM columns
     static constexpr uint32_t col_s = 0, col_a = 128, col_o1 = 256, col_o2 = 384;
     static constexpr uint32_t cols = out ? 512 : 128;
@@ -92,13 +109,14 @@ struct Ctl {
     unsigned long long pv_done;           // O1 and O2 are complete
     unsigned long long o_free;            // O1 and O2 have been read
     unsigned long long clean;             // rows behind a short chunk's end are zero
-    unsigned long long end;
+    unsigned long long ext_full, end;
     int dead;
     uint32_t tmem;
     alignas(16) float pc[2][kC], pe[2][kC];
     float pt[2][4];                         // P: c within the 32-token block, exp(to the block's far end); block sums
     float vw[kC], vt[2][4];                // V: w_s, block sums
-    float ot[2][4];                        // O: block sums
+    float xs[2][4];                        // DK, O: block sums
+    float ot[2][8];                        // O: block sums; DK, S: partial products with the checkpoint
 };
 
 // 32 bytes of one row: one whole sector when the address allows it
@@ -160,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
             mbar_init(smem_u32(&ctl.full[i]), 1);
             mbar_init(smem_u32(&ctl.free[i]), 1);
         }
-        unsigned long long *one[] = {&ctl.rd_full, &ctl.rd_free, &ctl.a_full, &ctl.vb_free, &ctl.kv_done, &ctl.pv_done, &ctl.end};
+        unsigned long long *one[] = {&ctl.rd_full, &ctl.rd_free, &ctl.a_full, &ctl.vb_free, &ctl.kv_done, &ctl.pv_done, &ctl.ext_full, &ctl.end};
         unsigned long long *wg[] = {&ctl.p_full, &ctl.s_full, &ctl.vb_full, &ctl.o_free, &ctl.clean};
         for (auto *b : one) mbar_init(smem_u32(b), 1);
         for (auto *b : wg) mbar_init(smem_u32(b), 128);
@@ -262,6 +280,8 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                     bar_sync(1, 128);
                     wait(ctl.a_full, it & 1);
                     tc_fence_after();
+                    float xr = 0.f;  // DQ: this row's sum of X over earlier tokens
+                    float *xc = reinterpret_cast<float *>(sm + C::off_xc) + warp * kC;
                     // block by block upwards: P's block lies in columns 16 blk .. + 15, which hold products of
                     // block blk / 2, read by then or not needed by this warp
 #pragma unroll 1
@@ -272,6 +292,8 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                             for (int e = 0; e < 16; ++e) pk[e] = 0u;
                         } else {
                             uint32_t r[32];
+                            uint32_t y[M == DQ ? 32 : 1];
+                            if constexpr (M == DQ) tmem_ld32(ta - C::col_a + C::col_o2 + 32 * blk, y);
                             tmem_ld32_wait(ta + 32 * blk, r);
                             if (blk == warp) {
 #pragma unroll
@@ -287,6 +309,13 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                                     }
                                     pk[2 * e4] = pack_bf16(v[0], v[1]);
                                     pk[2 * e4 + 1] = pack_bf16(v[2], v[3]);
+                                    if constexpr (M == DQ) {
+#pragma unroll
+                                        for (int e = 0; e < 4; ++e) {
+                                            const int s = 4 * e4 + e;
+                                            y[s] = __float_as_uint(s < lane ? v[e] * __uint_as_float(y[s]) : 0.f);
+                                        }
+                                    }
                                 }
                             } else {
                                 float far = c;  // + the blocks between
@@ -296,10 +325,32 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
 #pragma unroll
                                 for (int e4 = 0; e4 < 8; ++e4) {
                                     const float4 es = *reinterpret_cast<const float4 *>(&ctl.pe[pb][32 * blk + 4 * e4]);
-                                    pk[2 * e4] = pack_bf16(f2mul(f2mul(make_float2(es.x, es.y), f2),
-                                                                 make_float2(__uint_as_float(r[4 * e4]), __uint_as_float(r[4 * e4 + 1]))));
-                                    pk[2 * e4 + 1] = pack_bf16(f2mul(f2mul(make_float2(es.z, es.w), f2),
-                                                                     make_float2(__uint_as_float(r[4 * e4 + 2]), __uint_as_float(r[4 * e4 + 3]))));
+                                    const float2 v0 = f2mul(f2mul(make_float2(es.x, es.y), f2),
+                                                            make_float2(__uint_as_float(r[4 * e4]), __uint_as_float(r[4 * e4 + 1])));
+                                    const float2 v1 = f2mul(f2mul(make_float2(es.z, es.w), f2),
+                                                            make_float2(__uint_as_float(r[4 * e4 + 2]), __uint_as_float(r[4 * e4 + 3])));
+                                    pk[2 * e4] = pack_bf16(v0);
+                                    pk[2 * e4 + 1] = pack_bf16(v1);
+                                    if constexpr (M == DQ) {
+                                        y[4 * e4] = __float_as_uint(v0.x * __uint_as_float(y[4 * e4]));
+                                        y[4 * e4 + 1] = __float_as_uint(v0.y * __uint_as_float(y[4 * e4 + 1]));
+                                        y[4 * e4 + 2] = __float_as_uint(v1.x * __uint_as_float(y[4 * e4 + 2]));
+                                        y[4 * e4 + 3] = __float_as_uint(v1.y * __uint_as_float(y[4 * e4 + 3]));
+                                    }
+                                }
+                            }
+                            if constexpr (M == DQ) {
+                                // rows behind the end hold other tokens
+#pragma unroll
+                                for (int half = 0; half < 2; ++half) {
+                                    float v[16];
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e) {
+                                        v[e] = row < rows ? __uint_as_float(y[16 * half + e]) : 0.f;
+                                        xr += v[e];
+                                    }
+                                    const float cs = warp_sum16_scatter(v, lane);
+                                    if (!(lane & 1)) xc[32 * blk + 16 * half + row_of_lane(lane)] = cs;
                                 }
                             }
                         }
@@ -308,6 +359,13 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                     tc_wait_st();
                     tc_fence_before();
                     arrive(ctl.p_full);
+                    if constexpr (M == DQ) {
+                        // pairs (s, u), u < s, whose later token is this row less those whose earlier one is
+                        bar_sync(1, 128);
+                        const float *all = reinterpret_cast<const float *>(sm + C::off_xc);
+                        for (int j = warp; j < 4; ++j) xr -= all[j * kC + row];
+                        if (row < rows) p.xdot[(size_t)(base + row) * H + h] = xr;
+                    }
                     ++it;
                 });
             });
@@ -368,6 +426,9 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                     wait(ctl.kv_done, (it - 1) & 1);
                     tc_fence_after();
                 }
+                bf16 *ck = nullptr;
+                if (M == DQ || M == DK) ck = (bf16 *)p.ckpt + (((size_t)(base / kC + n)) * H + h) * (DA * DB) + (size_t)row * DB;
+                float dot = 0.f;
                 if (mine) {
 #pragma unroll 1
                     for (int cb = 0; cb < DB / 32; ++cb) {
@@ -391,6 +452,28 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                                 *reinterpret_cast<uint4 *>(box + ((((cb & 1) * 4 + e) ^ (row & 7)) << 4)) = v;
                             }
                         }
+                        if constexpr (M == DQ) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                *reinterpret_cast<uint4 *>(ck + 32 * cb + 8 * e) =
+                                    make_uint4(pack_bf16(__uint_as_float(r[8 * e]), __uint_as_float(r[8 * e + 1])),
+                                               pack_bf16(__uint_as_float(r[8 * e + 2]), __uint_as_float(r[8 * e + 3])),
+                                               pack_bf16(__uint_as_float(r[8 * e + 4]), __uint_as_float(r[8 * e + 5])),
+                                               pack_bf16(__uint_as_float(r[8 * e + 6]), __uint_as_float(r[8 * e + 7])));
+                        }
+                        if constexpr (M == DK) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const uint4 v = *reinterpret_cast<const uint4 *>(ck + 32 * cb + 8 * e);
+                                const uint32_t vs[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    const float2 u = unpack_bf16(vs[k]);
+                                    dot = fmaf(u.x, __uint_as_float(r[8 * e + 2 * k]), dot);
+                                    dot = fmaf(u.y, __uint_as_float(r[8 * e + 2 * k + 1]), dot);
+                                }
+                            }
+                        }
                         const float2 f2 = make_float2(f, f);
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
@@ -405,6 +488,16 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                 if (C::out) fence_async_smem();
                 tc_fence_before();
                 arrive(ctl.s_full);
+                if constexpr (M == DK) {
+                    // pairs whose tokens lie on either side of the chunk: the same for its every token
+                    dot = warp_sum(dot);
+                    if (lane == 0) ctl.ot[it & 1][4 + wl] = dot;
+                    bar_sync(4, 128);
+                    if (row < rows) {
+                        const float *d = &ctl.ot[it & 1][4];
+                        p.across[(size_t)(base + row) * H + h] = ((d[0] + d[1]) + (d[2] + d[3])) * f * exp2f(load_g(base));
+                    }
+                }
                 ++it;
             });
             // the state behind the segment
@@ -521,31 +614,83 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                         if (C::rev ? j > wl : j < wl) c += ctl.ot[pb][j];
                     const float f = exp2f(c) * p.rd_scale;
                     wait(ctl.pv_done, it & 1);
+                    if (M == DQ) wait(ctl.ext_full, it & 1);
                     tc_fence_after();
-                    bf16 *dst = (bf16 *)p.out + ((size_t)(base + row) * H + h) * DB;
+                    const size_t at = ((size_t)(base + row) * H + h) * DB;
+                    float xi = 0.f;  // gradient passes: the state's part of out . ext
 #pragma unroll 1
                     for (int cb = 0; cb < DB / 32; ++cb) {
                         uint32_t x[32], y[32];
                         tmem_ld32(to1 + 32 * cb, x);
                         tmem_ld32_wait(to2 + 32 * cb, y);
+                        if constexpr (M == DQ || M == DK) {
+                            uint4 e4[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                if (M == DQ)
+                                    e4[e] = *reinterpret_cast<const uint4 *>(sm + C::off_ext + (cb >> 1) * kBox + row * 128 +
+                                                                             ((((cb & 1) * 4 + e) ^ (row & 7)) << 4));
+                                else
+                                    e4[e] = row < rows ? *reinterpret_cast<const uint4 *>(
+                                                             (const bf16 *)p.ext +
+                                                             ((size_t)(base + row) * (H / p.ext_div) + h / p.ext_div) * DB + 32 * cb + 8 * e)
+                                                       : make_uint4(0u, 0u, 0u, 0u);
+                                const uint32_t es[4] = {e4[e].x, e4[e].y, e4[e].z, e4[e].w};
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    const float2 u = unpack_bf16(es[k]);
+                                    xi = fmaf(u.x, __uint_as_float(x[8 * e + 2 * k]), xi);
+                                    xi = fmaf(u.y, __uint_as_float(x[8 * e + 2 * k + 1]), xi);
+                                }
+                            }
+                        }
                         if (cb == DB / 32 - 1) {
                             tc_fence_before();
                             arrive(ctl.o_free);
                         }
+                        float2 o[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            o[e] = f2fma(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), make_float2(f, f),
+                                         make_float2(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1])));
                         if (row < rows) {
+                            if ((M == DQ || M == DK) && p.out_f32) {
+                                float *dst = (float *)p.out + at + 32 * cb;
 #pragma unroll
-                            for (int q = 0; q < 2; ++q) {
-                                uint32_t v[8];
+                                for (int q = 0; q < 8; ++q)
+                                    reinterpret_cast<float4 *>(dst)[q] = make_float4(o[2 * q].x, o[2 * q].y, o[2 * q + 1].x, o[2 * q + 1].y);
+                            } else {
+                                bf16 *dst = (bf16 *)p.out + at + 32 * cb;
 #pragma unroll
-                                for (int e = 0; e < 8; ++e) {
-                                    const int k = 16 * q + 2 * e;
-                                    v[e] = pack_bf16(f2fma(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])),
-                                                           make_float2(f, f),
-                                                           make_float2(__uint_as_float(y[k]), __uint_as_float(y[k + 1]))));
+                                for (int q = 0; q < 2; ++q) {
+                                    uint32_t v[8];
+#pragma unroll
+                                    for (int e = 0; e < 8; ++e) v[e] = pack_bf16(o[8 * q + e]);
+                                    st_global32(dst + 16 * q, v, al32);
                                 }
-                                st_global32(dst + 32 * cb + 16 * q, v, al32);
                             }
                         }
+                    }
+                    if constexpr (M == DQ) {
+                        if (row < rows) p.xstate[(size_t)(base + row) * H + h] = f * xi;
+                    }
+                    if constexpr (M == DK) {
+                        // dg but for the pairs across the chunk: the pairs inside it and those with an
+                        // earlier state from this token on, those with a later state before it
+                        float u = 0.f;
+                        const size_t th = (size_t)(base + row) * H + h;
+                        if (row < rows) u = p.xdot[th] + p.xstate[th];
+                        const float ik = row < rows ? f * xi : 0.f;
+                        float suf = scan_down(u, lane), pre = scan_up(ik, lane) - ik;
+                        if (lane == 0) ctl.xs[0][wl] = suf;
+                        if (lane == 31) ctl.xs[1][wl] = pre + ik;
+                        bar_sync(3, 128);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            if (j > wl) suf += ctl.xs[0][j];
+                            if (j < wl) pre += ctl.xs[1][j];
+                        }
+                        if (row < rows) p.xstate[th] = p.zero_first_dg && base + row == qa ? 0.f : suf + pre;
                     }
                     ++it;
                 });
@@ -581,6 +726,25 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                     }
                     __syncwarp();
                 }
+                if constexpr (M == DQ) {
+                    if (it > 0) wait(ctl.o_free, (it - 1) & 1);
+                    if (elect_one_sync() && !*dead) {
+                        const uint32_t bar = smem_u32(&ctl.ext_full);
+                        mbar_arrive_expect_tx(bar, C::ext_bytes);
+#pragma unroll
+                        for (int x = 0; x < DB / 64; ++x) {
+                            tma_load_3d(sbase + C::off_ext + x * kBox, &maps.ext, 64 * x, h / p.ext_div, base, bar);
+                            if (i + 1 < nch) tma_prefetch_3d(&maps.ext, 64 * x, h / p.ext_div, next_base(base));
+                        }
+                        if (i + 1 < nch) {  // one stage only: the next chunk's tiles at least to L2
+#pragma unroll
+                            for (int x = 0; x < DA / 64; ++x) tma_prefetch_3d(&maps.wr, 64 * x, hw, next_base(base));
+#pragma unroll
+                            for (int x = 0; x < DB / 64; ++x) tma_prefetch_3d(&maps.val, 64 * x, hv, next_base(base));
+                        }
+                    }
+                    __syncwarp();
+                }
                 ++it;
             });
         });
@@ -588,6 +752,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
             for (int x = max(0, it - C::stages); x < it; ++x)
                 mbar_wait(smem_u32(&ctl.full[x % C::stages]), (x / C::stages) & 1);
             if (C::out && it > 0) mbar_wait(smem_u32(&ctl.rd_full), (it - 1) & 1);
+            if (M == DQ && it > 0) mbar_wait(smem_u32(&ctl.ext_full), (it - 1) & 1);
         }
     } else {
         // --------------------------------------------------------------- MMA
@@ -616,9 +781,25 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                             tc_mma_ss(tmem + C::col_a, sdesc_sw128(tr + off, 16, 1024), sdesc_sw128(tw + off, 16, 1024), ID_A,
                                       kk > 0);
                         }
-                        tc_commit(smem_u32(&ctl.a_full));
+                        if (M != DQ) tc_commit(smem_u32(&ctl.a_full));
                     }
                     __syncwarp();
+                    if constexpr (M == DQ) {  // Q K^T beside it, in O2's columns
+                        wait(ctl.ext_full, it & 1);
+                        if (it > 0) wait(ctl.o_free, (it - 1) & 1);
+                        tc_fence_after();
+                        if (elect_one_sync() && !*dead) {
+                            const uint32_t te = sbase + C::off_ext;
+#pragma unroll
+                            for (int kk = 0; kk < DB / 16; ++kk) {
+                                const uint32_t off = (kk >> 2) * kBox + (kk & 3) * 32;
+                                tc_mma_ss(tmem + C::col_o2, sdesc_sw128(te + off, 16, 1024), sdesc_sw128(tv + off, 16, 1024),
+                                          ID_A, kk > 0);
+                            }
+                            tc_commit(smem_u32(&ctl.a_full));
+                        }
+                        __syncwarp();
+                    }
                 }
                 wait(ctl.s_full, it & 1);
                 if (C::out) {
@@ -715,7 +896,8 @@ cudaError_t launch_t(const Params &p, cudaStream_t st) {
     static_assert(bytes <= 232448, "shared memory");
     Maps maps;
     if (!encode(&maps.wr, p.wr, p.T, p.H / p.wr_div, DA) || !encode(&maps.val, p.val, p.T, p.H / p.val_div, DB) ||
-        !encode(&maps.rd, C::out ? p.rd : p.wr, p.T, C::out ? p.H / p.rd_div : p.H / p.wr_div, DA))
+        !encode(&maps.rd, C::out ? p.rd : p.wr, p.T, C::out ? p.H / p.rd_div : p.H / p.wr_div, DA) ||
+        !encode(&maps.ext, M == DQ ? p.ext : p.val, p.T, M == DQ ? p.H / p.ext_div : p.H / p.val_div, DB))
         return cudaErrorInvalidValue;
     cudaError_t e = cudaFuncSetAttribute(tc_kernel<DA, DB, M>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
@@ -734,7 +916,11 @@ cudaError_t launch_m(const Params &p, int da, int db, cudaStream_t st) {
 cudaError_t launch_tc(const Params &p, int mode, int da, int db, cudaStream_t st) {
     switch (mode) {
         case tc::FWD: return tc::launch_m<tc::FWD>(p, da, db, st);
-        default: return tc::launch_m<tc::SUM>(p, da, db, st);
+        case tc::SUM: return tc::launch_m<tc::SUM>(p, da, db, st);
+        case tc::SUMR: return tc::launch_m<tc::SUMR>(p, da, db, st);
+        case tc::DQ: return tc::launch_m<tc::DQ>(p, da, db, st);
+        case tc::DK: return tc::launch_m<tc::DK>(p, da, db, st);
+        default: return tc::launch_m<tc::DV>(p, da, db, st);
     }
 }
 

@@ -347,3 +347,31 @@ def test_a_layer_of_them(cuda_lib, dtype):
                        ("dq", got["dq"], ref["q"]), ("dk", got["dk"], ref["k"]), ("dv", got["dv"], ref["v"]),
                        ("dg", got["dg"], ref["g"])):
         near(t, e.detach().numpy(), tol, name)
+
+
+@pytest.mark.parametrize("per_head", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_gradients_of_rows_behind_the_last_sequence(cuda_lib, dtype, per_head):
+    """They are zero in the binding's results and stay out of the sums."""
+    d = make((100, 60), 4, 2, 64, 64, dtype, per_head=per_head, seed=23)
+    cut = lambda x: x if x.dim() == 1 else x[:150].contiguous()  # noqa: E731
+    cu = torch.tensor([0, 100, 150], dtype=torch.int32, device="cuda")
+    args = [d[x] for x in ("q", "k", "v", "g", "dy")]
+    want = kda.lin_bwd(*(cut(x) for x in args), cu, initial_state=d["s0"])
+    for x in args:
+        if x.dim() > 1:
+            x[150:] = float("nan")
+    got = kda.lin_bwd(*args, cu, initial_state=d["s0"])
+    for name in want:
+        g = got[name]
+        if g.shape != want[name].shape:
+            assert (g[150:] == 0).all(), name
+            g = g[:150]
+        near(g, np32(want[name]), TOL[DT[dtype]], name)
+
+
+def test_the_workspace_reports_no_error(cuda_lib):
+    d = make((300, 40), 2, 2, 64, 128, "bf16", seed=24)
+    ws = torch.full((kda.lin_workspace_size(340, 2, 2, 2, 64, 128),), 255, dtype=torch.uint8, device="cuda")
+    kda.lin_chunk_fwd(d["q"], d["k"], d["v"], d["g"], d["cu"], workspace=ws)
+    assert kda.chunk_fwd_check(ws) == 0
