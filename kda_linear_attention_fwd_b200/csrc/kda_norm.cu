@@ -62,56 +62,90 @@ KDA_DEVICE VecT<T, VEC> load_vec(const void *base, long at) {
 template <typename T, int VEC>
 KDA_DEVICE void store_vec(void *base, long at, const float (&v)[VEC]) {
     VecT<T, VEC> o;
+    if constexpr (VEC == 8) {
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) st(&o.e[e], v[e]);
+        for (int e = 0; e < 4; ++e)
+            reinterpret_cast<__nv_bfloat162 *>(o.e)[e] = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) st(&o.e[e], v[e]);
+    }
     *reinterpret_cast<VecT<T, VEC> *>((T *)base + at) = o;
 }
 
-// Sum of N values over the TPR threads of a row (every thread gets it).
+// Sum of N values over the TPR threads of a row (every thread gets it).  red
+// is not written again before another barrier of the CTA.
 template <int N>
-KDA_DEVICE void row_sum(float (&v)[N], int tpr, float (*red)[N]) {
-    for (int o = min(tpr, 32) >> 1; o > 0; o >>= 1)
+KDA_DEVICE void row_sum(float (&v)[N], int tpr, float (*red)[2]) {
+    if (tpr >= 32) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+        for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+    } else {
+        for (int o = tpr >> 1; o > 0; o >>= 1)
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+    }
     if (tpr > 32) {
-        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-        __syncthreads();  // earlier readers of red are done
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = tpr >> 5, first = warp / nw * nw;
         if (lane == 0)
 #pragma unroll
             for (int i = 0; i < N; ++i) red[warp][i] = v[i];
         __syncthreads();
-        const int nw = tpr >> 5, first = warp / nw * nw;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            float a = 0.f;
-            for (int j = 0; j < nw; ++j) a += red[first + j][i];
-            v[i] = a;
+            v[i] = lane < nw ? red[first + lane][i] : 0.f;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
         }
     }
 }
 
-KDA_DEVICE float act_of(float z, int flags) {
-    if (flags & (KDA_NORM_GATE_SIGMOID | KDA_NORM_GATE_SILU)) {
-        const float s = sigmoid_f(z);
-        return (flags & KDA_NORM_GATE_SILU) ? z * s : s;
-    }
-    return z;
+// The gate: none, as given, its logistic function, z times that.  GATE_ANY:
+// decided at run time (the single-element kernels, which are not worth four
+// instances each).
+enum Gate { GATE_NONE, GATE_GIVEN, GATE_SIGMOID, GATE_SILU, GATE_ANY };
+template <int G>
+KDA_DEVICE int gate_of(const Params &p) {
+    if (G != GATE_ANY) return G;
+    if (!p.gate) return GATE_NONE;
+    return (p.flags & KDA_NORM_GATE_SIGMOID) ? GATE_SIGMOID : (p.flags & KDA_NORM_GATE_SILU) ? GATE_SILU : GATE_GIVEN;
 }
-KDA_DEVICE float act_slope(float z, int flags) {
-    if (flags & (KDA_NORM_GATE_SIGMOID | KDA_NORM_GATE_SILU)) {
-        const float s = sigmoid_f(z);
-        return (flags & KDA_NORM_GATE_SILU) ? s * (1.f + z * (1.f - s)) : s * (1.f - s);
-    }
-    return 1.f;
+// 1 / (1 + exp(-z)) with the approximate reciprocal (1 ulp): an IEEE division
+// would be a third of the gated kernels' instructions.
+KDA_DEVICE float logistic(float z) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + __expf(-z)));
+    return r;
+}
+// act(z), s being logistic(z) where the gate has one
+KDA_DEVICE float act_of(int g, float z, float s) {
+    return g == GATE_NONE ? 1.f : g == GATE_GIVEN ? z : g == GATE_SIGMOID ? s : z * s;
+}
+KDA_DEVICE float slope_of(int g, float z, float s) {
+    return g == GATE_SIGMOID ? s * (1.f - s) : g == GATE_SILU ? s * (1.f + z * (1.f - s)) : 1.f;
 }
 
-template <typename T, int VEC, int NV, int MT>
-__global__ void __launch_bounds__(MT) fwd_kernel(const Params p) {
-    __shared__ float red[32][1];
-    const int tpr = p.tpr, t = threadIdx.x & (tpr - 1);
+// VEC elements of a weight, or ones
+template <typename T, int VEC>
+KDA_DEVICE void load_weight(float (&w)[VEC], const void *base, int c) {
+    if (base) {
+        const VecT<T, VEC> v = load_vec<T, VEC>(base, c);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) w[e] = ld(&v.e[e]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) w[e] = 1.f;
+    }
+}
+
+template <typename T, int VEC, int NV, int MT, int G>
+__global__ void __launch_bounds__(MT) fwd_kernel(const __grid_constant__ Params p) {
+    __shared__ float red[2][32][2];
+    const int tpr = p.tpr, t = threadIdx.x & (tpr - 1), g = gate_of<G>(p);
     const long row = (long)blockIdx.x * (blockDim.x / tpr) + threadIdx.x / tpr;
     const bool live = row < p.rows;
-    const bool post = p.flags & KDA_NORM_POST, pre = p.flags & KDA_NORM_PRE;
     const float inv_d = 1.f / p.D;
     VecT<T, VEC> y[NV], z[NV], x[NV];
     float u[NV][VEC];
@@ -121,7 +155,7 @@ __global__ void __launch_bounds__(MT) fwd_kernel(const Params p) {
         const int c = (i * tpr + t) * VEC;
         if (live && c < p.D) {
             y[i] = load_vec<T, VEC>(p.y, row * p.y_ld + c);
-            if (p.gate) z[i] = load_vec<T, VEC>(p.gate, row * p.gate_ld + c);
+            if (g != GATE_NONE) z[i] = load_vec<T, VEC>(p.gate, row * p.gate_ld + c);
             if (p.x) x[i] = load_vec<T, VEC>(p.x, row * p.x_ld + c);
         }
     }
@@ -135,8 +169,8 @@ __global__ void __launch_bounds__(MT) fwd_kernel(const Params p) {
         }
     }
     float iy = 1.f;
-    if (post) {
-        row_sum(ss, tpr, red);
+    if (p.flags & KDA_NORM_POST) {
+        row_sum(ss, tpr, red[0]);
         iy = rsqrtf(fmaf(ss[0], inv_d, p.eps));
     }
     float rr[1] = {0.f};
@@ -144,13 +178,15 @@ __global__ void __launch_bounds__(MT) fwd_kernel(const Params p) {
     for (int i = 0; i < NV; ++i) {
         const int c = (i * tpr + t) * VEC;
         if (live && c < p.D) {
-            VecT<T, VEC> wv;
-            if (p.w_post) wv = load_vec<T, VEC>(p.w_post, c);
+            float w[VEC];
+            load_weight<T, VEC>(w, p.w_post, c);
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
-                float a = u[i][e] * iy;
-                if (p.w_post) a *= ld(&wv.e[e]);
-                if (p.gate) a *= act_of(ld(&z[i].e[e]), p.flags);
+                float a = u[i][e] * iy * w[e];
+                if (g != GATE_NONE) {
+                    const float zz = ld(&z[i].e[e]);
+                    a *= act_of(g, zz, g >= GATE_SIGMOID ? logistic(zz) : 0.f);
+                }
                 a = p.x ? fmaf(a, p.c, ld(&x[i].e[e])) : a * p.c;
                 u[i][e] = a;
                 rr[0] = fmaf(a, a, rr[0]);
@@ -158,90 +194,110 @@ __global__ void __launch_bounds__(MT) fwd_kernel(const Params p) {
             store_vec<T, VEC>(p.out, row * p.D + c, u[i]);
         }
     }
-    if (!pre) return;
-    row_sum(rr, tpr, red);
+    if (!(p.flags & KDA_NORM_PRE)) return;
+    row_sum(rr, tpr, red[1]);
     const float ir = rsqrtf(fmaf(rr[0], inv_d, p.eps));
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (i * tpr + t) * VEC;
         if (live && c < p.D) {
-            VecT<T, VEC> wv;
-            if (p.w_pre) wv = load_vec<T, VEC>(p.w_pre, c);
+            float w[VEC];
+            load_weight<T, VEC>(w, p.w_pre, c);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) u[i][e] *= p.w_pre ? ir * ld(&wv.e[e]) : ir;
+            for (int e = 0; e < VEC; ++e) u[i][e] *= ir * w[e];
             store_vec<T, VEC>(p.normed, row * p.D + c, u[i]);
         }
     }
 }
 
-template <typename T, int VEC, int NV, int MT>
-__global__ void __launch_bounds__(MT) bwd_kernel(const Params p) {
-    __shared__ float red[32][2];
-    __shared__ float red1[32][1];
+// PRE: the next block's norm is there and has a gradient.  A row's vectors
+// stay in registers in their own type; those of the next row are requested as
+// soon as the last use of this row's is behind, before the last row sum.
+template <typename T, int VEC, int NV, int MT, int G, bool PRE>
+__global__ void __launch_bounds__(MT, 1024 / MT) bwd_kernel(const __grid_constant__ Params p) {
+    __shared__ float red[2][3][32][2];
     extern __shared__ float colsum[];  // [2][D], when a CTA holds more than one row
-    const int tpr = p.tpr, t = threadIdx.x & (tpr - 1);
+    const int tpr = p.tpr, t = threadIdx.x & (tpr - 1), g = gate_of<G>(p);
     const int per = blockDim.x / tpr, sub = threadIdx.x / tpr;
-    const bool post = p.flags & KDA_NORM_POST, pre = p.flags & KDA_NORM_PRE;
-    const bool need_r = pre && p.dh;
+    const bool post = p.flags & KDA_NORM_POST;
     const float inv_d = 1.f / p.D;
-    float gpost[NV][VEC], gpre[NV][VEC];
+    float gpost[NV][VEC], gpre[PRE ? NV : 1][VEC];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) gpost[i][e] = gpre[i][e] = 0.f;
-
-    for (long row0 = (long)blockIdx.x * per; row0 < p.rows; row0 += (long)gridDim.x * per) {
-        const long row = row0 + sub;
-        const bool live = row < p.rows;
-        VecT<T, VEC> y[NV], z[NV], x[NV], dr[NV], dh[NV];
-        float a1[1] = {0.f};
+        for (int e = 0; e < VEC; ++e) {
+            gpost[i][e] = 0.f;
+            if (PRE) gpre[i][e] = 0.f;
+        }
+    VecT<T, VEC> y[NV], z[NV], x[NV], dr[NV], dh[NV];
+    auto load_y = [&](long row) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * tpr + t) * VEC;
-            if (live && c < p.D) {
-                y[i] = load_vec<T, VEC>(p.y, row * p.y_ld + c);
-                if (p.gate) z[i] = load_vec<T, VEC>(p.gate, row * p.gate_ld + c);
-                if (p.x && need_r) x[i] = load_vec<T, VEC>(p.x, row * p.x_ld + c);
+            if (row < p.rows && c < p.D) y[i] = load_vec<T, VEC>(p.y, row * p.y_ld + c);
+        }
+    };
+    auto load_rest = [&](long row) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * tpr + t) * VEC;
+            if (row < p.rows && c < p.D) {
+                if (g != GATE_NONE) z[i] = load_vec<T, VEC>(p.gate, row * p.gate_ld + c);
+                if (PRE && p.x) x[i] = load_vec<T, VEC>(p.x, row * p.x_ld + c);
                 if (p.dr) dr[i] = load_vec<T, VEC>(p.dr, row * p.D + c);
-                if (need_r) dh[i] = load_vec<T, VEC>(p.dh, row * p.D + c);
+                if (PRE) dh[i] = load_vec<T, VEC>(p.dh, row * p.D + c);
             }
         }
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (live && (i * tpr + t) * VEC < p.D)
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    const float v = ld(&y[i].e[e]);
-                    a1[0] = fmaf(v, v, a1[0]);
-                }
+    };
+    const long step = (long)gridDim.x * per;
+    long row = (long)blockIdx.x * per + sub;
+    load_y(row);
+    load_rest(row);
+    int par = 0;
+    for (long row0 = (long)blockIdx.x * per; row0 < p.rows; row0 += step, row += step, par ^= 1) {
+        const bool live = row < p.rows;
         float iy = 1.f;
         if (post) {
-            row_sum(a1, tpr, red1);
+            float a1[1] = {0.f};
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (live && (i * tpr + t) * VEC < p.D)
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) {
+                        const float v = ld(&y[i].e[e]);
+                        a1[0] = fmaf(v, v, a1[0]);
+                    }
+            row_sum(a1, tpr, red[par][0]);
             iy = rsqrtf(fmaf(a1[0], inv_d, p.eps));
         }
         float ir = 0.f, mean_r = 0.f;
-        if (need_r) {
+        float r[PRE ? NV : 1][VEC], sg[NV][VEC];  // out, unrounded; logistic(gate)
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (g >= GATE_SIGMOID && live && (i * tpr + t) * VEC < p.D)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) sg[i][e] = logistic(ld(&z[i].e[e]));
+        if constexpr (PRE) {
             float s2[2] = {0.f, 0.f};  // sum r^2, sum dh w_pre r
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int c = (i * tpr + t) * VEC;
                 if (live && c < p.D) {
-                    VecT<T, VEC> wa, wb;
-                    if (p.w_post) wa = load_vec<T, VEC>(p.w_post, c);
-                    if (p.w_pre) wb = load_vec<T, VEC>(p.w_pre, c);
+                    float wa[VEC], wb[VEC];
+                    load_weight<T, VEC>(wa, p.w_post, c);
+                    load_weight<T, VEC>(wb, p.w_pre, c);
 #pragma unroll
                     for (int e = 0; e < VEC; ++e) {
-                        float a = ld(&y[i].e[e]) * iy;
-                        if (p.w_post) a *= ld(&wa.e[e]);
-                        if (p.gate) a *= act_of(ld(&z[i].e[e]), p.flags);
+                        float a = ld(&y[i].e[e]) * iy * wa[e];
+                        if (g != GATE_NONE) a *= act_of(g, ld(&z[i].e[e]), sg[i][e]);
                         a = p.x ? fmaf(a, p.c, ld(&x[i].e[e])) : a * p.c;
-                        const float m = ld(&dh[i].e[e]) * (p.w_pre ? ld(&wb.e[e]) : 1.f);
+                        r[i][e] = a;
                         s2[0] = fmaf(a, a, s2[0]);
-                        s2[1] = fmaf(m, a, s2[1]);
+                        s2[1] = fmaf(ld(&dh[i].e[e]) * wb[e], a, s2[1]);
                     }
                 }
             }
-            row_sum(s2, tpr, red);
+            row_sum(s2, tpr, red[par][1]);
             ir = rsqrtf(fmaf(s2[0], inv_d, p.eps));
             mean_r = s2[1] * ir * inv_d;
         }
@@ -251,40 +307,38 @@ __global__ void __launch_bounds__(MT) bwd_kernel(const Params p) {
         for (int i = 0; i < NV; ++i) {
             const int c = (i * tpr + t) * VEC;
             if (live && c < p.D) {
-                VecT<T, VEC> wa, wb;
-                if (p.w_post) wa = load_vec<T, VEC>(p.w_post, c);
-                if (need_r && p.w_pre) wb = load_vec<T, VEC>(p.w_pre, c);
-                float dR[VEC], dz[VEC];
+                float wa[VEC], wb[VEC], dR[VEC], dz[VEC];
+                load_weight<T, VEC>(wa, p.w_post, c);
+                if (PRE) load_weight<T, VEC>(wb, p.w_pre, c);
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
                     const float yn = ld(&y[i].e[e]) * iy;
-                    const float w = p.w_post ? ld(&wa.e[e]) : 1.f;
-                    const float zz = p.gate ? ld(&z[i].e[e]) : 1.f;
-                    const float act = p.gate ? act_of(zz, p.flags) : 1.f;
                     float d = p.dr ? ld(&dr[i].e[e]) : 0.f;
-                    if (need_r) {
-                        const float u = yn * w * act;
-                        const float rn = (p.x ? fmaf(u, p.c, ld(&x[i].e[e])) : u * p.c) * ir;
-                        const float dhe = ld(&dh[i].e[e]);
-                        const float m = p.w_pre ? dhe * ld(&wb.e[e]) : dhe;
-                        d += ir * (m - rn * mean_r);
+                    if constexpr (PRE) {
+                        const float rn = r[i][e] * ir, dhe = ld(&dh[i].e[e]);
+                        d = fmaf(ir, fmaf(-rn, mean_r, dhe * wb[e]), d);
                         gpre[i][e] = fmaf(dhe, rn, gpre[i][e]);
                     }
                     dR[e] = d;
                     const float du = d * p.c;
-                    if (p.gate) dz[e] = du * yn * w * act_slope(zz, p.flags);
-                    const float da = du * act;
+                    float da = du;
+                    if (g != GATE_NONE) {
+                        const float zz = ld(&z[i].e[e]);
+                        dz[e] = du * yn * wa[e] * slope_of(g, zz, sg[i][e]);
+                        da *= act_of(g, zz, sg[i][e]);
+                    }
                     gpost[i][e] = fmaf(da, yn, gpost[i][e]);
-                    dn[i][e] = da * w;
+                    dn[i][e] = da * wa[e];
                     a3[0] = fmaf(dn[i][e], yn, a3[0]);
                 }
                 if (p.dx) store_vec<T, VEC>(p.dx, row * p.D + c, dR);
-                if (p.dgate) store_vec<T, VEC>(p.dgate, row * p.D + c, dz);
+                if (g != GATE_NONE && p.dgate) store_vec<T, VEC>(p.dgate, row * p.D + c, dz);
             }
         }
+        load_rest(row + step);
         float mean_y = 0.f;
         if (post) {
-            row_sum(a3, tpr, red1);
+            row_sum(a3, tpr, red[par][2]);
             mean_y = a3[0] * inv_d;
         }
 #pragma unroll
@@ -293,43 +347,34 @@ __global__ void __launch_bounds__(MT) bwd_kernel(const Params p) {
             if (live && c < p.D) {
                 if (post)
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) dn[i][e] = iy * (dn[i][e] - ld(&y[i].e[e]) * iy * mean_y);
+                    for (int e = 0; e < VEC; ++e) dn[i][e] = iy * fmaf(-(ld(&y[i].e[e]) * iy), mean_y, dn[i][e]);
                 store_vec<T, VEC>(p.dy, row * p.D + c, dn[i]);
             }
         }
+        load_y(row + step);
     }
     if (!p.want_post && !p.want_pre) return;
     // this CTA's column sums: over its row groups in order, then to the workspace
     float *dst = p.part + (size_t)blockIdx.x * 2 * p.D;
-    if (per > 1) {
-        for (int s = 0; s < per; ++s) {
-            __syncthreads();
-            if (sub == s) {
+    for (int s = 0; s < per; ++s) {
+        if (per > 1) __syncthreads();
+        if (sub == s) {
+            float *to = per > 1 ? colsum : dst;
 #pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    const int c = (i * tpr + t) * VEC;
-                    if (c < p.D)
+            for (int i = 0; i < NV; ++i) {
+                const int c = (i * tpr + t) * VEC;
+                if (c < p.D)
 #pragma unroll
-                        for (int e = 0; e < VEC; ++e) {
-                            colsum[c + e] = (s ? colsum[c + e] : 0.f) + gpost[i][e];
-                            colsum[p.D + c + e] = (s ? colsum[p.D + c + e] : 0.f) + gpre[i][e];
-                        }
-                }
+                    for (int e = 0; e < VEC; ++e) {
+                        to[c + e] = (s ? to[c + e] : 0.f) + gpost[i][e];
+                        to[p.D + c + e] = PRE ? (s ? to[p.D + c + e] : 0.f) + gpre[i][e] : 0.f;
+                    }
             }
         }
+    }
+    if (per > 1) {
         __syncthreads();
         for (int c = threadIdx.x; c < 2 * p.D; c += blockDim.x) dst[c] = colsum[c];
-    } else {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (i * tpr + t) * VEC;
-            if (c < p.D)
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    dst[c + e] = gpost[i][e];
-                    dst[p.D + c + e] = gpre[i][e];
-                }
-        }
     }
 }
 
@@ -354,11 +399,11 @@ __global__ void __launch_bounds__(256) weight_sum_kernel(const float *part, int 
 struct Shape {
     int vec, nv, tpr, threads, per;
 };
-// Threads per row: each holds at most 2 vectors while 512 threads are enough
-// (the loads of a row are then all in flight at once), 4 or, for single
-// elements, 16 behind that.
+// Threads per row: one vector each while 512 threads are enough, so that all
+// of a row's loads are in flight at once and the row's values take few
+// registers; 2, 4 or, for single elements, 16 behind that.
 Shape choose_shape(int D, int vec) {
-    static constexpr int most[5][2] = {{2, 256}, {2, 512}, {4, 512}, {4, 1024}, {16, 1024}};
+    static constexpr int most[5][2] = {{1, 512}, {2, 512}, {2, 1024}, {4, 1024}, {16, 1024}};
     const int vecs = (D + vec - 1) / vec;
     int i = 0;
     while (i < 4 && most[i][0] * most[i][1] < vecs) ++i;
@@ -367,30 +412,43 @@ Shape choose_shape(int D, int vec) {
     s.nv = most[i][0];
     s.tpr = 1;
     while (s.tpr * s.nv < vecs) s.tpr *= 2;
-    if (vecs == 1) s.nv = 1;
     s.threads = std::max(kThreads, s.tpr);
     s.per = s.threads / s.tpr;
     return s;
 }
 
-template <typename T, int VEC, int NV, int MT>
-cudaError_t launch_nv(const Params &p, const Shape &s, bool bwd, unsigned grid, cudaStream_t st) {
+template <typename T, int VEC, int NV, int MT, int G>
+cudaError_t launch_g(const Params &p, const Shape &s, bool bwd, unsigned grid, cudaStream_t st) {
     if (bwd) {
         const size_t bytes = s.per > 1 ? (size_t)2 * p.D * sizeof(float) : 0;
-        bwd_kernel<T, VEC, NV, MT><<<grid, s.threads, bytes, st>>>(p);
+        if ((p.flags & KDA_NORM_PRE) && p.dh) bwd_kernel<T, VEC, NV, MT, G, true><<<grid, s.threads, bytes, st>>>(p);
+        else bwd_kernel<T, VEC, NV, MT, G, false><<<grid, s.threads, bytes, st>>>(p);
     } else {
-        fwd_kernel<T, VEC, NV, MT><<<grid, s.threads, 0, st>>>(p);
+        fwd_kernel<T, VEC, NV, MT, G><<<grid, s.threads, 0, st>>>(p);
     }
     return cudaGetLastError();
 }
+template <typename T, int VEC, int NV, int MT>
+cudaError_t launch_nv(const Params &p, const Shape &s, bool bwd, unsigned grid, cudaStream_t st) {
+    if constexpr (VEC == 1) {
+        return launch_g<T, VEC, NV, MT, GATE_ANY>(p, s, bwd, grid, st);
+    } else {
+        if (!p.gate) return launch_g<T, VEC, NV, MT, GATE_NONE>(p, s, bwd, grid, st);
+        if (p.flags & KDA_NORM_GATE_SIGMOID) return launch_g<T, VEC, NV, MT, GATE_SIGMOID>(p, s, bwd, grid, st);
+        if (p.flags & KDA_NORM_GATE_SILU) return launch_g<T, VEC, NV, MT, GATE_SILU>(p, s, bwd, grid, st);
+        return launch_g<T, VEC, NV, MT, GATE_GIVEN>(p, s, bwd, grid, st);
+    }
+}
 template <typename T, int VEC>
 cudaError_t launch_vec(const Params &p, const Shape &s, bool bwd, unsigned grid, cudaStream_t st) {
-    if (s.nv == 1) return launch_nv<T, VEC, 1, 256>(p, s, bwd, grid, st);
-    if (s.nv == 2 && s.threads == 256) return launch_nv<T, VEC, 2, 256>(p, s, bwd, grid, st);
-    if (s.nv == 2) return launch_nv<T, VEC, 2, 512>(p, s, bwd, grid, st);
-    if (s.nv == 4 && s.threads == 512) return launch_nv<T, VEC, 4, 512>(p, s, bwd, grid, st);
-    if (s.nv == 4) return launch_nv<T, VEC, 4, 1024>(p, s, bwd, grid, st);
-    // 16 x 1024 = kMaxD: only single elements come here
+    if (s.nv == 1 && s.threads == 256) return launch_nv<T, VEC, 1, 256>(p, s, bwd, grid, st);
+    if (s.nv == 1) return launch_nv<T, VEC, 1, 512>(p, s, bwd, grid, st);
+    if (s.nv == 2 && s.threads == 512) return launch_nv<T, VEC, 2, 512>(p, s, bwd, grid, st);
+    if (s.nv == 2) return launch_nv<T, VEC, 2, 1024>(p, s, bwd, grid, st);
+    // 8 elements x 2 x 1024 = kMaxD: longer rows are fp32 or single elements
+    if constexpr (VEC <= 4) {
+        if (s.nv == 4) return launch_nv<T, VEC, 4, 1024>(p, s, bwd, grid, st);
+    }
     if constexpr (VEC == 1) return launch_nv<T, 1, 16, 1024>(p, s, bwd, grid, st);
     return cudaErrorInvalidValue;
 }
@@ -444,7 +502,7 @@ int check_elems(const void *const *ptrs, int n, size_t esz) {
 
 int bwd_parts(int64_t rows, const Shape &s) {
     const int64_t batches = (rows + s.per - 1) / s.per;
-    return (int)std::max<int64_t>(1, std::min<int64_t>(batches, (int64_t)sm_count() * (s.threads > 512 ? 1 : 1024 / s.threads)));
+    return (int)std::max<int64_t>(1, std::min<int64_t>(batches, (int64_t)sm_count() * (1024 / s.threads)));
 }
 
 }  // namespace
