@@ -26,11 +26,11 @@
 // step has its own warpgroup, one chunk apart at most, joined by mbarriers:
 //   warps  0- 3  P    the decayed products           (TMEM lane = token)
 //   warps  4- 7  S    the state: scaled in TMEM, bf16 copy to shared memory
-//   warps  8-11  V    w V as hi and lo halves, 64 tokens at a time
+//   warps  8-11  V    w V as hi and lo parts, 32 tokens at a time into two alternating buffers
 //   warps 12-15  O    the outputs                    (TMEM lane = token)
 //   warp  16     TMA  tiles of 128 tokens x 64 channels, 128-byte swizzle
 //   warp  17     MMA  issues every product
-// Shared memory (128 x 128): W and V tiles twice (128 KB), R, the hi/lo halves
+// Shared memory (128 x 128): W and V tiles twice (128 KB), R, the hi/lo buffers
 // and the state copy (32 KB each).
 //
 // The gradient (kda_lin_rec.cu has the formulas) is three such passes: dq
@@ -52,6 +52,8 @@
 // products in flight are waited for before TMEM is released.
 #include <cuda.h>
 #include <cudaTypedefs.h>
+
+#include <type_traits>
 
 #include "kda_common.cuh"
 #include "kda_lin.cuh"
@@ -84,11 +86,12 @@ struct Cfg {
     static constexpr int wr_bytes = DA / 64 * kBox, val_bytes = DB / 64 * kBox;
     static constexpr int stage_bytes = wr_bytes + val_bytes;
     static constexpr int rd_bytes = out ? wr_bytes : 0;
-    static constexpr int vb_part = DB / 64 * (64 * 64 * 2);  // 64 tokens of hi or lo
+    static constexpr int vb_part = DB / 64 * (32 * 128);  // 32 tokens of hi or lo
+    static constexpr int vb_bytes = 2 * vb_part;
     static constexpr int sb_bytes = out ? DB / 64 * (DA * 128) : 0;
     static constexpr int off_rd = stages * stage_bytes;
     static constexpr int off_vb = off_rd + rd_bytes;
-    static constexpr int off_sb = off_vb + 2 * vb_part;
+    static constexpr int off_sb = off_vb + 2 * vb_bytes;
     static constexpr int off_ext = off_sb + sb_bytes;
     static constexpr int ext_bytes = M == DQ ? DB / 64 * kBox : 0;
     static constexpr int off_xc = off_ext + ext_bytes;  // DQ: column sums of X, per warp
@@ -104,7 +107,7 @@ struct Ctl {
     unsigned long long a_full;            // A is in TMEM
     unsigned long long p_full;            // P is in TMEM
     unsigned long long s_full;            // the scaled state and its copy are in place
-    unsigned long long vb_full, vb_free;  // the hi/lo half
+    unsigned long long vb_full[2], vb_free[2];  // the hi/lo quarters, alternating
     unsigned long long kv_done;           // the state has this chunk's writes
     unsigned long long pv_done;           // O1 and O2 are complete
     unsigned long long o_free;            // O1 and O2 have been read
@@ -178,8 +181,12 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
             mbar_init(smem_u32(&ctl.full[i]), 1);
             mbar_init(smem_u32(&ctl.free[i]), 1);
         }
-        unsigned long long *one[] = {&ctl.rd_full, &ctl.rd_free, &ctl.a_full, &ctl.vb_free, &ctl.kv_done, &ctl.pv_done, &ctl.ext_full, &ctl.end};
-        unsigned long long *wg[] = {&ctl.p_full, &ctl.s_full, &ctl.vb_full, &ctl.o_free, &ctl.clean};
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&ctl.vb_full[i]), 128);
+            mbar_init(smem_u32(&ctl.vb_free[i]), 1);
+        }
+        unsigned long long *one[] = {&ctl.rd_full, &ctl.rd_free, &ctl.a_full, &ctl.kv_done, &ctl.pv_done, &ctl.ext_full, &ctl.end};
+        unsigned long long *wg[] = {&ctl.p_full, &ctl.s_full, &ctl.o_free, &ctl.clean};
         for (auto *b : one) mbar_init(smem_u32(b), 1);
         for (auto *b : wg) mbar_init(smem_u32(b), 128);
         ctl.dead = (sbase & 1023u) != 0;  // never: the tiles would be read wrongly
@@ -192,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
     const uint32_t tmem = ctl.tmem;
 
     auto wait = [&](unsigned long long &bar, uint32_t parity) {
-        if (*dead) return;
+        if (mbar_try_wait(smem_u32(&bar), parity) || *dead) return;
         if (!mbar_wait(smem_u32(&bar), parity)) {
             *dead = 1;
             if (p.err) atomicOr(p.err + 2, 1);
@@ -532,8 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
     } else if (role == 2) {
         // --------------------------------------------------------------- V
         const int vt = tid - 256, wl = warp & 3;
-        const int vrow = vt & 63, vhalf = vt >> 6;
-        int halves = 0;
+        int quarters = 0;
         segments([&](int n, int a, int b, int qa, int qb) {
             float gx = 0.f;
             chunks(a, b, [&](int base, int rows, int i, int nch) {
@@ -554,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                 unsigned char *tw = sm + st * C::stage_bytes, *tv = tw + C::wr_bytes;
                 if (rows < kC) {
                     // the MMA warp has passed the short chunk before this one
-                    if (halves > 0) wait(ctl.vb_free, (halves - 1) & 1);
+                    if (quarters > 0) wait(ctl.vb_free[(quarters - 1) & 1], ((quarters - 1) >> 1) & 1);
                     // rows behind the end hold other tokens: zero, whatever they are
                     if (vt >= rows) {
                         const uint4 z = make_uint4(0u, 0u, 0u, 0u);
@@ -565,30 +571,33 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                     arrive(ctl.clean);
                 }
                 bar_sync(2, 128);  // vw, and the zeros
-                for (int hh = 0; hh < (rows > 64 ? 2 : 1); ++hh) {
-                    if (halves > 0) wait(ctl.vb_free, (halves - 1) & 1);
-                    const float f = ctl.vw[64 * hh + vrow];
-                    constexpr int CH = DB / 16;  // 16-byte pieces of this thread: its half of the channels
+                // 32 tokens at a time: lane = token, warp = quarter of the channels
+                for (int qq = 0; qq < (rows + 31) / 32; ++qq, ++quarters) {
+                    const int vb = quarters & 1;
+                    if (quarters > 1) wait(ctl.vb_free[vb], ((quarters >> 1) - 1) & 1);
+                    const int r = 32 * qq + lane;
+                    const float f = ctl.vw[r];
+                    const float2 f2 = make_float2(f, f);
+                    constexpr int CH = DB / 32;  // 16-byte pieces
 #pragma unroll
                     for (int c0 = 0; c0 < CH; ++c0) {
-                        const int c = vhalf * CH + c0, box = c >> 3, cc = c & 7, r = 64 * hh + vrow;
-                        const uint4 x = *reinterpret_cast<const uint4 *>(tv + box * kBox + r * 128 + ((cc ^ (r & 7)) << 4));
+                        const int c = wl * CH + c0, box = c >> 3, off = ((c & 7) ^ (lane & 7)) << 4;
+                        const uint4 x = *reinterpret_cast<const uint4 *>(tv + box * kBox + r * 128 + off);
                         const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
                         uint32_t hi[4], lw[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const float2 v = f2mul(unpack_bf16(xs[e]), make_float2(f, f));
+                            const float2 v = f2mul(unpack_bf16(xs[e]), f2);
                             hi[e] = pack_bf16(v);
                             const float2 k2 = unpack_bf16(hi[e]);
                             lw[e] = pack_bf16(v.x - k2.x, v.y - k2.y);
                         }
-                        unsigned char *dst = sm + C::off_vb + box * 8192 + vrow * 128 + ((cc ^ (vrow & 7)) << 4);
+                        unsigned char *dst = sm + C::off_vb + vb * C::vb_bytes + box * 4096 + lane * 128 + off;
                         *reinterpret_cast<uint4 *>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                         *reinterpret_cast<uint4 *>(dst + C::vb_part) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
                     }
                     fence_async_smem();
-                    arrive(ctl.vb_full);
-                    ++halves;
+                    arrive(ctl.vb_full[vb]);
                 }
                 ++it;
             });
@@ -760,94 +769,113 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
         constexpr uint32_t ID_O1 = idesc_bf16(128, DB, 0, 1);  // R (K-major) x S (MN-major)
         constexpr uint32_t ID_KV = idesc_bf16(128, DB, 1, 1);  // W^T (MN-major) x w V (MN-major)
         constexpr uint32_t ID_PV = idesc_bf16(128, DB, 0, 1);  // P (TMEM) x V (MN-major)
-        int halves = 0, cleans = 0;
+        int quarters = 0, cleans = 0;
         segments([&](int n, int a, int b, int qa, int qb) {
             chunks(a, b, [&](int base, int rows, int i, int nch) {
-                const int st = it % C::stages;
-                const uint32_t tw = sbase + st * C::stage_bytes, tv = tw + C::wr_bytes, tr = sbase + C::off_rd;
-                wait(ctl.full[st], (it / C::stages) & 1);
+                const int st = it % C::stages, full_phase = (it / C::stages) & 1;
+                wait(ctl.full[st], full_phase);
                 if (C::out) wait(ctl.rd_full, it & 1);
                 if (rows < kC) {
                     wait(ctl.clean, cleans & 1);
                     ++cleans;
                 }
-                if (C::out) {
-                    if (it > 0) wait(ctl.pv_done, (it - 1) & 1);  // P's columns are A's
-                    tc_fence_after();
-                    if (elect_one_sync() && !*dead) {
-#pragma unroll
-                        for (int kk = 0; kk < DA / 16; ++kk) {
-                            const uint32_t off = (kk >> 2) * kBox + (kk & 3) * 32;
-                            tc_mma_ss(tmem + C::col_a, sdesc_sw128(tr + off, 16, 1024), sdesc_sw128(tw + off, 16, 1024), ID_A,
-                                      kk > 0);
-                        }
-                        if (M != DQ) tc_commit(smem_u32(&ctl.a_full));
-                    }
-                    __syncwarp();
-                    if constexpr (M == DQ) {  // Q K^T beside it, in O2's columns
-                        wait(ctl.ext_full, it & 1);
-                        if (it > 0) wait(ctl.o_free, (it - 1) & 1);
+                // one instance per stage: every descriptor is then a constant of the CTA
+                auto run = [&](auto stage) {
+                    constexpr uint32_t S = decltype(stage)::value;
+                    const uint32_t tw = sbase + S * C::stage_bytes, tv = tw + C::wr_bytes, tr = sbase + C::off_rd;
+                    if (C::out) {
+                        if (it > 0) wait(ctl.pv_done, (it - 1) & 1);  // P's columns are A's
                         tc_fence_after();
-                        if (elect_one_sync() && !*dead) {
-                            const uint32_t te = sbase + C::off_ext;
+                        if (elect_one_sync()) {
 #pragma unroll
-                            for (int kk = 0; kk < DB / 16; ++kk) {
+                            for (int kk = 0; kk < DA / 16; ++kk) {
                                 const uint32_t off = (kk >> 2) * kBox + (kk & 3) * 32;
-                                tc_mma_ss(tmem + C::col_o2, sdesc_sw128(te + off, 16, 1024), sdesc_sw128(tv + off, 16, 1024),
+                                tc_mma_ss(tmem + C::col_a, sdesc_sw128(tr + off, 16, 1024), sdesc_sw128(tw + off, 16, 1024),
                                           ID_A, kk > 0);
                             }
-                            tc_commit(smem_u32(&ctl.a_full));
+                            if (M != DQ) tc_commit(smem_u32(&ctl.a_full));
+                        }
+                        __syncwarp();
+                        if constexpr (M == DQ) {  // Q K^T beside it, in O2's columns
+                            wait(ctl.ext_full, it & 1);
+                            if (it > 0) wait(ctl.o_free, (it - 1) & 1);
+                            tc_fence_after();
+                            if (elect_one_sync()) {
+                                const uint32_t te = sbase + C::off_ext;
+#pragma unroll
+                                for (int kk = 0; kk < DB / 16; ++kk) {
+                                    const uint32_t off = (kk >> 2) * kBox + (kk & 3) * 32;
+                                    tc_mma_ss(tmem + C::col_o2, sdesc_sw128(te + off, 16, 1024),
+                                              sdesc_sw128(tv + off, 16, 1024), ID_A, kk > 0);
+                                }
+                                tc_commit(smem_u32(&ctl.a_full));
+                            }
+                            __syncwarp();
+                        }
+                    }
+                    wait(ctl.s_full, it & 1);
+                    if (C::out) {
+                        if (it > 0) wait(ctl.o_free, (it - 1) & 1);
+                        tc_fence_after();
+                        if (elect_one_sync()) {
+#pragma unroll
+                            for (int kk = 0; kk < DA / 16; ++kk)
+                                tc_mma_ss(tmem + C::col_o1, sdesc_sw128(tr + (kk >> 2) * kBox + (kk & 3) * 32, 16, 1024),
+                                          sdesc_sw128(sbase + C::off_sb + 2048 * kk, DA * 128, 1024), ID_O1, kk > 0);
+                            tc_commit(smem_u32(&ctl.rd_free));
                         }
                         __syncwarp();
                     }
-                }
-                wait(ctl.s_full, it & 1);
-                if (C::out) {
-                    if (it > 0) wait(ctl.o_free, (it - 1) & 1);
-                    tc_fence_after();
-                    if (elect_one_sync() && !*dead) {
+                    const int nq = (rows + 31) / 32;
+                    auto quarter = [&](int qq, auto buffer) {
+                        constexpr uint32_t B = decltype(buffer)::value;
+                        wait(ctl.vb_full[B], (quarters >> 1) & 1);
+                        tc_fence_after();
+                        if (elect_one_sync()) {
+                            const uint32_t vb = sbase + C::off_vb + B * C::vb_bytes;
 #pragma unroll
-                        for (int kk = 0; kk < DA / 16; ++kk)
-                            tc_mma_ss(tmem + C::col_o1, sdesc_sw128(tr + (kk >> 2) * kBox + (kk & 3) * 32, 16, 1024),
-                                      sdesc_sw128(sbase + C::off_sb + 2048 * kk, DA * 128, 1024), ID_O1, kk > 0);
-                        tc_commit(smem_u32(&ctl.rd_free));
-                    }
-                    __syncwarp();
-                }
-                const int nh = rows > 64 ? 2 : 1;
-                for (int hh = 0; hh < nh; ++hh) {
-                    wait(ctl.vb_full, halves & 1);
-                    tc_fence_after();
-                    if (elect_one_sync() && !*dead) {
-                        const uint32_t vb = sbase + C::off_vb;
+                            for (int part = 0; part < 2; ++part)
 #pragma unroll
-                        for (int part = 0; part < 2; ++part)
-#pragma unroll
-                            for (int kk = 0; kk < 4; ++kk)
-                                tc_mma_ss(tmem + C::col_s, sdesc_sw128(tw + 8192 * hh + 2048 * kk, kBox, 1024),
-                                          sdesc_sw128(vb + part * C::vb_part + 2048 * kk, 8192, 1024), ID_KV, 1u);
-                        tc_commit(smem_u32(&ctl.vb_free));
-                        if (hh == nh - 1) {
-                            tc_commit(smem_u32(&ctl.kv_done));
-                            if (C::sum) tc_commit(smem_u32(&ctl.free[st]));
+                                for (int kk = 0; kk < 2; ++kk)
+                                    tc_mma_ss(tmem + C::col_s, sdesc_sw128(tw + 4096 * qq + 2048 * kk, kBox, 1024),
+                                              sdesc_sw128(vb + part * C::vb_part + 2048 * kk, 4096, 1024), ID_KV, 1u);
+                            tc_commit(smem_u32(&ctl.vb_free[B]));
+                            if (qq == nq - 1) {
+                                tc_commit(smem_u32(&ctl.kv_done));
+                                if (C::sum) tc_commit(smem_u32(&ctl.free[S]));
+                            }
                         }
+                        __syncwarp();
+                        ++quarters;
+                    };
+                    for (int qq = 0; qq < nq; ++qq) {
+                        if (quarters & 1) quarter(qq, std::integral_constant<int, 1>());
+                        else quarter(qq, std::integral_constant<int, 0>());
                     }
-                    __syncwarp();
-                    ++halves;
-                }
-                if (C::out) {
-                    wait(ctl.p_full, it & 1);
-                    tc_fence_after();
-                    if (elect_one_sync() && !*dead) {
-                        const int steps = (rows + 15) / 16;
-                        for (int kk = 0; kk < steps; ++kk)
-                            tc_mma_ts(tmem + C::col_o2, tmem + C::col_a + 8 * kk, sdesc_sw128(tv + 2048 * kk, kBox, 1024), ID_PV,
-                                      kk > 0);
-                        tc_commit(smem_u32(&ctl.pv_done));
-                        tc_commit(smem_u32(&ctl.free[st]));
+                    if (C::out) {
+                        wait(ctl.p_full, it & 1);
+                        tc_fence_after();
+                        if (elect_one_sync()) {
+                            const int steps = (rows + 15) / 16;
+                            if (steps == kC / 16) {
+#pragma unroll
+                                for (int kk = 0; kk < kC / 16; ++kk)
+                                    tc_mma_ts(tmem + C::col_o2, tmem + C::col_a + 8 * kk, sdesc_sw128(tv + 2048 * kk, kBox, 1024),
+                                              ID_PV, kk > 0);
+                            } else {
+                                for (int kk = 0; kk < steps; ++kk)
+                                    tc_mma_ts(tmem + C::col_o2, tmem + C::col_a + 8 * kk, sdesc_sw128(tv + 2048 * kk, kBox, 1024),
+                                              ID_PV, kk > 0);
+                            }
+                            tc_commit(smem_u32(&ctl.pv_done));
+                            tc_commit(smem_u32(&ctl.free[S]));
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
-                }
+                };
+                if (C::stages == 1 || st == 0) run(std::integral_constant<int, 0>());
+                else if (C::stages == 2 || st == 1) run(std::integral_constant<int, 1>());
+                else run(std::integral_constant<int, 2>());
                 ++it;
             });
         });
