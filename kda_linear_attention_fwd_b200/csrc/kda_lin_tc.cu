@@ -67,7 +67,7 @@ using namespace sm100;
 
 constexpr int kC = 128;             // tokens per chunk
 constexpr int kBox = 64 * kC * 2;   // bytes of one TMA box: 64 channels x 128 tokens
-constexpr int kWarps = 18;
+constexpr int kWarps = 22;
 constexpr int kThreads = 32 * kWarps;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -77,49 +77,59 @@ struct Maps {
     CUtensorMap rd, wr, val, ext;
 };
 
+constexpr int kMaxSlots = 8;  // of the ring; more would let a chunk's V arrive too early (see clean)
+
+template <bool DQ>
+struct Ctl {
+    unsigned long long full[kMaxSlots], free[kMaxSlots];  // the ring's slots
+    unsigned long long a_full[2];         // A is in TMEM (two buffers)
+    unsigned long long p_full[2];         // P is in TMEM, in A's place
+    unsigned long long s_full;            // the scaled state and its copy are in place
+    unsigned long long vb_full[2], vb_free[2];  // the hi/lo quarters, alternating
+    unsigned long long kv_done;           // the state has this chunk's writes
+    unsigned long long qs_done;           // R S is in O
+    unsigned long long o_scaled;          // and multiplied by its rows' decays
+    unsigned long long pv_done;           // O is complete
+    unsigned long long o_free;            // O has been read
+    unsigned long long clean[2];          // rows behind a short chunk's end are zero (even, odd chunks)
+    unsigned long long end;
+    int dead;
+    uint32_t tmem;
+    // P: c within the 32-token block, exp(to the block's far end), block sums.  In two
+    // buffers where no barrier of the warpgroup follows their last use
+    alignas(16) float pc[DQ ? 1 : 2][kC], pe[DQ ? 1 : 2][kC];
+    float pt[2][4];
+    float ot[2][8];                        // O: block sums; DK, S: partial products with the checkpoint
+    float xs[2][4];                        // DK, O: block sums
+};
+
 template <int DA, int DB, int M>
 struct Cfg {
     static constexpr bool rev = M == SUMR || M == DK || M == DV;
     static constexpr bool sum = M == SUM || M == SUMR;
     static constexpr bool out = !sum;
-    static constexpr int stages = sum ? 3 : M == DQ ? 1 : 2;
-    static constexpr int wr_bytes = DA / 64 * kBox, val_bytes = DB / 64 * kBox;
-    static constexpr int stage_bytes = wr_bytes + val_bytes;
-    static constexpr int rd_bytes = out ? wr_bytes : 0;
+    // Shared memory: a ring of tiles in the order in which their products are
+    // done with them -- [E,] R, W, V of each chunk (W, V in a summary) -- then
+    // the hi/lo buffers and the state copy
+    static constexpr int tiles = sum ? 2 : M == DQ ? 4 : 3;
+    static constexpr int tE = 0, tR = M == DQ ? 1 : 0, tW = sum ? 0 : tR + 1, tV = tW + 1;
+    static constexpr int a_bytes = DA / 64 * kBox, b_bytes = DB / 64 * kBox;  // tiles of R, W and of V, E
+    static constexpr int slot_bytes = a_bytes > b_bytes ? a_bytes : b_bytes;
     static constexpr int vb_part = DB / 64 * (32 * 128);  // 32 tokens of hi or lo
     static constexpr int vb_bytes = 2 * vb_part;
     static constexpr int sb_bytes = out ? DB / 64 * (DA * 128) : 0;
-    static constexpr int off_rd = stages * stage_bytes;
-    static constexpr int off_vb = off_rd + rd_bytes;
+    static constexpr int xc_bytes = M == DQ ? 10 * 32 * 4 : 0;  // DQ: column sums of X, per warp and block
+    static constexpr int fit = (232448 - 2 * vb_bytes - sb_bytes - xc_bytes - (int)sizeof(Ctl<M == DQ>)) / slot_bytes;
+    static constexpr int slots = fit < kMaxSlots ? fit : kMaxSlots;
+    static_assert(slots > tiles, "ring");
+    static constexpr int off_vb = slots * slot_bytes;
     static constexpr int off_sb = off_vb + 2 * vb_bytes;
-    static constexpr int off_ext = off_sb + sb_bytes;
-    static constexpr int ext_bytes = M == DQ ? DB / 64 * kBox : 0;
-    static constexpr int off_xc = off_ext + ext_bytes;  // DQ: column sums of X, per warp
-    static constexpr int off_ctl = off_xc + (M == DQ ? 4 * kC * 4 : 0);
+    static constexpr int off_xc = off_sb + sb_bytes;
+    static constexpr int off_ctl = off_xc + xc_bytes;
+    static constexpr int bytes = off_ctl + (int)sizeof(Ctl<M == DQ>);
     // TMEM columns
-    static constexpr uint32_t col_s = 0, col_a = 128, col_o1 = 256, col_o2 = 384;
+    static constexpr uint32_t col_s = 0, col_a = 128, col_o = 384;  // A twice (DQ: A and Q K^T)
     static constexpr uint32_t cols = out ? 512 : 128;
-};
-
-struct Ctl {
-    unsigned long long full[3], free[3];  // the stages of W and V
-    unsigned long long rd_full, rd_free;  // R; rd_free also releases the state copy
-    unsigned long long a_full;            // A is in TMEM
-    unsigned long long p_full;            // P is in TMEM
-    unsigned long long s_full;            // the scaled state and its copy are in place
-    unsigned long long vb_full[2], vb_free[2];  // the hi/lo quarters, alternating
-    unsigned long long kv_done;           // the state has this chunk's writes
-    unsigned long long pv_done;           // O1 and O2 are complete
-    unsigned long long o_free;            // O1 and O2 have been read
-    unsigned long long clean;             // rows behind a short chunk's end are zero
-    unsigned long long ext_full, end;
-    int dead;
-    uint32_t tmem;
-    alignas(16) float pc[2][kC], pe[2][kC];
-    float pt[2][4];                         // P: c within the 32-token block, exp(to the block's far end); block sums
-    float vw[kC], vt[2][4];                // V: w_s, block sums
-    float xs[2][4];                        // DK, O: block sums
-    float ot[2][8];                        // O: block sums; DK, S: partial products with the checkpoint
 };
 
 // 32 bytes of one row: one whole sector when the address allows it
@@ -161,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                                                          const __grid_constant__ Maps maps) {
     using C = Cfg<DA, DB, M>;
     extern __shared__ __align__(1024) unsigned char sm[];  // the swizzle's period
-    Ctl &ctl = *reinterpret_cast<Ctl *>(sm + C::off_ctl);
+    Ctl<M == DQ> &ctl = *reinterpret_cast<Ctl<M == DQ> *>(sm + C::off_ctl);
     const uint32_t sbase = smem_u32(sm);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, role = warp >> 2;
     const int h = blockIdx.x, w = blockIdx.y, H = p.H, N = p.num_seqs;
@@ -177,16 +187,18 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     if (tid == 32) {
-        for (int i = 0; i < 3; ++i) {
+        for (int i = 0; i < C::slots; ++i) {
             mbar_init(smem_u32(&ctl.full[i]), 1);
             mbar_init(smem_u32(&ctl.free[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&ctl.vb_full[i]), 128);
             mbar_init(smem_u32(&ctl.vb_free[i]), 1);
+            mbar_init(smem_u32(&ctl.a_full[i]), 1);
+            mbar_init(smem_u32(&ctl.p_full[i]), 128);
         }
-        unsigned long long *one[] = {&ctl.rd_full, &ctl.rd_free, &ctl.a_full, &ctl.kv_done, &ctl.pv_done, &ctl.ext_full, &ctl.end};
-        unsigned long long *wg[] = {&ctl.p_full, &ctl.s_full, &ctl.o_free, &ctl.clean};
+        unsigned long long *one[] = {&ctl.qs_done, &ctl.kv_done, &ctl.pv_done, &ctl.end};
+        unsigned long long *wg[] = {&ctl.s_full, &ctl.o_scaled, &ctl.o_free, &ctl.clean[0], &ctl.clean[1]};
         for (auto *b : one) mbar_init(smem_u32(b), 1);
         for (auto *b : wg) mbar_init(smem_u32(b), 128);
         ctl.dead = (sbase & 1023u) != 0;  // never: the tiles would be read wrongly
@@ -206,6 +218,9 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
         }
     };
     auto arrive = [&](unsigned long long &bar) { mbar_arrive(smem_u32(&bar)); };
+    // tile j of chunk c in the ring
+    auto slot = [&](int c, int j) { return (c * C::tiles + j) % C::slots; };
+    auto phase = [&](int c, int j) -> uint32_t { return (uint32_t)((c * C::tiles + j) / C::slots) & 1u; };
     auto load_g = [&](int t) -> float {  // in powers of two
         const size_t at = p.g_per_head ? (size_t)h : (size_t)t * H + h;
         return fmaxf(__bfloat162float(((const bf16 *)p.g)[at]), kMinG) * kLog2e;
@@ -271,13 +286,13 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
         // --------------------------------------------------------------- P
         if (C::out) {
             const int row = tid;  // 32 * warp + lane
-            const uint32_t ta = tmem + ((uint32_t)(32 * warp) << 16) + C::col_a;
+            const uint32_t ta0 = tmem + ((uint32_t)(32 * warp) << 16) + C::col_a;
             const float sc = p.rd_scale * p.wr_scale;
             segments([&](int n, int a, int b, int qa, int qb) {
                 float gx = 0.f;
                 chunks(a, b, [&](int base, int rows, int i, int nch) {
                     if (i == 0) gx = row_g(base, rows, row, qb);
-                    const int pb = it & 1;
+                    const int pb = M == DQ ? 0 : it & 1;
                     const float c = C::rev ? scan_down(gx, lane) : scan_up(gx, lane);
                     const float tot = __shfl_sync(0xffffffffu, c, C::rev ? 0 : 31);
                     ctl.pc[pb][row] = c;
@@ -285,10 +300,12 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                     if (lane == 0) ctl.pt[pb][warp] = tot;
                     if (i + 1 < nch) gx = row_g(next_base(base), min(kC, b - next_base(base)), row, qb);
                     bar_sync(1, 128);
-                    wait(ctl.a_full, it & 1);
+                    const int ab = M == DQ ? 0 : it & 1;
+                    const uint32_t ta = ta0 + 128 * ab;
+                    wait(ctl.a_full[ab], (M == DQ ? it : it >> 1) & 1);
                     tc_fence_after();
                     float xr = 0.f;  // DQ: this row's sum of X over earlier tokens
-                    float *xc = reinterpret_cast<float *>(sm + C::off_xc) + warp * kC;
+                    float *xc = reinterpret_cast<float *>(sm + C::off_xc) + 16 * warp * (warp + 1);  // blocks 0 .. warp
                     // block by block upwards: P's block lies in columns 16 blk .. + 15, which hold products of
                     // block blk / 2, read by then or not needed by this warp
 #pragma unroll 1
@@ -300,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                         } else {
                             uint32_t r[32];
                             uint32_t y[M == DQ ? 32 : 1];
-                            if constexpr (M == DQ) tmem_ld32(ta - C::col_a + C::col_o2 + 32 * blk, y);
+                            if constexpr (M == DQ) tmem_ld32(ta + 128 + 32 * blk, y);
                             tmem_ld32_wait(ta + 32 * blk, r);
                             if (blk == warp) {
 #pragma unroll
@@ -365,12 +382,12 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                     }
                     tc_wait_st();
                     tc_fence_before();
-                    arrive(ctl.p_full);
+                    arrive(ctl.p_full[ab]);
                     if constexpr (M == DQ) {
                         // pairs (s, u), u < s, whose later token is this row less those whose earlier one is
                         bar_sync(1, 128);
                         const float *all = reinterpret_cast<const float *>(sm + C::off_xc);
-                        for (int j = warp; j < 4; ++j) xr -= all[j * kC + row];
+                        for (int j = warp; j < 4; ++j) xr -= all[16 * j * (j + 1) + row];
                         if (row < rows) p.xdot[(size_t)(base + row) * H + h] = xr;
                     }
                     ++it;
@@ -499,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                     // pairs whose tokens lie on either side of the chunk: the same for its every token
                     dot = warp_sum(dot);
                     if (lane == 0) ctl.ot[it & 1][4 + wl] = dot;
-                    bar_sync(4, 128);
+                    bar_sync(5, 128);
                     if (row < rows) {
                         const float *d = &ctl.ot[it & 1][4];
                         p.across[(size_t)(base + row) * H + h] = ((d[0] + d[1]) + (d[2] + d[3])) * f * exp2f(load_g(base));
@@ -536,47 +553,71 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
             if (C::sum && row == 0) p.gamma[(size_t)w * H + h] = from_win ? gamma : 0.f;
         });
         tc_fence_before();
-    } else if (role == 2) {
-        // --------------------------------------------------------------- V
-        const int vt = tid - 256, wl = warp & 3;
+    } else if (role == 2 || role == 3) {
+        // --------------------------------------------------------------- V (two groups, every other quarter each)
+        const int grp = role - 2, wl = warp & 3;
         int quarters = 0;
         segments([&](int n, int a, int b, int qa, int qb) {
-            float gx = 0.f;
+            float gx[4] = {0.f, 0.f, 0.f, 0.f};
             chunks(a, b, [&](int base, int rows, int i, int nch) {
-                if (i == 0) gx = row_g(base, rows, vt, qb);
-                const int pb = it & 1, st = it % C::stages;
-                // the decays behind this row, in the order of the pass
-                const float inc = C::rev ? scan_up(gx, lane) : scan_down(gx, lane);
-                float exc = C::rev ? __shfl_up_sync(0xffffffffu, inc, 1) : __shfl_down_sync(0xffffffffu, inc, 1);
-                if (lane == (C::rev ? 0 : 31)) exc = 0.f;
-                if (lane == (C::rev ? 31 : 0)) ctl.vt[pb][wl] = inc;
-                if (i + 1 < nch) gx = row_g(next_base(base), min(kC, b - next_base(base)), vt, qb);
-                bar_sync(2, 128);
+                if (i == 0)
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (C::rev ? j < wl : j > wl) exc += ctl.vt[pb][j];
-                ctl.vw[vt] = exp2f(exc) * p.wr_scale;
-                wait(ctl.full[st], (it / C::stages) & 1);
-                unsigned char *tw = sm + st * C::stage_bytes, *tv = tw + C::wr_bytes;
-                if (rows < kC) {
-                    // the MMA warp has passed the short chunk before this one
-                    if (quarters > 0) wait(ctl.vb_free[(quarters - 1) & 1], ((quarters - 1) >> 1) & 1);
-                    // rows behind the end hold other tokens: zero, whatever they are
-                    if (vt >= rows) {
+                    for (int x = 0; x < 4; ++x) gx[x] = row_g(base, rows, 32 * x + lane, qb);
+                const int nq = (rows + 31) / 32;
+                // this group's quarters: f0 and f0 + 2; the decays behind their rows, in the order of the pass
+                const int f0 = (quarters & 1) ^ grp;
+                float wq[2];
+                {
+                    float tot[4];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) tot[x] = warp_sum(gx[x]);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float g1 = f0 ? gx[2 * e + 1] : gx[2 * e];
+                        const float inc = C::rev ? scan_up(g1, lane) : scan_down(g1, lane);
+                        float exc = C::rev ? __shfl_up_sync(0xffffffffu, inc, 1) : __shfl_down_sync(0xffffffffu, inc, 1);
+                        if (lane == (C::rev ? 0 : 31)) exc = 0.f;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (C::rev ? j < f0 + 2 * e : j > f0 + 2 * e) exc += tot[j];
+                        wq[e] = exp2f(exc) * p.wr_scale;
+                    }
+                }
+                if (i + 1 < nch)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) gx[x] = row_g(next_base(base), min(kC, b - next_base(base)), 32 * x + lane, qb);
+                unsigned char *tw = sm + slot(it, C::tW) * C::slot_bytes, *tv = sm + slot(it, C::tV) * C::slot_bytes;
+                wait(ctl.full[slot(it, C::tV)], phase(it, C::tV));
+                if (rows < kC && ((quarters + nq - 1) & 1) == grp) {
+                    // The last quarter's rows behind the end hold other tokens: zero, whatever they are (the
+                    // quarters behind it are not read); each thread the channels that it reads below.  The MMA
+                    // warp has passed its wait for the short chunk two before this one, if that was one: this
+                    // chunk's V lies in a slot (of kMaxSlots at most) whose last tile was released behind it.
+                    wait(ctl.full[slot(it, C::tW)], phase(it, C::tW));
+                    const int r = 32 * (nq - 1) + lane;
+                    if (r >= rows) {
                         const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-                        for (int c = 0; c < (DA + DB) / 8; ++c)
-                            *reinterpret_cast<uint4 *>(tw + (c >> 3) * kBox + vt * 128 + (c & 7) * 16) = z;
+#pragma unroll
+                        for (int c0 = 0; c0 < DA / 32; ++c0) {
+                            const int c = wl * (DA / 32) + c0;
+                            *reinterpret_cast<uint4 *>(tw + (c >> 3) * kBox + r * 128 + (c & 7) * 16) = z;
+                        }
+#pragma unroll
+                        for (int c0 = 0; c0 < DB / 32; ++c0) {
+                            const int c = wl * (DB / 32) + c0;
+                            *reinterpret_cast<uint4 *>(tv + (c >> 3) * kBox + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = z;
+                        }
                     }
                     fence_async_smem();
-                    arrive(ctl.clean);
+                    arrive(ctl.clean[it & 1]);
                 }
-                bar_sync(2, 128);  // vw, and the zeros
                 // 32 tokens at a time: lane = token, warp = quarter of the channels
-                for (int qq = 0; qq < (rows + 31) / 32; ++qq, ++quarters) {
+                for (int qq = 0; qq < nq; ++qq, ++quarters) {
                     const int vb = quarters & 1;
+                    if (vb != grp) continue;
                     if (quarters > 1) wait(ctl.vb_free[vb], ((quarters >> 1) - 1) & 1);
                     const int r = 32 * qq + lane;
-                    const float f = ctl.vw[r];
+                    const float f = (qq >> 1) ? wq[1] : wq[0];
                     const float2 f2 = make_float2(f, f);
                     constexpr int CH = DB / 32;  // 16-byte pieces
 #pragma unroll
@@ -602,13 +643,13 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                 ++it;
             });
         });
-    } else if (role == 3) {
+    } else if (role == 4) {
         // --------------------------------------------------------------- O
         if (C::out) {
-            const int row = tid - 384, wl = warp & 3;
+            const int row = tid - 512, wl = warp & 3;
             const uint32_t lane_off = (uint32_t)(32 * wl) << 16;
             const bool al32 = ((uintptr_t)p.out & 31) == 0;
-            const uint32_t to1 = tmem + lane_off + C::col_o1, to2 = tmem + lane_off + C::col_o2;
+            const uint32_t to = tmem + lane_off + C::col_o;
             segments([&](int n, int a, int b, int qa, int qb) {
                 float gx = 0.f;
                 chunks(a, b, [&](int base, int rows, int i, int nch) {
@@ -617,33 +658,41 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                     float c = C::rev ? scan_down(gx, lane) : scan_up(gx, lane);
                     if (lane == (C::rev ? 0 : 31)) ctl.ot[pb][wl] = c;
                     if (i + 1 < nch) gx = row_g(next_base(base), min(kC, b - next_base(base)), row, qb);
-                    bar_sync(3, 128);
+                    bar_sync(4, 128);
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         if (C::rev ? j > wl : j < wl) c += ctl.ot[pb][j];
                     const float f = exp2f(c) * p.rd_scale;
-                    wait(ctl.pv_done, it & 1);
-                    if (M == DQ) wait(ctl.ext_full, it & 1);
+                    // the state's part, scaled by its rows' decays before P V is added to it
+                    wait(ctl.qs_done, it & 1);
                     tc_fence_after();
                     const size_t at = ((size_t)(base + row) * H + h) * DB;
+                    const float2 f2 = make_float2(f, f);
                     float xi = 0.f;  // gradient passes: the state's part of out . ext
 #pragma unroll 1
                     for (int cb = 0; cb < DB / 32; ++cb) {
-                        uint32_t x[32], y[32];
-                        tmem_ld32(to1 + 32 * cb, x);
-                        tmem_ld32_wait(to2 + 32 * cb, y);
+                        uint32_t x[32];
+                        tmem_ld32(to + 32 * cb, x);
+                        uint4 e4[(M == DQ || M == DK) ? 4 : 1];
                         if constexpr (M == DQ || M == DK) {
-                            uint4 e4[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                e4[e] = row < rows ? *reinterpret_cast<const uint4 *>(
+                                                         (const bf16 *)p.ext +
+                                                         ((size_t)(base + row) * (H / p.ext_div) + h / p.ext_div) * DB + 32 * cb + 8 * e)
+                                                   : make_uint4(0u, 0u, 0u, 0u);
+                        }
+                        tc_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const float2 v = f2mul(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), f2);
+                            x[2 * e] = __float_as_uint(v.x);
+                            x[2 * e + 1] = __float_as_uint(v.y);
+                        }
+                        tmem_st32(to + 32 * cb, x);
+                        if constexpr (M == DQ || M == DK) {
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                if (M == DQ)
-                                    e4[e] = *reinterpret_cast<const uint4 *>(sm + C::off_ext + (cb >> 1) * kBox + row * 128 +
-                                                                             ((((cb & 1) * 4 + e) ^ (row & 7)) << 4));
-                                else
-                                    e4[e] = row < rows ? *reinterpret_cast<const uint4 *>(
-                                                             (const bf16 *)p.ext +
-                                                             ((size_t)(base + row) * (H / p.ext_div) + h / p.ext_div) * DB + 32 * cb + 8 * e)
-                                                       : make_uint4(0u, 0u, 0u, 0u);
                                 const uint32_t es[4] = {e4[e].x, e4[e].y, e4[e].z, e4[e].w};
 #pragma unroll
                                 for (int k = 0; k < 4; ++k) {
@@ -653,35 +702,40 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                                 }
                             }
                         }
+                    }
+                    tc_wait_st();
+                    tc_fence_before();
+                    arrive(ctl.o_scaled);
+                    wait(ctl.pv_done, it & 1);
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int cb = 0; cb < DB / 32; ++cb) {
+                        uint32_t x[32];
+                        tmem_ld32_wait(to + 32 * cb, x);
                         if (cb == DB / 32 - 1) {
                             tc_fence_before();
                             arrive(ctl.o_free);
                         }
-                        float2 o[16];
-#pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            o[e] = f2fma(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), make_float2(f, f),
-                                         make_float2(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1])));
                         if (row < rows) {
                             if ((M == DQ || M == DK) && p.out_f32) {
-                                float *dst = (float *)p.out + at + 32 * cb;
+                                uint4 *dst = reinterpret_cast<uint4 *>((float *)p.out + at + 32 * cb);
 #pragma unroll
-                                for (int q = 0; q < 8; ++q)
-                                    reinterpret_cast<float4 *>(dst)[q] = make_float4(o[2 * q].x, o[2 * q].y, o[2 * q + 1].x, o[2 * q + 1].y);
+                                for (int q = 0; q < 8; ++q) dst[q] = make_uint4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
                             } else {
                                 bf16 *dst = (bf16 *)p.out + at + 32 * cb;
 #pragma unroll
                                 for (int q = 0; q < 2; ++q) {
                                     uint32_t v[8];
 #pragma unroll
-                                    for (int e = 0; e < 8; ++e) v[e] = pack_bf16(o[8 * q + e]);
+                                    for (int e = 0; e < 8; ++e)
+                                        v[e] = pack_bf16(__uint_as_float(x[16 * q + 2 * e]), __uint_as_float(x[16 * q + 2 * e + 1]));
                                     st_global32(dst + 16 * q, v, al32);
                                 }
                             }
                         }
                     }
                     if constexpr (M == DQ) {
-                        if (row < rows) p.xstate[(size_t)(base + row) * H + h] = f * xi;
+                        if (row < rows) p.xstate[(size_t)(base + row) * H + h] = xi;
                     }
                     if constexpr (M == DK) {
                         // dg but for the pairs across the chunk: the pairs inside it and those with an
@@ -689,11 +743,11 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                         float u = 0.f;
                         const size_t th = (size_t)(base + row) * H + h;
                         if (row < rows) u = p.xdot[th] + p.xstate[th];
-                        const float ik = row < rows ? f * xi : 0.f;
+                        const float ik = row < rows ? xi : 0.f;
                         float suf = scan_down(u, lane), pre = scan_up(ik, lane) - ik;
                         if (lane == 0) ctl.xs[0][wl] = suf;
                         if (lane == 31) ctl.xs[1][wl] = pre + ik;
-                        bar_sync(3, 128);
+                        bar_sync(4, 128);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             if (j > wl) suf += ctl.xs[0][j];
@@ -705,180 +759,166 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                 });
             });
         }
-    } else if (warp == 16) {
+    } else if (warp == 20) {
         // --------------------------------------------------------------- TMA
-        const int hr = C::out ? h / p.rd_div : 0, hw = h / p.wr_div, hv = h / p.val_div;
+        const int hr = C::out ? h / p.rd_div : 0, hw = h / p.wr_div, hv = h / p.val_div, he = M == DQ ? h / p.ext_div : 0;
         segments([&](int n, int a, int b, int qa, int qb) {
             chunks(a, b, [&](int base, int rows, int i, int nch) {
-                const int st = it % C::stages;
-                if (it >= C::stages) wait(ctl.free[st], (it / C::stages - 1) & 1);
-                if (elect_one_sync() && !*dead) {
-                    const uint32_t bar = smem_u32(&ctl.full[st]), dst = sbase + st * C::stage_bytes;
-                    mbar_arrive_expect_tx(bar, C::stage_bytes);
-#pragma unroll
-                    for (int x = 0; x < DA / 64; ++x) tma_load_3d(dst + x * kBox, &maps.wr, 64 * x, hw, base, bar);
-#pragma unroll
-                    for (int x = 0; x < DB / 64; ++x)
-                        tma_load_3d(dst + C::wr_bytes + x * kBox, &maps.val, 64 * x, hv, base, bar);
-                }
-                __syncwarp();
-                if (C::out) {
-                    if (it > 0) wait(ctl.rd_free, (it - 1) & 1);
+                auto load = [&](int j, const CUtensorMap &map, int head, int boxes) {
+                    const int sl = slot(it, j);
+                    if (it * C::tiles + j >= C::slots) wait(ctl.free[sl], phase(it, j) ^ 1u);
                     if (elect_one_sync() && !*dead) {
-                        const uint32_t bar = smem_u32(&ctl.rd_full);
-                        mbar_arrive_expect_tx(bar, C::rd_bytes);
-#pragma unroll
-                        for (int x = 0; x < DA / 64; ++x) {
-                            tma_load_3d(sbase + C::off_rd + x * kBox, &maps.rd, 64 * x, hr, base, bar);
-                            if (i + 1 < nch) tma_prefetch_3d(&maps.rd, 64 * x, hr, next_base(base));
+                        const uint32_t bar = smem_u32(&ctl.full[sl]), dst = sbase + sl * C::slot_bytes;
+                        mbar_arrive_expect_tx(bar, boxes * kBox);
+                        for (int x = 0; x < boxes; ++x) {
+                            tma_load_3d(dst + x * kBox, &map, 64 * x, head, base, bar);
+                            if (i + 1 < nch) tma_prefetch_3d(&map, 64 * x, head, next_base(base));
                         }
                     }
                     __syncwarp();
-                }
-                if constexpr (M == DQ) {
-                    if (it > 0) wait(ctl.o_free, (it - 1) & 1);
-                    if (elect_one_sync() && !*dead) {
-                        const uint32_t bar = smem_u32(&ctl.ext_full);
-                        mbar_arrive_expect_tx(bar, C::ext_bytes);
-#pragma unroll
-                        for (int x = 0; x < DB / 64; ++x) {
-                            tma_load_3d(sbase + C::off_ext + x * kBox, &maps.ext, 64 * x, h / p.ext_div, base, bar);
-                            if (i + 1 < nch) tma_prefetch_3d(&maps.ext, 64 * x, h / p.ext_div, next_base(base));
-                        }
-                        if (i + 1 < nch) {  // one stage only: the next chunk's tiles at least to L2
-#pragma unroll
-                            for (int x = 0; x < DA / 64; ++x) tma_prefetch_3d(&maps.wr, 64 * x, hw, next_base(base));
-#pragma unroll
-                            for (int x = 0; x < DB / 64; ++x) tma_prefetch_3d(&maps.val, 64 * x, hv, next_base(base));
-                        }
-                    }
-                    __syncwarp();
-                }
+                };
+                if (M == DQ) load(C::tE, maps.ext, he, DB / 64);
+                if (C::out) load(C::tR, maps.rd, hr, DA / 64);
+                load(C::tW, maps.wr, hw, DA / 64);
+                load(C::tV, maps.val, hv, DB / 64);
                 ++it;
             });
         });
-        if (*dead) {  // loads in flight land before the CTA ends (bounded)
-            for (int x = max(0, it - C::stages); x < it; ++x)
-                mbar_wait(smem_u32(&ctl.full[x % C::stages]), (x / C::stages) & 1);
-            if (C::out && it > 0) mbar_wait(smem_u32(&ctl.rd_full), (it - 1) & 1);
-            if (M == DQ && it > 0) mbar_wait(smem_u32(&ctl.ext_full), (it - 1) & 1);
-        }
+        if (*dead)  // loads in flight land before the CTA ends (bounded)
+            for (int x = max(0, it * C::tiles - C::slots); x < it * C::tiles; ++x)
+                mbar_wait(smem_u32(&ctl.full[x % C::slots]), (uint32_t)(x / C::slots) & 1u);
     } else {
         // --------------------------------------------------------------- MMA
         constexpr uint32_t ID_A = idesc_bf16(128, 128, 0, 0);  // R (K-major) x W (K-major)
-        constexpr uint32_t ID_O1 = idesc_bf16(128, DB, 0, 1);  // R (K-major) x S (MN-major)
+        constexpr uint32_t ID_O = idesc_bf16(128, DB, 0, 1);  // R (K-major) x S (MN-major)
         constexpr uint32_t ID_KV = idesc_bf16(128, DB, 1, 1);  // W^T (MN-major) x w V (MN-major)
         constexpr uint32_t ID_PV = idesc_bf16(128, DB, 0, 1);  // P (TMEM) x V (MN-major)
-        int quarters = 0, cleans = 0;
-        segments([&](int n, int a, int b, int qa, int qb) {
-            chunks(a, b, [&](int base, int rows, int i, int nch) {
-                const int st = it % C::stages, full_phase = (it / C::stages) & 1;
-                wait(ctl.full[st], full_phase);
-                if (C::out) wait(ctl.rd_full, it & 1);
-                if (rows < kC) {
-                    wait(ctl.clean, cleans & 1);
-                    ++cleans;
+        // A of a chunk is issued one chunk ahead (its operands are there by then, and P's warps
+        // need not wait for this chunk's other products); two cursors walk the chunks.
+        struct Cursor {
+            int seg, ci, nch, a, b, base, rows;
+        };
+        auto next = [&](Cursor &c) -> bool {
+            ++c.ci;
+            while (c.ci >= c.nch) {
+                if (++c.seg >= end - first) return false;
+                const int n = C::rev ? end - 1 - c.seg : first + c.seg;
+                c.a = min(max(p.cu[n], t0), t1);
+                c.b = max(c.a, min(min(p.cu[n + 1], p.T), t1));
+                c.nch = (c.b - c.a + kC - 1) / kC;
+                c.ci = 0;
+            }
+            c.base = c.a + (C::rev ? c.nch - 1 - c.ci : c.ci) * kC;
+            c.rows = min(kC, c.b - c.base);
+            return true;
+        };
+        Cursor ahead{-1, 0, 0, 0, 0, 0, 0}, cur{-1, 0, 0, 0, 0, 0, 0};
+        int quarters = 0, k = 0;  // k: chunks whose A has been issued
+        uint32_t cleans[2] = {0u, 0u};
+        auto tile = [&](int c, int j) -> uint32_t { return sbase + (uint32_t)slot(c, j) * C::slot_bytes; };
+        auto begin = [&]() {
+            if (!next(ahead)) return;
+            if (C::out) wait(ctl.full[slot(k, C::tR)], phase(k, C::tR));
+            wait(ctl.full[slot(k, C::tW)], phase(k, C::tW));
+            if (M == DQ) {
+                wait(ctl.full[slot(k, C::tE)], phase(k, C::tE));
+                wait(ctl.full[slot(k, C::tV)], phase(k, C::tV));
+            }
+            if (ahead.rows < kC) {
+                const uint32_t seen = k & 1 ? cleans[1] : cleans[0];
+                wait(ctl.clean[k & 1], seen & 1);
+                (k & 1 ? cleans[1] : cleans[0]) = seen + 1;
+            }
+            if (C::out) {
+                const int behind = M == DQ ? 1 : 2;
+                if (k >= behind) wait(ctl.pv_done, (k - behind) & 1);  // P's columns are A's
+                tc_fence_after();
+                const uint32_t tr = tile(k, C::tR), tw = tile(k, C::tW), ab = M == DQ ? 0u : (uint32_t)(k & 1);
+                const uint32_t te = M == DQ ? tile(k, C::tE) : 0u, tv = M == DQ ? tile(k, C::tV) : 0u;
+                if (elect_one_sync()) {
+#pragma unroll
+                    for (int kk = 0; kk < DA / 16; ++kk) {
+                        const uint32_t off = (kk >> 2) * kBox + (kk & 3) * 32;
+                        tc_mma_ss(tmem + C::col_a + 128 * ab, sdesc_sw128(tr + off, 16, 1024), sdesc_sw128(tw + off, 16, 1024),
+                                  ID_A, kk > 0);
+                    }
+                    if constexpr (M == DQ) {  // Q K^T beside it
+#pragma unroll
+                        for (int kk = 0; kk < DB / 16; ++kk) {
+                            const uint32_t off = (kk >> 2) * kBox + (kk & 3) * 32;
+                            tc_mma_ss(tmem + C::col_a + 128, sdesc_sw128(te + off, 16, 1024), sdesc_sw128(tv + off, 16, 1024), ID_A,
+                                      kk > 0);
+                        }
+                        tc_commit(smem_u32(&ctl.free[slot(k, C::tE)]));
+                    }
+                    tc_commit(smem_u32(&ctl.a_full[ab]));
                 }
-                // one instance per stage: every descriptor is then a constant of the CTA
-                auto run = [&](auto stage) {
-                    constexpr uint32_t S = decltype(stage)::value;
-                    const uint32_t tw = sbase + S * C::stage_bytes, tv = tw + C::wr_bytes, tr = sbase + C::off_rd;
-                    if (C::out) {
-                        if (it > 0) wait(ctl.pv_done, (it - 1) & 1);  // P's columns are A's
-                        tc_fence_after();
-                        if (elect_one_sync()) {
+                __syncwarp();
+            }
+            ++k;
+        };
+        if (M != DQ) begin();
+        while (next(cur)) {
+            if (M == DQ) begin();
+            const int rows = cur.rows, nq = (rows + 31) / 32;
+            const uint32_t tw = tile(it, C::tW);
+            wait(ctl.s_full, it & 1);
+            if (C::out) {
+                if (it > 0) wait(ctl.o_free, (it - 1) & 1);
+                tc_fence_after();
+                const uint32_t tr = tile(it, C::tR);
+                if (elect_one_sync()) {
 #pragma unroll
-                            for (int kk = 0; kk < DA / 16; ++kk) {
-                                const uint32_t off = (kk >> 2) * kBox + (kk & 3) * 32;
-                                tc_mma_ss(tmem + C::col_a, sdesc_sw128(tr + off, 16, 1024), sdesc_sw128(tw + off, 16, 1024),
-                                          ID_A, kk > 0);
-                            }
-                            if (M != DQ) tc_commit(smem_u32(&ctl.a_full));
-                        }
-                        __syncwarp();
-                        if constexpr (M == DQ) {  // Q K^T beside it, in O2's columns
-                            wait(ctl.ext_full, it & 1);
-                            if (it > 0) wait(ctl.o_free, (it - 1) & 1);
-                            tc_fence_after();
-                            if (elect_one_sync()) {
-                                const uint32_t te = sbase + C::off_ext;
+                    for (int kk = 0; kk < DA / 16; ++kk)
+                        tc_mma_ss(tmem + C::col_o, sdesc_sw128(tr + (kk >> 2) * kBox + (kk & 3) * 32, 16, 1024),
+                                  sdesc_sw128(sbase + C::off_sb + 2048 * kk, DA * 128, 1024), ID_O, kk > 0);
+                    tc_commit(smem_u32(&ctl.free[slot(it, C::tR)]));
+                    tc_commit(smem_u32(&ctl.qs_done));
+                }
+                __syncwarp();
+            }
+            for (int qq = 0; qq < nq; ++qq, ++quarters) {
+                const int vbuf = quarters & 1;
+                wait(ctl.vb_full[vbuf], (quarters >> 1) & 1);
+                tc_fence_after();
+                const uint32_t vb = sbase + C::off_vb + vbuf * C::vb_bytes;
+                if (elect_one_sync()) {
 #pragma unroll
-                                for (int kk = 0; kk < DB / 16; ++kk) {
-                                    const uint32_t off = (kk >> 2) * kBox + (kk & 3) * 32;
-                                    tc_mma_ss(tmem + C::col_o2, sdesc_sw128(te + off, 16, 1024),
-                                              sdesc_sw128(tv + off, 16, 1024), ID_A, kk > 0);
-                                }
-                                tc_commit(smem_u32(&ctl.a_full));
-                            }
-                            __syncwarp();
-                        }
+                    for (int part = 0; part < 2; ++part)
+#pragma unroll
+                        for (int kk = 0; kk < 2; ++kk)
+                            tc_mma_ss(tmem + C::col_s, sdesc_sw128(tw + 4096 * qq + 2048 * kk, kBox, 1024),
+                                      sdesc_sw128(vb + part * C::vb_part + 2048 * kk, 4096, 1024), ID_KV, 1u);
+                    tc_commit(smem_u32(&ctl.vb_free[vbuf]));
+                    if (qq == nq - 1) {
+                        tc_commit(smem_u32(&ctl.kv_done));
+                        tc_commit(smem_u32(&ctl.free[slot(it, C::tW)]));
+                        if (C::sum) tc_commit(smem_u32(&ctl.free[slot(it, C::tV)]));
                     }
-                    wait(ctl.s_full, it & 1);
-                    if (C::out) {
-                        if (it > 0) wait(ctl.o_free, (it - 1) & 1);
-                        tc_fence_after();
-                        if (elect_one_sync()) {
+                }
+                __syncwarp();
+            }
+            if (M != DQ) begin();  // the next chunk's
+            if (C::out) {
+                const uint32_t ab = M == DQ ? 0u : (uint32_t)(it & 1), tv = tile(it, C::tV);
+                wait(ctl.full[slot(it, C::tV)], phase(it, C::tV));
+                wait(ctl.p_full[ab], (M == DQ ? it : it >> 1) & 1);
+                wait(ctl.o_scaled, it & 1);
+                tc_fence_after();
+                if (elect_one_sync()) {
+                    const int steps = (rows + 15) / 16;
 #pragma unroll
-                            for (int kk = 0; kk < DA / 16; ++kk)
-                                tc_mma_ss(tmem + C::col_o1, sdesc_sw128(tr + (kk >> 2) * kBox + (kk & 3) * 32, 16, 1024),
-                                          sdesc_sw128(sbase + C::off_sb + 2048 * kk, DA * 128, 1024), ID_O1, kk > 0);
-                            tc_commit(smem_u32(&ctl.rd_free));
-                        }
-                        __syncwarp();
-                    }
-                    const int nq = (rows + 31) / 32;
-                    auto quarter = [&](int qq, auto buffer) {
-                        constexpr uint32_t B = decltype(buffer)::value;
-                        wait(ctl.vb_full[B], (quarters >> 1) & 1);
-                        tc_fence_after();
-                        if (elect_one_sync()) {
-                            const uint32_t vb = sbase + C::off_vb + B * C::vb_bytes;
-#pragma unroll
-                            for (int part = 0; part < 2; ++part)
-#pragma unroll
-                                for (int kk = 0; kk < 2; ++kk)
-                                    tc_mma_ss(tmem + C::col_s, sdesc_sw128(tw + 4096 * qq + 2048 * kk, kBox, 1024),
-                                              sdesc_sw128(vb + part * C::vb_part + 2048 * kk, 4096, 1024), ID_KV, 1u);
-                            tc_commit(smem_u32(&ctl.vb_free[B]));
-                            if (qq == nq - 1) {
-                                tc_commit(smem_u32(&ctl.kv_done));
-                                if (C::sum) tc_commit(smem_u32(&ctl.free[S]));
-                            }
-                        }
-                        __syncwarp();
-                        ++quarters;
-                    };
-                    for (int qq = 0; qq < nq; ++qq) {
-                        if (quarters & 1) quarter(qq, std::integral_constant<int, 1>());
-                        else quarter(qq, std::integral_constant<int, 0>());
-                    }
-                    if (C::out) {
-                        wait(ctl.p_full, it & 1);
-                        tc_fence_after();
-                        if (elect_one_sync()) {
-                            const int steps = (rows + 15) / 16;
-                            if (steps == kC / 16) {
-#pragma unroll
-                                for (int kk = 0; kk < kC / 16; ++kk)
-                                    tc_mma_ts(tmem + C::col_o2, tmem + C::col_a + 8 * kk, sdesc_sw128(tv + 2048 * kk, kBox, 1024),
-                                              ID_PV, kk > 0);
-                            } else {
-                                for (int kk = 0; kk < steps; ++kk)
-                                    tc_mma_ts(tmem + C::col_o2, tmem + C::col_a + 8 * kk, sdesc_sw128(tv + 2048 * kk, kBox, 1024),
-                                              ID_PV, kk > 0);
-                            }
-                            tc_commit(smem_u32(&ctl.pv_done));
-                            tc_commit(smem_u32(&ctl.free[S]));
-                        }
-                        __syncwarp();
-                    }
-                };
-                if (C::stages == 1 || st == 0) run(std::integral_constant<int, 0>());
-                else if (C::stages == 2 || st == 1) run(std::integral_constant<int, 1>());
-                else run(std::integral_constant<int, 2>());
-                ++it;
-            });
-        });
+                    for (int kk = 0; kk < kC / 16; ++kk)
+                        if (kk < steps)
+                            tc_mma_ts(tmem + C::col_o, tmem + C::col_a + 128 * ab + 8 * kk, sdesc_sw128(tv + 2048 * kk, kBox, 1024),
+                                      ID_PV, 1u);
+                    tc_commit(smem_u32(&ctl.pv_done));
+                    tc_commit(smem_u32(&ctl.free[slot(it, C::tV)]));
+                }
+                __syncwarp();
+            }
+            ++it;
+        }
         if (*dead) {  // the products in flight end before TMEM is released (bounded)
             if (elect_one_sync()) tc_commit(smem_u32(&ctl.end));
             __syncwarp();
@@ -920,8 +960,8 @@ bool encode(CUtensorMap *m, const void *base, int T, int Hx, int D) {
 template <int DA, int DB, int M>
 cudaError_t launch_t(const Params &p, cudaStream_t st) {
     using C = Cfg<DA, DB, M>;
-    constexpr int bytes = C::off_ctl + (int)sizeof(Ctl);
-    static_assert(bytes <= 232448, "shared memory");
+    constexpr int bytes = C::bytes;
+    static_assert(bytes <= 232448 && C::off_ctl % 16 == 0, "shared memory");
     Maps maps;
     if (!encode(&maps.wr, p.wr, p.T, p.H / p.wr_div, DA) || !encode(&maps.val, p.val, p.T, p.H / p.val_div, DB) ||
         !encode(&maps.rd, C::out ? p.rd : p.wr, p.T, C::out ? p.H / p.rd_div : p.H / p.wr_div, DA) ||
