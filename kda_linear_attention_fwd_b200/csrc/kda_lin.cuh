@@ -24,6 +24,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace kda {
 namespace lin {
 
@@ -65,6 +67,12 @@ struct Params {
     void *dg;               // [T][H], input type, or fp32 when g_per_head
     int zero_first_dg;      // no initial state: d(first log-decay) is exactly 0
 };
+
+// SMs of the current device (148 when there is none).
+int sm_count();
+// Lets `kernel` use `bytes` of dynamic shared memory on the current device;
+// `done` remembers the devices where it has been said.
+cudaError_t allow_smem(std::atomic<uint64_t> &done, const void *kernel, int bytes);
 
 }  // namespace lin
 }  // namespace kda

@@ -2,6 +2,7 @@
 // include/kda.h): argument checks, the window plan and the launch sequences.
 // No allocation, no host synchronisation, no exceptions across the boundary.
 #include <algorithm>
+#include <atomic>
 
 #include "../../include/kda.h"
 #include "kda_args.h"
@@ -18,6 +19,35 @@ cudaError_t launch_decode(bool bf16, int dk, int dv, const void *q, const void *
                           void *out, float *state, long nh, int H, int rep, int g_per_head, float scale, int sms,
                           cudaStream_t st);
 enum { kFwd, kSum, kSumR, kDq, kDk, kDv };  // launch_rec's modes
+
+int sm_count() {
+    static std::atomic<int> cache[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+        cudaGetLastError();
+        return 148;
+    }
+    int n = cache[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
+            cudaGetLastError();
+            return 148;
+        }
+        cache[dev].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
+cudaError_t allow_smem(std::atomic<uint64_t> &done, const void *kernel, int bytes) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
+    if (bit & done.load(std::memory_order_relaxed)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 
 // The tokens of a packed call that lie in a sequence: [cu[0], cu[num_seqs]).
 struct Tokens {
@@ -92,15 +122,7 @@ namespace {
 using kda::is_aligned;
 using kda::lin::Params;
 
-int sm_count() {
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
-        cudaGetLastError();
-        n = 148;
-    }
-    return n;
-}
+using kda::lin::sm_count;
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 

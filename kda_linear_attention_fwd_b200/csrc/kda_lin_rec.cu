@@ -445,7 +445,8 @@ cudaError_t launch_scan(float *z, const float *gamma, int W, int H, int elems, b
 template <typename T, int DA, int DB, int M>
 static cudaError_t launch_rec_t(const Params &p, cudaStream_t st) {
     constexpr int bytes = (int)sizeof(Smem<T, DA, DB, M>);
-    cudaError_t e = cudaFuncSetAttribute(rec_kernel<T, DA, DB, M>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    static std::atomic<uint64_t> done;
+    cudaError_t e = allow_smem(done, (const void *)rec_kernel<T, DA, DB, M>, bytes);
     if (e != cudaSuccess) return e;
     rec_kernel<T, DA, DB, M><<<dim3(p.H, p.W), kThreads, bytes, st>>>(p);
     return cudaGetLastError();

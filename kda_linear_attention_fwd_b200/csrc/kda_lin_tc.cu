@@ -967,7 +967,8 @@ cudaError_t launch_t(const Params &p, cudaStream_t st) {
         !encode(&maps.rd, C::out ? p.rd : p.wr, p.T, C::out ? p.H / p.rd_div : p.H / p.wr_div, DA) ||
         !encode(&maps.ext, M == DQ ? p.ext : p.val, p.T, M == DQ ? p.H / p.ext_div : p.H / p.val_div, DB))
         return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(tc_kernel<DA, DB, M>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    static std::atomic<uint64_t> done;
+    cudaError_t e = allow_smem(done, (const void *)tc_kernel<DA, DB, M>, bytes);
     if (e != cudaSuccess) return e;
     tc_kernel<DA, DB, M><<<dim3(p.H, p.W), kThreads, bytes, st>>>(p, maps);
     return cudaGetLastError();

@@ -29,6 +29,7 @@
 #include "../../include/kda.h"
 #include "kda_args.h"
 #include "kda_common.cuh"
+#include "kda_lin.cuh"
 
 namespace kda {
 namespace norm {
@@ -214,7 +215,7 @@ __global__ void __launch_bounds__(MT) fwd_kernel(const __grid_constant__ Params 
 // stay in registers in their own type; those of the next row are requested as
 // soon as the last use of this row's is behind, before the last row sum.
 template <typename T, int VEC, int NV, int MT, int G, bool PRE>
-__global__ void __launch_bounds__(MT, 1024 / MT) bwd_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(MT, MT == 256 ? 3 : 1) bwd_kernel(const __grid_constant__ Params p) {
     __shared__ float red[2][3][32][2];
     extern __shared__ float colsum[];  // [2][D], when a CTA holds more than one row
     const int tpr = p.tpr, t = threadIdx.x & (tpr - 1), g = gate_of<G>(p);
@@ -378,22 +379,29 @@ __global__ void __launch_bounds__(MT, 1024 / MT) bwd_kernel(const __grid_constan
     }
 }
 
-// dw[c] = sum over the CTAs' partial sums, in order: 32 columns x 8 parts per CTA.
-__global__ void __launch_bounds__(256) weight_sum_kernel(const float *part, int parts, int D, float *dpost, float *dpre) {
-    __shared__ float s[8][33];
+// dw[c] = sum over the CTAs' partial sums in a fixed order: 32 columns x 32
+// parts at a time per CTA, four of each thread's loads in flight.
+__global__ void __launch_bounds__(1024) weight_sum_kernel(const float *part, int parts, int D, float *dpost, float *dpre) {
+    __shared__ float s[32][33];
     const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5, c = blockIdx.x * 32 + cx;
     float *out = blockIdx.y ? dpre : dpost;
     if (!out) return;
+    const float *src = part + (size_t)blockIdx.y * D + c;
     float a = 0.f;
-    if (c < D)
-        for (int i = ry; i < parts; i += 8) a += part[(size_t)i * 2 * D + (size_t)blockIdx.y * D + c];
+    if (c < D) {
+        int i = ry;
+        for (; i + 96 < parts; i += 128) {
+            const float x0 = src[(size_t)i * 2 * D], x1 = src[(size_t)(i + 32) * 2 * D], x2 = src[(size_t)(i + 64) * 2 * D],
+                        x3 = src[(size_t)(i + 96) * 2 * D];
+            a += (x0 + x1) + (x2 + x3);
+        }
+        for (; i < parts; i += 32) a += src[(size_t)i * 2 * D];
+    }
     s[ry][cx] = a;
     __syncthreads();
-    if (ry == 0 && c < D) {
-#pragma unroll
-        for (int i = 1; i < 8; ++i) a += s[i][cx];
-        out[c] = a;
-    }
+    a = s[cx][ry];  // column ry, part cx
+    a = warp_sum(a);
+    if (cx == 0 && blockIdx.x * 32 + ry < D) out[blockIdx.x * 32 + ry] = a;
 }
 
 struct Shape {
@@ -467,15 +475,7 @@ using kda::is_aligned;
 using kda::norm::Params;
 using kda::norm::Shape;
 
-int sm_count() {
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
-        cudaGetLastError();
-        n = 148;
-    }
-    return n;
-}
+int sm_count() { return kda::lin::sm_count(); }
 
 int check_shape(int64_t rows, int32_t D, kda_dtype dtype, int32_t flags, float eps) {
     const int all = KDA_NORM_POST | KDA_NORM_PRE | KDA_NORM_GATE_SIGMOID | KDA_NORM_GATE_SILU;
@@ -502,7 +502,7 @@ int check_elems(const void *const *ptrs, int n, size_t esz) {
 
 int bwd_parts(int64_t rows, const Shape &s) {
     const int64_t batches = (rows + s.per - 1) / s.per;
-    return (int)std::max<int64_t>(1, std::min<int64_t>(batches, (int64_t)sm_count() * (1024 / s.threads)));
+    return (int)std::max<int64_t>(1, std::min<int64_t>(batches, (int64_t)sm_count() * (s.threads == 256 ? 3 : 1)));
 }
 
 }  // namespace
@@ -585,7 +585,7 @@ int kda_block_norm_bwd(const void *dout, const void *dnormed, const void *y, int
         if (e != cudaSuccess) return KDA_ERR_CUDA;
     }
     if (weights) {
-        kda::norm::weight_sum_kernel<<<dim3((D + 31) / 32, 2), 256, 0, st>>>(p.part, rows > 0 ? parts : 0, D,
+        kda::norm::weight_sum_kernel<<<dim3((D + 31) / 32, 2), 1024, 0, st>>>(p.part, rows > 0 ? parts : 0, D,
                                                                             dpost_weight, dpre_weight);
         if (cudaGetLastError() != cudaSuccess) return KDA_ERR_CUDA;
     }
