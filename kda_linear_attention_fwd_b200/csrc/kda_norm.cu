@@ -30,6 +30,7 @@
 #include "kda_args.h"
 #include "kda_common.cuh"
 #include "kda_lin.cuh"
+#include "kda_sm100.cuh"
 
 namespace kda {
 namespace norm {
@@ -60,16 +61,39 @@ template <typename T, int VEC>
 KDA_DEVICE VecT<T, VEC> load_vec(const void *base, long at) {
     return *reinterpret_cast<const VecT<T, VEC> *>((const T *)base + at);
 }
+// The arithmetic runs on pairs (one fp32 instruction for two elements); a
+// single element is a pair whose second half is zero.
+using sm100::f2fma;
+using sm100::f2mul;
+KDA_DEVICE float2 pair(float x) { return make_float2(x, x); }
+KDA_DEVICE float2 f2add(float2 a, float2 b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(d)
+        : "l"(*reinterpret_cast<uint64_t *>(&a)), "l"(*reinterpret_cast<uint64_t *>(&b)));
+    return *reinterpret_cast<float2 *>(&d);
+}
+template <int VEC> constexpr int kPairs = VEC == 1 ? 1 : VEC / 2;
 template <typename T, int VEC>
-KDA_DEVICE void store_vec(void *base, long at, const float (&v)[VEC]) {
+KDA_DEVICE float2 get(const VecT<T, VEC> &v, int i) {
+    if constexpr (VEC == 1) return make_float2(ld(&v.e[0]), 0.f);
+    else if constexpr (VEC == 8) return sm100::unpack_bf16(reinterpret_cast<const uint32_t *>(v.e)[i]);
+    else return make_float2(ld(&v.e[2 * i]), ld(&v.e[2 * i + 1]));
+}
+template <typename T, int VEC>
+KDA_DEVICE void store_vec(void *base, long at, const float2 (&v)[kPairs<VEC>]) {
     VecT<T, VEC> o;
-    if constexpr (VEC == 8) {
+    if constexpr (VEC == 1) {
+        st(&o.e[0], v[0].x);
+    } else if constexpr (VEC == 8) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            reinterpret_cast<__nv_bfloat162 *>(o.e)[e] = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
+        for (int i = 0; i < 4; ++i) reinterpret_cast<uint32_t *>(o.e)[i] = sm100::pack_bf16(v[i]);
     } else {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) st(&o.e[e], v[e]);
+        for (int i = 0; i < kPairs<VEC>; ++i) {
+            st(&o.e[2 * i], v[i].x);
+            st(&o.e[2 * i + 1], v[i].y);
+        }
     }
     *reinterpret_cast<VecT<T, VEC> *>((T *)base + at) = o;
 }
@@ -113,122 +137,151 @@ KDA_DEVICE int gate_of(const Params &p) {
     if (!p.gate) return GATE_NONE;
     return (p.flags & KDA_NORM_GATE_SIGMOID) ? GATE_SIGMOID : (p.flags & KDA_NORM_GATE_SILU) ? GATE_SILU : GATE_GIVEN;
 }
-// 1 / (1 + exp(-z)) with the approximate reciprocal (1 ulp): an IEEE division
-// would be a third of the gated kernels' instructions.
-KDA_DEVICE float logistic(float z) {
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + __expf(-z)));
+// 1 / (1 + exp(-z)) of a pair, with the approximate exponential and reciprocal
+// (each off by an ulp or two): IEEE division would be a third of the gated
+// kernels' instructions.
+KDA_DEVICE float2 logistic(float2 z) {
+    const float2 t = f2mul(z, pair(-1.4426950408889634f));
+    float2 e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
+    e = f2add(e, pair(1.f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(e.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(e.y));
     return r;
 }
-// act(z), s being logistic(z) where the gate has one
-KDA_DEVICE float act_of(int g, float z, float s) {
-    return g == GATE_NONE ? 1.f : g == GATE_GIVEN ? z : g == GATE_SIGMOID ? s : z * s;
+// act(z) and its slope, s being logistic(z) where the gate has one
+KDA_DEVICE float2 act_of(int g, float2 z, float2 s) {
+    return g == GATE_GIVEN ? z : g == GATE_SIGMOID ? s : f2mul(z, s);
 }
-KDA_DEVICE float slope_of(int g, float z, float s) {
-    return g == GATE_SIGMOID ? s * (1.f - s) : g == GATE_SILU ? s * (1.f + z * (1.f - s)) : 1.f;
+KDA_DEVICE float2 slope_of(int g, float2 z, float2 s) {
+    if (g == GATE_GIVEN) return pair(1.f);
+    const float2 rest = f2fma(s, pair(-1.f), pair(1.f));  // 1 - s
+    return g == GATE_SIGMOID ? f2mul(s, rest) : f2fma(f2mul(z, s), rest, s);
 }
 
-// VEC elements of a weight, or ones
-template <typename T, int VEC>
-KDA_DEVICE void load_weight(float (&w)[VEC], const void *base, int c) {
-    if (base) {
-        const VecT<T, VEC> v = load_vec<T, VEC>(base, c);
+// The thread's part of a weight, or ones
+template <typename T, int VEC, int NV>
+KDA_DEVICE void load_weight(float2 (&w)[NV][kPairs<VEC>], const void *base, int tpr, int t, int D) {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) w[e] = ld(&v.e[e]);
-    } else {
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * tpr + t) * VEC;
+        VecT<T, VEC> v;
+        if (base && c < D) v = load_vec<T, VEC>(base, c);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) w[e] = 1.f;
+        for (int e = 0; e < kPairs<VEC>; ++e) w[i][e] = base && c < D ? get<T, VEC>(v, e) : pair(1.f);
     }
 }
 
-template <typename T, int VEC, int NV, int MT, int G>
+// A fixed number of CTAs runs over the rows; the weights stay in registers
+// (rows of one vector per thread) and the vectors of the next row are
+// requested before this row's arithmetic ends.
+template <typename T, int VEC, int NV, int MT, int G, bool RES, bool PRE>
 __global__ void __launch_bounds__(MT) fwd_kernel(const __grid_constant__ Params p) {
-    __shared__ float red[2][32][2];
+    constexpr int NP = kPairs<VEC>;
+    __shared__ float red[2][2][32][2];
     const int tpr = p.tpr, t = threadIdx.x & (tpr - 1), g = gate_of<G>(p);
-    const long row = (long)blockIdx.x * (blockDim.x / tpr) + threadIdx.x / tpr;
-    const bool live = row < p.rows;
+    const int per = blockDim.x / tpr;
+    const bool post = p.flags & KDA_NORM_POST;
     const float inv_d = 1.f / p.D;
     VecT<T, VEC> y[NV], z[NV], x[NV];
-    float u[NV][VEC];
-    float ss[1] = {0.f};
+    auto load = [&](long row) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = (i * tpr + t) * VEC;
-        if (live && c < p.D) {
-            y[i] = load_vec<T, VEC>(p.y, row * p.y_ld + c);
-            if (g != GATE_NONE) z[i] = load_vec<T, VEC>(p.gate, row * p.gate_ld + c);
-            if (p.x) x[i] = load_vec<T, VEC>(p.x, row * p.x_ld + c);
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const bool in = live && (i * tpr + t) * VEC < p.D;
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            u[i][e] = in ? ld(&y[i].e[e]) : 0.f;
-            ss[0] = fmaf(u[i][e], u[i][e], ss[0]);
-        }
-    }
-    float iy = 1.f;
-    if (p.flags & KDA_NORM_POST) {
-        row_sum(ss, tpr, red[0]);
-        iy = rsqrtf(fmaf(ss[0], inv_d, p.eps));
-    }
-    float rr[1] = {0.f};
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = (i * tpr + t) * VEC;
-        if (live && c < p.D) {
-            float w[VEC];
-            load_weight<T, VEC>(w, p.w_post, c);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                float a = u[i][e] * iy * w[e];
-                if (g != GATE_NONE) {
-                    const float zz = ld(&z[i].e[e]);
-                    a *= act_of(g, zz, g >= GATE_SIGMOID ? logistic(zz) : 0.f);
-                }
-                a = p.x ? fmaf(a, p.c, ld(&x[i].e[e])) : a * p.c;
-                u[i][e] = a;
-                rr[0] = fmaf(a, a, rr[0]);
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * tpr + t) * VEC;
+            if (row < p.rows && c < p.D) {
+                y[i] = load_vec<T, VEC>(p.y, row * p.y_ld + c);
+                if (g != GATE_NONE) z[i] = load_vec<T, VEC>(p.gate, row * p.gate_ld + c);
+                if (RES) x[i] = load_vec<T, VEC>(p.x, row * p.x_ld + c);
             }
-            store_vec<T, VEC>(p.out, row * p.D + c, u[i]);
         }
+    };
+    const long step = (long)gridDim.x * per;
+    long row = (long)blockIdx.x * per + threadIdx.x / tpr;
+    load(row);
+    float2 wa[NV][NP], wb[PRE ? NV : 1][NP];
+    if (NV == 1) {
+        load_weight<T, VEC, NV>(wa, p.w_post, tpr, t, p.D);
+        if constexpr (PRE) load_weight<T, VEC, NV>(wb, p.w_pre, tpr, t, p.D);
     }
-    if (!(p.flags & KDA_NORM_PRE)) return;
-    row_sum(rr, tpr, red[1]);
-    const float ir = rsqrtf(fmaf(rr[0], inv_d, p.eps));
+    int par = 0;
+    for (long row0 = (long)blockIdx.x * per; row0 < p.rows; row0 += step, row += step, par ^= 1) {
+        if (NV > 1) load_weight<T, VEC, NV>(wa, p.w_post, tpr, t, p.D);
+        float2 u[NV][NP];
+        float f = p.c;  // iy c
+        float2 ss = pair(0.f);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = (i * tpr + t) * VEC;
-        if (live && c < p.D) {
-            float w[VEC];
-            load_weight<T, VEC>(w, p.w_pre, c);
+        for (int i = 0; i < NV; ++i) {
+            const bool in = row < p.rows && (i * tpr + t) * VEC < p.D;
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) u[i][e] *= ir * w[e];
-            store_vec<T, VEC>(p.normed, row * p.D + c, u[i]);
+            for (int e = 0; e < NP; ++e) {
+                u[i][e] = in ? get<T, VEC>(y[i], e) : pair(0.f);
+                ss = f2fma(u[i][e], u[i][e], ss);
+            }
+        }
+        if (post) {
+            float s1[1] = {ss.x + ss.y};
+            row_sum(s1, tpr, red[par][0]);
+            f *= rsqrtf(fmaf(s1[0], inv_d, p.eps));
+        }
+        float2 rr = pair(0.f);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * tpr + t) * VEC;
+            if (row < p.rows && c < p.D) {
+#pragma unroll
+                for (int e = 0; e < NP; ++e) {
+                    float2 a = wa[i][e];
+                    if (g != GATE_NONE) {
+                        const float2 zz = get<T, VEC>(z[i], e);
+                        a = f2mul(a, act_of(g, zz, g >= GATE_SIGMOID ? logistic(zz) : pair(0.f)));
+                    }
+                    a = f2mul(a, u[i][e]);
+                    u[i][e] = RES ? f2fma(a, pair(f), get<T, VEC>(x[i], e)) : f2mul(a, pair(f));
+                    if (PRE) rr = f2fma(u[i][e], u[i][e], rr);
+                }
+                store_vec<T, VEC>(p.out, row * p.D + c, u[i]);
+            }
+        }
+        load(row + step);
+        if constexpr (PRE) {
+            if (NV > 1) load_weight<T, VEC, NV>(wb, p.w_pre, tpr, t, p.D);
+            float s1[1] = {rr.x + rr.y};
+            row_sum(s1, tpr, red[par][1]);
+            const float2 ir = pair(rsqrtf(fmaf(s1[0], inv_d, p.eps)));
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = (i * tpr + t) * VEC;
+                if (row < p.rows && c < p.D) {
+#pragma unroll
+                    for (int e = 0; e < NP; ++e) u[i][e] = f2mul(u[i][e], f2mul(ir, wb[i][e]));
+                    store_vec<T, VEC>(p.normed, row * p.D + c, u[i]);
+                }
+            }
         }
     }
 }
 
-// PRE: the next block's norm is there and has a gradient.  A row's vectors
-// stay in registers in their own type; those of the next row are requested as
-// soon as the last use of this row's is behind, before the last row sum.
-template <typename T, int VEC, int NV, int MT, int G, bool PRE>
+// RES: a residual that the norm of `out` needs.  PRE: that norm is there and
+// has a gradient.  A row's vectors stay in registers in their own type; those
+// of the next row are requested as soon as the last use of this row's is
+// behind, before the last row sum.
+template <typename T, int VEC, int NV, int MT, int G, bool PRE, bool RES>
 __global__ void __launch_bounds__(MT, MT == 256 ? 3 : 1) bwd_kernel(const __grid_constant__ Params p) {
+    constexpr int NP = kPairs<VEC>;
     __shared__ float red[2][3][32][2];
     extern __shared__ float colsum[];  // [2][D], when a CTA holds more than one row
     const int tpr = p.tpr, t = threadIdx.x & (tpr - 1), g = gate_of<G>(p);
     const int per = blockDim.x / tpr, sub = threadIdx.x / tpr;
     const bool post = p.flags & KDA_NORM_POST;
     const float inv_d = 1.f / p.D;
-    float gpost[NV][VEC], gpre[PRE ? NV : 1][VEC];
+    float2 gpost[NV][NP], gpre[PRE ? NV : 1][NP];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            gpost[i][e] = 0.f;
-            if (PRE) gpre[i][e] = 0.f;
+        for (int e = 0; e < NP; ++e) {
+            gpost[i][e] = pair(0.f);
+            if (PRE) gpre[i][e] = pair(0.f);
         }
     VecT<T, VEC> y[NV], z[NV], x[NV], dr[NV], dh[NV];
     auto load_y = [&](long row) {
@@ -244,7 +297,7 @@ __global__ void __launch_bounds__(MT, MT == 256 ? 3 : 1) bwd_kernel(const __grid
             const int c = (i * tpr + t) * VEC;
             if (row < p.rows && c < p.D) {
                 if (g != GATE_NONE) z[i] = load_vec<T, VEC>(p.gate, row * p.gate_ld + c);
-                if (PRE && p.x) x[i] = load_vec<T, VEC>(p.x, row * p.x_ld + c);
+                if (RES) x[i] = load_vec<T, VEC>(p.x, row * p.x_ld + c);
                 if (p.dr) dr[i] = load_vec<T, VEC>(p.dr, row * p.D + c);
                 if (PRE) dh[i] = load_vec<T, VEC>(p.dh, row * p.D + c);
             }
@@ -254,101 +307,112 @@ __global__ void __launch_bounds__(MT, MT == 256 ? 3 : 1) bwd_kernel(const __grid
     long row = (long)blockIdx.x * per + sub;
     load_y(row);
     load_rest(row);
+    float2 wa[NV][NP], wb[PRE ? NV : 1][NP];
+    if (NV == 1) {
+        load_weight<T, VEC, NV>(wa, p.w_post, tpr, t, p.D);
+        if constexpr (PRE) load_weight<T, VEC, NV>(wb, p.w_pre, tpr, t, p.D);
+    }
     int par = 0;
     for (long row0 = (long)blockIdx.x * per; row0 < p.rows; row0 += step, row += step, par ^= 1) {
         const bool live = row < p.rows;
+        if (NV > 1) {
+            load_weight<T, VEC, NV>(wa, p.w_post, tpr, t, p.D);
+            if constexpr (PRE) load_weight<T, VEC, NV>(wb, p.w_pre, tpr, t, p.D);
+        }
         float iy = 1.f;
         if (post) {
-            float a1[1] = {0.f};
+            float2 ss = pair(0.f);
 #pragma unroll
             for (int i = 0; i < NV; ++i)
                 if (live && (i * tpr + t) * VEC < p.D)
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
-                        const float v = ld(&y[i].e[e]);
-                        a1[0] = fmaf(v, v, a1[0]);
+                    for (int e = 0; e < NP; ++e) {
+                        const float2 v = get<T, VEC>(y[i], e);
+                        ss = f2fma(v, v, ss);
                     }
-            row_sum(a1, tpr, red[par][0]);
-            iy = rsqrtf(fmaf(a1[0], inv_d, p.eps));
+            float s1[1] = {ss.x + ss.y};
+            row_sum(s1, tpr, red[par][0]);
+            iy = rsqrtf(fmaf(s1[0], inv_d, p.eps));
         }
-        float ir = 0.f, mean_r = 0.f;
-        float r[PRE ? NV : 1][VEC], sg[NV][VEC];  // out, unrounded; logistic(gate)
+        float ir = 0.f, k2 = 0.f;                           // d = dr + ir m - k2 r
+        float2 r[PRE ? NV : 1][NP], sg[NV][NP];             // out, unrounded; logistic(gate)
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             if (g >= GATE_SIGMOID && live && (i * tpr + t) * VEC < p.D)
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) sg[i][e] = logistic(ld(&z[i].e[e]));
+                for (int e = 0; e < NP; ++e) sg[i][e] = logistic(get<T, VEC>(z[i], e));
         if constexpr (PRE) {
-            float s2[2] = {0.f, 0.f};  // sum r^2, sum dh w_pre r
+            float2 s2 = pair(0.f), s3 = pair(0.f);          // sum r^2, sum dh w_pre r
+            const float f = iy * p.c;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const int c = (i * tpr + t) * VEC;
-                if (live && c < p.D) {
-                    float wa[VEC], wb[VEC];
-                    load_weight<T, VEC>(wa, p.w_post, c);
-                    load_weight<T, VEC>(wb, p.w_pre, c);
+                if (live && (i * tpr + t) * VEC < p.D) {
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
-                        float a = ld(&y[i].e[e]) * iy * wa[e];
-                        if (g != GATE_NONE) a *= act_of(g, ld(&z[i].e[e]), sg[i][e]);
-                        a = p.x ? fmaf(a, p.c, ld(&x[i].e[e])) : a * p.c;
+                    for (int e = 0; e < NP; ++e) {
+                        float2 a = wa[i][e];
+                        if (g != GATE_NONE) a = f2mul(a, act_of(g, get<T, VEC>(z[i], e), sg[i][e]));
+                        a = f2mul(a, get<T, VEC>(y[i], e));
+                        a = RES ? f2fma(a, pair(f), get<T, VEC>(x[i], e)) : f2mul(a, pair(f));
                         r[i][e] = a;
-                        s2[0] = fmaf(a, a, s2[0]);
-                        s2[1] = fmaf(ld(&dh[i].e[e]) * wb[e], a, s2[1]);
+                        s2 = f2fma(a, a, s2);
+                        s3 = f2fma(f2mul(get<T, VEC>(dh[i], e), wb[i][e]), a, s3);
                     }
                 }
             }
-            row_sum(s2, tpr, red[par][1]);
-            ir = rsqrtf(fmaf(s2[0], inv_d, p.eps));
-            mean_r = s2[1] * ir * inv_d;
+            float s[2] = {s2.x + s2.y, s3.x + s3.y};
+            row_sum(s, tpr, red[par][1]);
+            ir = rsqrtf(fmaf(s[0], inv_d, p.eps));
+            k2 = s[1] * ir * ir * ir * inv_d;
         }
-        float dn[NV][VEC];
-        float a3[1] = {0.f};
+        float2 dn[NV][NP];
+        float2 a3 = pair(0.f);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * tpr + t) * VEC;
             if (live && c < p.D) {
-                float wa[VEC], wb[VEC], dR[VEC], dz[VEC];
-                load_weight<T, VEC>(wa, p.w_post, c);
-                if (PRE) load_weight<T, VEC>(wb, p.w_pre, c);
+                float2 dR[NP], dz[NP];
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    const float yn = ld(&y[i].e[e]) * iy;
-                    float d = p.dr ? ld(&dr[i].e[e]) : 0.f;
+                for (int e = 0; e < NP; ++e) {
+                    const float2 yn = f2mul(get<T, VEC>(y[i], e), pair(iy));
+                    float2 d = p.dr ? get<T, VEC>(dr[i], e) : pair(0.f);
                     if constexpr (PRE) {
-                        const float rn = r[i][e] * ir, dhe = ld(&dh[i].e[e]);
-                        d = fmaf(ir, fmaf(-rn, mean_r, dhe * wb[e]), d);
-                        gpre[i][e] = fmaf(dhe, rn, gpre[i][e]);
+                        const float2 dhe = get<T, VEC>(dh[i], e);
+                        d = f2fma(r[i][e], pair(-k2), f2fma(f2mul(dhe, wb[i][e]), pair(ir), d));
+                        gpre[i][e] = f2fma(dhe, f2mul(r[i][e], pair(ir)), gpre[i][e]);
                     }
                     dR[e] = d;
-                    const float du = d * p.c;
-                    float da = du;
+                    const float2 du = f2mul(d, pair(p.c));
+                    const float2 q = f2mul(du, yn);
+                    float2 aw = wa[i][e];
                     if (g != GATE_NONE) {
-                        const float zz = ld(&z[i].e[e]);
-                        dz[e] = du * yn * wa[e] * slope_of(g, zz, sg[i][e]);
-                        da *= act_of(g, zz, sg[i][e]);
+                        const float2 zz = get<T, VEC>(z[i], e), act = act_of(g, zz, sg[i][e]);
+                        dz[e] = f2mul(f2mul(q, aw), slope_of(g, zz, sg[i][e]));
+                        gpost[i][e] = f2fma(q, act, gpost[i][e]);
+                        aw = f2mul(aw, act);
+                    } else {
+                        gpost[i][e] = f2add(gpost[i][e], q);
                     }
-                    gpost[i][e] = fmaf(da, yn, gpost[i][e]);
-                    dn[i][e] = da * wa[e];
-                    a3[0] = fmaf(dn[i][e], yn, a3[0]);
+                    dn[i][e] = f2mul(du, aw);
+                    a3 = f2fma(q, aw, a3);
                 }
                 if (p.dx) store_vec<T, VEC>(p.dx, row * p.D + c, dR);
                 if (g != GATE_NONE && p.dgate) store_vec<T, VEC>(p.dgate, row * p.D + c, dz);
             }
         }
         load_rest(row + step);
-        float mean_y = 0.f;
+        float k3 = 0.f;                                     // dy = iy dn - k3 y
         if (post) {
-            row_sum(a3, tpr, red[par][2]);
-            mean_y = a3[0] * inv_d;
+            float s1[1] = {a3.x + a3.y};
+            row_sum(s1, tpr, red[par][2]);
+            k3 = s1[0] * iy * iy * inv_d;
         }
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * tpr + t) * VEC;
             if (live && c < p.D) {
-                if (post)
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) dn[i][e] = iy * fmaf(-(ld(&y[i].e[e]) * iy), mean_y, dn[i][e]);
+                for (int e = 0; e < NP; ++e)
+                    dn[i][e] = f2fma(get<T, VEC>(y[i], e), pair(-k3), f2mul(dn[i][e], pair(iy)));
                 store_vec<T, VEC>(p.dy, row * p.D + c, dn[i]);
             }
         }
@@ -367,8 +431,14 @@ __global__ void __launch_bounds__(MT, MT == 256 ? 3 : 1) bwd_kernel(const __grid
                 if (c < p.D)
 #pragma unroll
                     for (int e = 0; e < VEC; ++e) {
-                        to[c + e] = (s ? to[c + e] : 0.f) + gpost[i][e];
-                        to[p.D + c + e] = PRE ? (s ? to[p.D + c + e] : 0.f) + gpre[i][e] : 0.f;
+                        const float a = e & 1 ? gpost[i][e / 2].y : gpost[i][e / 2].x;
+                        to[c + e] = (s ? to[c + e] : 0.f) + a;
+                        if (PRE) {
+                            const float b = e & 1 ? gpre[i][e / 2].y : gpre[i][e / 2].x;
+                            to[p.D + c + e] = (s ? to[p.D + c + e] : 0.f) + b;
+                        } else {
+                            to[p.D + c + e] = 0.f;
+                        }
                     }
             }
         }
@@ -425,15 +495,22 @@ Shape choose_shape(int D, int vec) {
     return s;
 }
 
-template <typename T, int VEC, int NV, int MT, int G>
-cudaError_t launch_g(const Params &p, const Shape &s, bool bwd, unsigned grid, cudaStream_t st) {
+template <typename T, int VEC, int NV, int MT, int G, bool PRE, bool RES>
+void launch_k(const Params &p, const Shape &s, bool bwd, unsigned grid, cudaStream_t st) {
     if (bwd) {
         const size_t bytes = s.per > 1 ? (size_t)2 * p.D * sizeof(float) : 0;
-        if ((p.flags & KDA_NORM_PRE) && p.dh) bwd_kernel<T, VEC, NV, MT, G, true><<<grid, s.threads, bytes, st>>>(p);
-        else bwd_kernel<T, VEC, NV, MT, G, false><<<grid, s.threads, bytes, st>>>(p);
+        bwd_kernel<T, VEC, NV, MT, G, PRE, RES><<<grid, s.threads, bytes, st>>>(p);
     } else {
-        fwd_kernel<T, VEC, NV, MT, G><<<grid, s.threads, 0, st>>>(p);
+        fwd_kernel<T, VEC, NV, MT, G, RES, PRE><<<grid, s.threads, 0, st>>>(p);
     }
+}
+template <typename T, int VEC, int NV, int MT, int G>
+cudaError_t launch_g(const Params &p, const Shape &s, bool bwd, unsigned grid, cudaStream_t st) {
+    const bool pre = (p.flags & KDA_NORM_PRE) && (!bwd || p.dh);
+    if (pre && p.x) launch_k<T, VEC, NV, MT, G, true, true>(p, s, bwd, grid, st);
+    else if (pre) launch_k<T, VEC, NV, MT, G, true, false>(p, s, bwd, grid, st);
+    else if (p.x && !bwd) fwd_kernel<T, VEC, NV, MT, G, true, false><<<grid, s.threads, 0, st>>>(p);
+    else launch_k<T, VEC, NV, MT, G, false, false>(p, s, bwd, grid, st);
     return cudaGetLastError();
 }
 template <typename T, int VEC, int NV, int MT>
@@ -531,8 +608,8 @@ int kda_block_norm(const void *y, int64_t y_stride, const void *post_weight, con
     p.rows = rows; p.D = D; p.flags = flags; p.c = res_scale; p.eps = eps;
     const Shape s = kda::norm::choose_shape(D, vec_of(p, ptrs, 7, bf16 ? 2 : 4));
     p.tpr = s.tpr;
-    const int64_t grid = (rows + s.per - 1) / s.per;
-    if (grid > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
+    // as many CTAs as an SM holds at 64 (with the pre norm) or 40 registers a thread
+    const int64_t grid = std::min<int64_t>((rows + s.per - 1) / s.per, (int64_t)sm_count() * std::max(1, (flags & KDA_NORM_PRE ? 1024 : 1536) / s.threads));
     const cudaError_t e = bf16 ? kda::norm::launch_t<__nv_bfloat16>(p, s, false, (unsigned)grid, (cudaStream_t)stream)
                                : kda::norm::launch_t<float>(p, s, false, (unsigned)grid, (cudaStream_t)stream);
     return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
