@@ -101,7 +101,7 @@ KDA_DEVICE void store_vec(void *base, long at, const float2 (&v)[kPairs<VEC>]) {
 // Sum of N values over the TPR threads of a row (every thread gets it).  red
 // is not written again before another barrier of the CTA.
 template <int N>
-KDA_DEVICE void row_sum(float (&v)[N], int tpr, float (*red)[2]) {
+KDA_DEVICE void row_sum(float (&v)[N], int tpr, float (*red)[3]) {
     if (tpr >= 32) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
@@ -179,7 +179,7 @@ KDA_DEVICE void load_weight(float2 (&w)[NV][kPairs<VEC>], const void *base, int 
 template <typename T, int VEC, int NV, int MT, int G, bool RES, bool PRE>
 __global__ void __launch_bounds__(MT) fwd_kernel(const __grid_constant__ Params p) {
     constexpr int NP = kPairs<VEC>;
-    __shared__ float red[2][2][32][2];
+    __shared__ float red[2][2][32][3];
     const int tpr = p.tpr, t = threadIdx.x & (tpr - 1), g = gate_of<G>(p);
     const int per = blockDim.x / tpr;
     const bool post = p.flags & KDA_NORM_POST;
@@ -263,13 +263,14 @@ __global__ void __launch_bounds__(MT) fwd_kernel(const __grid_constant__ Params 
 }
 
 // RES: a residual that the norm of `out` needs.  PRE: that norm is there and
-// has a gradient.  A row's vectors stay in registers in their own type; those
-// of the next row are requested as soon as the last use of this row's is
-// behind, before the last row sum.
+// has a gradient.  A row's vectors stay in registers in their own type.  The
+// row sums are what a row waits for, so there are as few as the algebra allows:
+// mean(dn yn) is taken apart into sums over a = w_post act(gate) y that are
+// known before dn is, one round of sums without PRE and two with it.
 template <typename T, int VEC, int NV, int MT, int G, bool PRE, bool RES>
 __global__ void __launch_bounds__(MT, MT == 256 ? 3 : 1) bwd_kernel(const __grid_constant__ Params p) {
     constexpr int NP = kPairs<VEC>;
-    __shared__ float red[2][3][32][2];
+    __shared__ float red[2][2][32][3];
     extern __shared__ float colsum[];  // [2][D], when a CTA holds more than one row
     const int tpr = p.tpr, t = threadIdx.x & (tpr - 1), g = gate_of<G>(p);
     const int per = blockDim.x / tpr, sub = threadIdx.x / tpr;
@@ -284,18 +285,12 @@ __global__ void __launch_bounds__(MT, MT == 256 ? 3 : 1) bwd_kernel(const __grid
             if (PRE) gpre[i][e] = pair(0.f);
         }
     VecT<T, VEC> y[NV], z[NV], x[NV], dr[NV], dh[NV];
-    auto load_y = [&](long row) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (i * tpr + t) * VEC;
-            if (row < p.rows && c < p.D) y[i] = load_vec<T, VEC>(p.y, row * p.y_ld + c);
-        }
-    };
-    auto load_rest = [&](long row) {
+    auto load = [&](long row) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * tpr + t) * VEC;
             if (row < p.rows && c < p.D) {
+                y[i] = load_vec<T, VEC>(p.y, row * p.y_ld + c);
                 if (g != GATE_NONE) z[i] = load_vec<T, VEC>(p.gate, row * p.gate_ld + c);
                 if (RES) x[i] = load_vec<T, VEC>(p.x, row * p.x_ld + c);
                 if (p.dr) dr[i] = load_vec<T, VEC>(p.dr, row * p.D + c);
@@ -305,8 +300,7 @@ __global__ void __launch_bounds__(MT, MT == 256 ? 3 : 1) bwd_kernel(const __grid
     };
     const long step = (long)gridDim.x * per;
     long row = (long)blockIdx.x * per + sub;
-    load_y(row);
-    load_rest(row);
+    load(row);
     float2 wa[NV][NP], wb[PRE ? NV : 1][NP];
     if (NV == 1) {
         load_weight<T, VEC, NV>(wa, p.w_post, tpr, t, p.D);
@@ -319,61 +313,72 @@ __global__ void __launch_bounds__(MT, MT == 256 ? 3 : 1) bwd_kernel(const __grid
             load_weight<T, VEC, NV>(wa, p.w_post, tpr, t, p.D);
             if constexpr (PRE) load_weight<T, VEC, NV>(wb, p.w_pre, tpr, t, p.D);
         }
-        float iy = 1.f;
-        if (post) {
-            float2 ss = pair(0.f);
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (live && (i * tpr + t) * VEC < p.D)
-#pragma unroll
-                    for (int e = 0; e < NP; ++e) {
-                        const float2 v = get<T, VEC>(y[i], e);
-                        ss = f2fma(v, v, ss);
-                    }
-            float s1[1] = {ss.x + ss.y};
-            row_sum(s1, tpr, red[par][0]);
-            iy = rsqrtf(fmaf(s1[0], inv_d, p.eps));
-        }
-        float ir = 0.f, k2 = 0.f;                           // d = dr + ir m - k2 r
-        float2 r[PRE ? NV : 1][NP], sg[NV][NP];             // out, unrounded; logistic(gate)
+        float2 sg[NV][NP];                                  // logistic(gate)
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             if (g >= GATE_SIGMOID && live && (i * tpr + t) * VEC < p.D)
 #pragma unroll
                 for (int e = 0; e < NP; ++e) sg[i][e] = logistic(get<T, VEC>(z[i], e));
+        auto weighted_act = [&](int i, int e) {             // w_post act(gate)
+            return g == GATE_NONE ? wa[i][e] : f2mul(wa[i][e], act_of(g, get<T, VEC>(z[i], e), sg[i][e]));
+        };
+        // with a = w_post act(gate) y: sum y^2, sum dr a, sum dh w_pre a
+        float iy = 1.f, s_dra = 0.f, s_ma = 0.f;
+        if (post || PRE) {
+            float2 q[3] = {pair(0.f), pair(0.f), pair(0.f)};
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (live && (i * tpr + t) * VEC < p.D)
+#pragma unroll
+                    for (int e = 0; e < NP; ++e) {
+                        const float2 v = get<T, VEC>(y[i], e), a = f2mul(weighted_act(i, e), v);
+                        q[0] = f2fma(v, v, q[0]);
+                        if (p.dr) q[1] = f2fma(get<T, VEC>(dr[i], e), a, q[1]);
+                        if constexpr (PRE) q[2] = f2fma(f2mul(get<T, VEC>(dh[i], e), wb[i][e]), a, q[2]);
+                    }
+            float s1[PRE ? 3 : 2] = {q[0].x + q[0].y, q[1].x + q[1].y};
+            if constexpr (PRE) s1[2] = q[2].x + q[2].y;
+            row_sum(s1, tpr, red[par][0]);
+            if (post) iy = rsqrtf(fmaf(s1[0], inv_d, p.eps));
+            s_dra = s1[1];
+            if constexpr (PRE) s_ma = s1[2];
+        }
+        // sum r^2, sum dh w_pre r, sum r a
+        const float f = iy * p.c;
+        float ir = 0.f, k2 = 0.f;                           // dR = dr + ir dh w_pre - k2 r
+        float k3 = f * s_dra;                               // sum dn yn, then dy = iy dn - k3 y
+        float2 r[PRE ? NV : 1][NP];                         // out, unrounded
         if constexpr (PRE) {
-            float2 s2 = pair(0.f), s3 = pair(0.f);          // sum r^2, sum dh w_pre r
-            const float f = iy * p.c;
+            float2 q[3] = {pair(0.f), pair(0.f), pair(0.f)};
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 if (live && (i * tpr + t) * VEC < p.D) {
 #pragma unroll
                     for (int e = 0; e < NP; ++e) {
-                        float2 a = wa[i][e];
-                        if (g != GATE_NONE) a = f2mul(a, act_of(g, get<T, VEC>(z[i], e), sg[i][e]));
-                        a = f2mul(a, get<T, VEC>(y[i], e));
-                        a = RES ? f2fma(a, pair(f), get<T, VEC>(x[i], e)) : f2mul(a, pair(f));
-                        r[i][e] = a;
-                        s2 = f2fma(a, a, s2);
-                        s3 = f2fma(f2mul(get<T, VEC>(dh[i], e), wb[i][e]), a, s3);
+                        const float2 a = f2mul(weighted_act(i, e), get<T, VEC>(y[i], e));
+                        const float2 v = RES ? f2fma(a, pair(f), get<T, VEC>(x[i], e)) : f2mul(a, pair(f));
+                        r[i][e] = v;
+                        q[0] = f2fma(v, v, q[0]);
+                        q[1] = f2fma(f2mul(get<T, VEC>(dh[i], e), wb[i][e]), v, q[1]);
+                        q[2] = f2fma(v, a, q[2]);
                     }
                 }
             }
-            float s[2] = {s2.x + s2.y, s3.x + s3.y};
+            float s[3] = {q[0].x + q[0].y, q[1].x + q[1].y, q[2].x + q[2].y};
             row_sum(s, tpr, red[par][1]);
             ir = rsqrtf(fmaf(s[0], inv_d, p.eps));
             k2 = s[1] * ir * ir * ir * inv_d;
+            k3 = f * (s_dra + ir * s_ma - k2 * s[2]);
         }
-        float2 dn[NV][NP];
-        float2 a3 = pair(0.f);
+        k3 = post ? k3 * iy * iy * inv_d : 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * tpr + t) * VEC;
             if (live && c < p.D) {
-                float2 dR[NP], dz[NP];
+                float2 dR[NP], dz[NP], dy[NP];
 #pragma unroll
                 for (int e = 0; e < NP; ++e) {
-                    const float2 yn = f2mul(get<T, VEC>(y[i], e), pair(iy));
+                    const float2 yv = get<T, VEC>(y[i], e), yn = f2mul(yv, pair(iy));
                     float2 d = p.dr ? get<T, VEC>(dr[i], e) : pair(0.f);
                     if constexpr (PRE) {
                         const float2 dhe = get<T, VEC>(dh[i], e);
@@ -383,40 +388,21 @@ __global__ void __launch_bounds__(MT, MT == 256 ? 3 : 1) bwd_kernel(const __grid
                     dR[e] = d;
                     const float2 du = f2mul(d, pair(p.c));
                     const float2 q = f2mul(du, yn);
-                    float2 aw = wa[i][e];
                     if (g != GATE_NONE) {
-                        const float2 zz = get<T, VEC>(z[i], e), act = act_of(g, zz, sg[i][e]);
-                        dz[e] = f2mul(f2mul(q, aw), slope_of(g, zz, sg[i][e]));
-                        gpost[i][e] = f2fma(q, act, gpost[i][e]);
-                        aw = f2mul(aw, act);
+                        const float2 zz = get<T, VEC>(z[i], e);
+                        dz[e] = f2mul(f2mul(q, wa[i][e]), slope_of(g, zz, sg[i][e]));
+                        gpost[i][e] = f2fma(q, act_of(g, zz, sg[i][e]), gpost[i][e]);
                     } else {
                         gpost[i][e] = f2add(gpost[i][e], q);
                     }
-                    dn[i][e] = f2mul(du, aw);
-                    a3 = f2fma(q, aw, a3);
+                    dy[e] = f2fma(yv, pair(-k3), f2mul(f2mul(du, weighted_act(i, e)), pair(iy)));
                 }
                 if (p.dx) store_vec<T, VEC>(p.dx, row * p.D + c, dR);
                 if (g != GATE_NONE && p.dgate) store_vec<T, VEC>(p.dgate, row * p.D + c, dz);
+                store_vec<T, VEC>(p.dy, row * p.D + c, dy);
             }
         }
-        load_rest(row + step);
-        float k3 = 0.f;                                     // dy = iy dn - k3 y
-        if (post) {
-            float s1[1] = {a3.x + a3.y};
-            row_sum(s1, tpr, red[par][2]);
-            k3 = s1[0] * iy * iy * inv_d;
-        }
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (i * tpr + t) * VEC;
-            if (live && c < p.D) {
-#pragma unroll
-                for (int e = 0; e < NP; ++e)
-                    dn[i][e] = f2fma(get<T, VEC>(y[i], e), pair(-k3), f2mul(dn[i][e], pair(iy)));
-                store_vec<T, VEC>(p.dy, row * p.D + c, dn[i]);
-            }
-        }
-        load_y(row + step);
+        load(row + step);
     }
     if (!p.want_post && !p.want_pre) return;
     // this CTA's column sums: over its row groups in order, then to the workspace
