@@ -267,11 +267,22 @@ __global__ void __launch_bounds__(MT) fwd_kernel(const __grid_constant__ Params 
 // row sums are what a row waits for, so there are as few as the algebra allows:
 // mean(dn yn) is taken apart into sums over a = w_post act(gate) y that are
 // known before dn is, one round of sums without PRE and two with it.
+// Rows that bwd_kernel requests ahead through shared memory, and its CTAs per
+// SM.  One row's vectors of 512 threads are 40 KB: without rows ahead a CTA
+// waited for memory once per row (198 us on 8192 x 4096; see the launch for
+// the figure with them).
+template <int MT> constexpr int kBwdCtas = MT == 256 ? 3 : 1;
+template <int VEC, int NV, int MT>
+constexpr int kStages = VEC == 1 || 5 * NV * MT * 16 * 2 * kBwdCtas<MT> > 200 * 1024 ? 0
+                        : 5 * NV * MT * 16 * 3 * kBwdCtas<MT> > 200 * 1024 ? 2 : 3;
+
 template <typename T, int VEC, int NV, int MT, int G, bool PRE, bool RES>
-__global__ void __launch_bounds__(MT, MT == 256 ? 3 : 1) bwd_kernel(const __grid_constant__ Params p) {
-    constexpr int NP = kPairs<VEC>;
+__global__ void __launch_bounds__(MT, kBwdCtas<MT>) bwd_kernel(const __grid_constant__ Params p) {
+    constexpr int NP = kPairs<VEC>, ST = kStages<VEC, NV, MT>;
+    using V = VecT<T, VEC>;
     __shared__ float red[2][2][32][3];
-    extern __shared__ float colsum[];  // [2][D], when a CTA holds more than one row
+    extern __shared__ __align__(16) unsigned char dyn[];
+    float *colsum = reinterpret_cast<float *>(dyn);  // [2][D], when a CTA holds more than one row (at the end)
     const int tpr = p.tpr, t = threadIdx.x & (tpr - 1), g = gate_of<G>(p);
     const int per = blockDim.x / tpr, sub = threadIdx.x / tpr;
     const bool post = p.flags & KDA_NORM_POST;
@@ -284,23 +295,37 @@ __global__ void __launch_bounds__(MT, MT == 256 ? 3 : 1) bwd_kernel(const __grid
             gpost[i][e] = pair(0.f);
             if (PRE) gpre[i][e] = pair(0.f);
         }
-    VecT<T, VEC> y[NV], z[NV], x[NV], dr[NV], dh[NV];
-    auto load = [&](long row) {
+    // The vectors of a row, y, gate, residual, dr, dh: with stages they wait in
+    // shared memory, each thread reading back only what it has copied
+    V reg[ST ? 1 : 5][ST ? 1 : NV];
+    V *stage = reinterpret_cast<V *>(dyn) + threadIdx.x;
+    int slot = 0;
+    auto at = [&](int kind, int i) -> V { return ST ? stage[((slot * 5 + kind) * NV + i) * MT] : reg[ST ? 0 : kind][ST ? 0 : i]; };
+    auto load = [&](long row, int to) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * tpr + t) * VEC;
             if (row < p.rows && c < p.D) {
-                y[i] = load_vec<T, VEC>(p.y, row * p.y_ld + c);
-                if (g != GATE_NONE) z[i] = load_vec<T, VEC>(p.gate, row * p.gate_ld + c);
-                if (RES) x[i] = load_vec<T, VEC>(p.x, row * p.x_ld + c);
-                if (p.dr) dr[i] = load_vec<T, VEC>(p.dr, row * p.D + c);
-                if (PRE) dh[i] = load_vec<T, VEC>(p.dh, row * p.D + c);
+                auto one = [&](int kind, const void *base, long off) {
+                    if constexpr (ST > 0)
+                        sm100::cp_async16(&stage[((to * 5 + kind) * NV + i) * MT], (const T *)base + off, true);
+                    else
+                        reg[ST ? 0 : kind][ST ? 0 : i] = load_vec<T, VEC>(base, off);
+                };
+                one(0, p.y, row * p.y_ld + c);
+                if (g != GATE_NONE) one(1, p.gate, row * p.gate_ld + c);
+                if (RES) one(2, p.x, row * p.x_ld + c);
+                if (p.dr) one(3, p.dr, row * p.D + c);
+                if (PRE) one(4, p.dh, row * p.D + c);
             }
         }
+        if (ST > 0) sm100::cp_async_commit();
     };
     const long step = (long)gridDim.x * per;
     long row = (long)blockIdx.x * per + sub;
-    load(row);
+    if (ST == 0) load(row, 0);
+#pragma unroll
+    for (int i = 0; i + 1 < ST; ++i) load(row + i * step, i);
     float2 wa[NV][NP], wb[PRE ? NV : 1][NP];
     if (NV == 1) {
         load_weight<T, VEC, NV>(wa, p.w_post, tpr, t, p.D);
@@ -309,6 +334,10 @@ __global__ void __launch_bounds__(MT, MT == 256 ? 3 : 1) bwd_kernel(const __grid
     int par = 0;
     for (long row0 = (long)blockIdx.x * per; row0 < p.rows; row0 += step, row += step, par ^= 1) {
         const bool live = row < p.rows;
+        if constexpr (ST > 0) {
+            load(row + (ST - 1) * step, slot == 0 ? ST - 1 : slot - 1);
+            sm100::cp_async_wait<ST - 1>();
+        }
         if (NV > 1) {
             load_weight<T, VEC, NV>(wa, p.w_post, tpr, t, p.D);
             if constexpr (PRE) load_weight<T, VEC, NV>(wb, p.w_pre, tpr, t, p.D);
@@ -318,9 +347,9 @@ __global__ void __launch_bounds__(MT, MT == 256 ? 3 : 1) bwd_kernel(const __grid
         for (int i = 0; i < NV; ++i)
             if (g >= GATE_SIGMOID && live && (i * tpr + t) * VEC < p.D)
 #pragma unroll
-                for (int e = 0; e < NP; ++e) sg[i][e] = logistic(get<T, VEC>(z[i], e));
+                for (int e = 0; e < NP; ++e) sg[i][e] = logistic(get<T, VEC>(at(1, i), e));
         auto weighted_act = [&](int i, int e) {             // w_post act(gate)
-            return g == GATE_NONE ? wa[i][e] : f2mul(wa[i][e], act_of(g, get<T, VEC>(z[i], e), sg[i][e]));
+            return g == GATE_NONE ? wa[i][e] : f2mul(wa[i][e], act_of(g, get<T, VEC>(at(1, i), e), sg[i][e]));
         };
         // with a = w_post act(gate) y: sum y^2, sum dr a, sum dh w_pre a
         float iy = 1.f, s_dra = 0.f, s_ma = 0.f;
@@ -331,10 +360,10 @@ __global__ void __launch_bounds__(MT, MT == 256 ? 3 : 1) bwd_kernel(const __grid
                 if (live && (i * tpr + t) * VEC < p.D)
 #pragma unroll
                     for (int e = 0; e < NP; ++e) {
-                        const float2 v = get<T, VEC>(y[i], e), a = f2mul(weighted_act(i, e), v);
+                        const float2 v = get<T, VEC>(at(0, i), e), a = f2mul(weighted_act(i, e), v);
                         q[0] = f2fma(v, v, q[0]);
-                        if (p.dr) q[1] = f2fma(get<T, VEC>(dr[i], e), a, q[1]);
-                        if constexpr (PRE) q[2] = f2fma(f2mul(get<T, VEC>(dh[i], e), wb[i][e]), a, q[2]);
+                        if (p.dr) q[1] = f2fma(get<T, VEC>(at(3, i), e), a, q[1]);
+                        if constexpr (PRE) q[2] = f2fma(f2mul(get<T, VEC>(at(4, i), e), wb[i][e]), a, q[2]);
                     }
             float s1[PRE ? 3 : 2] = {q[0].x + q[0].y, q[1].x + q[1].y};
             if constexpr (PRE) s1[2] = q[2].x + q[2].y;
@@ -355,11 +384,11 @@ __global__ void __launch_bounds__(MT, MT == 256 ? 3 : 1) bwd_kernel(const __grid
                 if (live && (i * tpr + t) * VEC < p.D) {
 #pragma unroll
                     for (int e = 0; e < NP; ++e) {
-                        const float2 a = f2mul(weighted_act(i, e), get<T, VEC>(y[i], e));
-                        const float2 v = RES ? f2fma(a, pair(f), get<T, VEC>(x[i], e)) : f2mul(a, pair(f));
+                        const float2 a = f2mul(weighted_act(i, e), get<T, VEC>(at(0, i), e));
+                        const float2 v = RES ? f2fma(a, pair(f), get<T, VEC>(at(2, i), e)) : f2mul(a, pair(f));
                         r[i][e] = v;
                         q[0] = f2fma(v, v, q[0]);
-                        q[1] = f2fma(f2mul(get<T, VEC>(dh[i], e), wb[i][e]), v, q[1]);
+                        q[1] = f2fma(f2mul(get<T, VEC>(at(4, i), e), wb[i][e]), v, q[1]);
                         q[2] = f2fma(v, a, q[2]);
                     }
                 }
@@ -378,10 +407,10 @@ __global__ void __launch_bounds__(MT, MT == 256 ? 3 : 1) bwd_kernel(const __grid
                 float2 dR[NP], dz[NP], dy[NP];
 #pragma unroll
                 for (int e = 0; e < NP; ++e) {
-                    const float2 yv = get<T, VEC>(y[i], e), yn = f2mul(yv, pair(iy));
-                    float2 d = p.dr ? get<T, VEC>(dr[i], e) : pair(0.f);
+                    const float2 yv = get<T, VEC>(at(0, i), e), yn = f2mul(yv, pair(iy));
+                    float2 d = p.dr ? get<T, VEC>(at(3, i), e) : pair(0.f);
                     if constexpr (PRE) {
-                        const float2 dhe = get<T, VEC>(dh[i], e);
+                        const float2 dhe = get<T, VEC>(at(4, i), e);
                         d = f2fma(r[i][e], pair(-k2), f2fma(f2mul(dhe, wb[i][e]), pair(ir), d));
                         gpre[i][e] = f2fma(dhe, f2mul(r[i][e], pair(ir)), gpre[i][e]);
                     }
@@ -389,7 +418,7 @@ __global__ void __launch_bounds__(MT, MT == 256 ? 3 : 1) bwd_kernel(const __grid
                     const float2 du = f2mul(d, pair(p.c));
                     const float2 q = f2mul(du, yn);
                     if (g != GATE_NONE) {
-                        const float2 zz = get<T, VEC>(z[i], e);
+                        const float2 zz = get<T, VEC>(at(1, i), e);
                         dz[e] = f2mul(f2mul(q, wa[i][e]), slope_of(g, zz, sg[i][e]));
                         gpost[i][e] = f2fma(q, act_of(g, zz, sg[i][e]), gpost[i][e]);
                     } else {
@@ -402,8 +431,10 @@ __global__ void __launch_bounds__(MT, MT == 256 ? 3 : 1) bwd_kernel(const __grid
                 store_vec<T, VEC>(p.dy, row * p.D + c, dy);
             }
         }
-        load(row + step);
+        if (ST == 0) load(row + step, 0);
+        slot = slot + 1 == ST ? 0 : slot + 1;
     }
+    if (ST > 0) __syncthreads();  // the stages become the column sums
     if (!p.want_post && !p.want_pre) return;
     // this CTA's column sums: over its row groups in order, then to the workspace
     float *dst = p.part + (size_t)blockIdx.x * 2 * p.D;
@@ -484,8 +515,13 @@ Shape choose_shape(int D, int vec) {
 template <typename T, int VEC, int NV, int MT, int G, bool PRE, bool RES>
 void launch_k(const Params &p, const Shape &s, bool bwd, unsigned grid, cudaStream_t st) {
     if (bwd) {
-        const size_t bytes = s.per > 1 ? (size_t)2 * p.D * sizeof(float) : 0;
-        bwd_kernel<T, VEC, NV, MT, G, PRE, RES><<<grid, s.threads, bytes, st>>>(p);
+        constexpr int stages = 5 * kStages<VEC, NV, MT> * NV * MT * 16;
+        if (stages > 48 * 1024) {
+            static std::atomic<uint64_t> done;
+            if (lin::allow_smem(done, (const void *)bwd_kernel<T, VEC, NV, MT, G, PRE, RES>, stages) != cudaSuccess) return;
+        }
+        const int sums = s.per > 1 ? 2 * p.D * (int)sizeof(float) : 0;
+        bwd_kernel<T, VEC, NV, MT, G, PRE, RES><<<grid, s.threads, std::max(stages, sums), st>>>(p);
     } else {
         fwd_kernel<T, VEC, NV, MT, G, RES, PRE><<<grid, s.threads, 0, st>>>(p);
     }
@@ -565,7 +601,7 @@ int check_elems(const void *const *ptrs, int n, size_t esz) {
 
 int bwd_parts(int64_t rows, const Shape &s) {
     const int64_t batches = (rows + s.per - 1) / s.per;
-    return (int)std::max<int64_t>(1, std::min<int64_t>(batches, (int64_t)sm_count() * (s.threads == 256 ? 3 : 1)));
+    return (int)std::max<int64_t>(1, std::min<int64_t>(batches, (int64_t)sm_count() * (s.threads == 256 ? kda::norm::kBwdCtas<256> : 1)));
 }
 
 }  // namespace
