@@ -99,31 +99,45 @@ KDA_DEVICE void store_vec(void *base, long at, const float2 (&v)[kPairs<VEC>]) {
 }
 
 // Sum of N values over the TPR threads of a row (every thread gets it).  red
-// is not written again before another barrier of the CTA.
+// is not written again before another barrier of the CTA.  Two or three sums
+// over several warps go through one tree of four: a step halves the values
+// that a lane still carries, 6 shuffles instead of 5 for each.
 template <int N>
-KDA_DEVICE void row_sum(float (&v)[N], int tpr, float (*red)[3]) {
-    if (tpr >= 32) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-            for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-    } else {
+KDA_DEVICE void row_sum(float (&v)[N], int tpr, float (*red)[4]) {
+    const unsigned all = 0xffffffffu;
+    if (tpr <= 32) {
         for (int o = tpr >> 1; o > 0; o >>= 1)
 #pragma unroll
-            for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+            for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(all, v[i], o);
+        return;
     }
-    if (tpr > 32) {
-        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = tpr >> 5, first = warp / nw * nw;
-        if (lane == 0)
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = tpr >> 5, first = warp / nw * nw;
+    if constexpr (N == 1) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) red[warp][i] = v[i];
+        for (int o = 16; o > 0; o >>= 1) v[0] += __shfl_xor_sync(all, v[0], o);
+        if (lane == 0) red[warp][0] = v[0];
         __syncthreads();
+        v[0] = lane < nw ? red[first + lane][0] : 0.f;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            v[i] = lane < nw ? red[first + lane][i] : 0.f;
+        for (int o = 16; o > 0; o >>= 1) v[0] += __shfl_xor_sync(all, v[0], o);
+    } else {
+        float x[4] = {v[0], v[1], N > 2 ? v[N > 2 ? 2 : 0] : 0.f, 0.f};
+        const bool hi = lane & 16, mid = lane & 8;  // value 2 hi + mid stays in this lane
+        const float y0 = (hi ? x[2] : x[0]) + __shfl_xor_sync(all, hi ? x[0] : x[2], 16);
+        const float y1 = (hi ? x[3] : x[1]) + __shfl_xor_sync(all, hi ? x[1] : x[3], 16);
+        float z = (mid ? y1 : y0) + __shfl_xor_sync(all, mid ? y0 : y1, 8);
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-        }
+        for (int o = 4; o > 0; o >>= 1) z += __shfl_xor_sync(all, z, o);
+        if ((lane & 7) == 0) red[warp][(hi ? 2 : 0) + (mid ? 1 : 0)] = z;
+        __syncthreads();
+        z = 0.f;  // lane: value lane % 4 of warps lane / 4, + 8, ...
+#pragma unroll
+        for (int w = 0; w < 32; w += 8)
+            if (w + (lane >> 2) < nw) z += red[first + w + (lane >> 2)][lane & 3];
+#pragma unroll
+        for (int o = 16; o > 2; o >>= 1) z += __shfl_xor_sync(all, z, o);
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = __shfl_sync(all, z, i);
     }
 }
 
@@ -179,7 +193,7 @@ KDA_DEVICE void load_weight(float2 (&w)[NV][kPairs<VEC>], const void *base, int 
 template <typename T, int VEC, int NV, int MT, int G, bool RES, bool PRE>
 __global__ void __launch_bounds__(MT) fwd_kernel(const __grid_constant__ Params p) {
     constexpr int NP = kPairs<VEC>;
-    __shared__ float red[2][2][32][3];
+    __shared__ float red[2][2][32][4];
     const int tpr = p.tpr, t = threadIdx.x & (tpr - 1), g = gate_of<G>(p);
     const int per = blockDim.x / tpr;
     const bool post = p.flags & KDA_NORM_POST;
@@ -280,7 +294,7 @@ template <typename T, int VEC, int NV, int MT, int G, bool PRE, bool RES>
 __global__ void __launch_bounds__(MT, kBwdCtas<MT>) bwd_kernel(const __grid_constant__ Params p) {
     constexpr int NP = kPairs<VEC>, ST = kStages<VEC, NV, MT>;
     using V = VecT<T, VEC>;
-    __shared__ float red[2][2][32][3];
+    __shared__ float red[2][2][32][4];
     extern __shared__ __align__(16) unsigned char dyn[];
     float *colsum = reinterpret_cast<float *>(dyn);  // [2][D], when a CTA holds more than one row (at the end)
     const int tpr = p.tpr, t = threadIdx.x & (tpr - 1), g = gate_of<G>(p);
@@ -297,7 +311,7 @@ __global__ void __launch_bounds__(MT, kBwdCtas<MT>) bwd_kernel(const __grid_cons
         }
     // The vectors of a row, y, gate, residual, dr, dh: with stages they wait in
     // shared memory, each thread reading back only what it has copied
-    V reg[ST ? 1 : 5][ST ? 1 : NV];
+    V reg[ST ? 1 : 5][ST ? 1 : NV] = {};
     V *stage = reinterpret_cast<V *>(dyn) + threadIdx.x;
     int slot = 0;
     auto at = [&](int kind, int i) -> V { return ST ? stage[((slot * 5 + kind) * NV + i) * MT] : reg[ST ? 0 : kind][ST ? 0 : i]; };
