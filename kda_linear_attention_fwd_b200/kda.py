@@ -361,39 +361,35 @@ def chunk_fwd_check(workspace, stream=None, lib=None) -> int:
 _CODES = {torch.bfloat16: KDA_DTYPE_BF16, torch.float32: KDA_DTYPE_F32}
 
 
-class _on:
-    """The call's device and stream: the tensors' device is made current (the
-    library launches there), the stream defaults to that device's current one."""
-    __slots__ = ("dev", "prev")
-
-    def __init__(self, t):
-        self.dev = t.device.index
-
-    def __enter__(self):
-        self.prev = torch.cuda.current_device()
-        if self.prev != self.dev:
-            torch.cuda.set_device(self.dev)
-        return self
-
-    def __exit__(self, *exc):
-        if self.prev != self.dev:
-            torch.cuda.set_device(self.prev)
-
-    def stream(self, stream):
-        return torch._C._cuda_getCurrentRawStream(self.dev) if stream is None else stream.cuda_stream
+def _launch(fn, dev, stream, *args):
+    """Calls a library function on the tensors' device (made current for the
+    call) with the given stream or that device's current one; raises its error."""
+    if torch._C._cuda_getDevice() != dev:
+        with torch.cuda.device(dev):
+            return _launch(fn, dev, stream, *args)
+    st = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+    if st:
+        _check(fn.__name__, st)
 
 
-def _tensor(name, t, shape, dtype, like):
-    """Refuses a tensor the kernels could not read as it is."""
-    if t.dtype != dtype or t.shape != shape or t.device != like.device or not t.is_contiguous():
-        raise ValueError(f"{name}: want a contiguous {dtype} tensor of shape {tuple(shape)} on "
-                         f"{like.device}, got {t.dtype} {tuple(t.shape)} on {t.device}"
-                         f"{'' if t.is_contiguous() else ', not contiguous'}")
-    return t.data_ptr()
+def _tensor(name, t, shape, dtype, dev):
+    """Address of a tensor, refused when the kernels could not read it as it is."""
+    if t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name}: want a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{dev}, "
+                     f"got {t.dtype} {tuple(t.shape)} on {t.device}"
+                     f"{'' if t.is_contiguous() else ', not contiguous'}")
 
 
-def _opt(name, t, shape, dtype, like):
-    return None if t is None else _tensor(name, t, shape, dtype, like)
+def _opt(name, t, shape, dtype, dev):
+    return None if t is None else _tensor(name, t, shape, dtype, dev)
+
+
+def _device(t):
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("all tensors must be CUDA tensors")
+    return dev
 
 
 def _code(t):
@@ -403,26 +399,31 @@ def _code(t):
         raise TypeError(f"unsupported dtype {t.dtype}") from None
 
 
-def _space(workspace, need, like):
+def _space(workspace, dev, need):
+    """(tensor, address, bytes); need() sizes a new one."""
     if workspace is None:
-        return torch.empty(max(need, 16), dtype=torch.uint8, device=like.device)
-    if workspace.device != like.device or not workspace.is_contiguous():
-        raise ValueError(f"workspace: want a contiguous tensor on {like.device}")
-    return workspace  # too small a one is refused by the library
+        if torch._C._cuda_getDevice() != dev:  # the plan is the device's
+            with torch.cuda.device(dev):
+                return _space(None, dev, need)
+        workspace = torch.empty(max(need(), 16), dtype=torch.uint8, device="cuda")
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace: want a contiguous tensor on cuda:{dev}")
+    # too small a one is refused by the library
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def _lin_shapes(q, k, v, g):
-    if not q.is_cuda:
-        raise ValueError("all tensors must be CUDA tensors")
+    dev = _device(q)
     if q.dim() != 3 or v.dim() != 3:
         raise ValueError("q, k are [tokens, Hk, dk], v is [tokens, H, dv]")
-    T, Hk, dk = q.shape
+    T, Hk, dk = shape = q.shape
     H, dv = v.shape[1], v.shape[2]
     per_head = g.dim() == 1
     dt = q.dtype
-    ptrs = (_tensor("q", q, q.shape, dt, q), _tensor("k", k, q.shape, dt, q),
-            _tensor("v", v, (T, H, dv), dt, q), _tensor("g", g, (H,) if per_head else (T, H), dt, q))
-    return T, H, Hk, dk, dv, LIN_DECAY_PER_HEAD if per_head else 0, _code(q), ptrs
+    code = _code(q)
+    ptrs = (_tensor("q", q, shape, dt, dev), _tensor("k", k, shape, dt, dev), _tensor("v", v, (T, H, dv), dt, dev),
+            _tensor("g", g, (H,) if per_head else (T, H), dt, dev))
+    return dev, T, H, Hk, dk, dv, LIN_DECAY_PER_HEAD if per_head else 0, code, ptrs
 
 
 def _host_offsets(cu_seqlens_host, N):
@@ -447,25 +448,21 @@ def lin_chunk_fwd(q, k, v, g, cu_seqlens, *, scale=1.0, initial_state=None, fina
     cu_seqlens int32 [N+1] (device).  Returns (out, final_state); final_state
     may be initial_state itself."""
     lib = load()
-    T, H, Hk, dk, dv, flags, code, ptrs = _lin_shapes(q, k, v, g)
+    dev, T, H, Hk, dk, dv, flags, code, ptrs = _lin_shapes(q, k, v, g)
     N = cu_seqlens.shape[0] - 1
-    p_cu = _tensor("cu_seqlens", cu_seqlens, (N + 1,), torch.int32, q)
+    p_cu = _tensor("cu_seqlens", cu_seqlens, (N + 1,), torch.int32, dev)
     states = (N, H, dk, dv)
     if out is None:
         out = torch.empty_like(v)
     if final_state is None and output_final_state:
-        final_state = torch.empty(states, dtype=torch.float32, device=q.device)
-    p_out = _tensor("out", out, v.shape, q.dtype, q)
-    p_s0 = _opt("initial_state", initial_state, states, torch.float32, q)
-    p_s1 = _opt("final_state", final_state, states, torch.float32, q)
+        final_state = q.new_empty(states, dtype=torch.float32)
+    p_out = _tensor("out", out, v.shape, q.dtype, dev)
+    p_s0 = _opt("initial_state", initial_state, states, torch.float32, dev)
+    p_s1 = _opt("final_state", final_state, states, torch.float32, dev)
     host = _host_offsets(cu_seqlens_host, N)
-    with _on(q) as on:
-        ws = _space(workspace, 0 if workspace is not None else lib.kda_lin_chunk_fwd_workspace_size(
-            T, N, H, Hk, dk, dv, code), q)
-        st = lib.kda_lin_chunk_fwd(*ptrs, p_out, p_cu, host, N, T, H, Hk, dk, dv, code, scale, flags,
-                                   p_s0, p_s1, ws.data_ptr(), ws.numel() * ws.element_size(),
-                                   on.stream(stream))
-    _check("kda_lin_chunk_fwd", st)
+    ws, p_ws, n_ws = _space(workspace, dev, lambda: lib.kda_lin_chunk_fwd_workspace_size(T, N, H, Hk, dk, dv, code))
+    _launch(lib.kda_lin_chunk_fwd, dev, stream, *ptrs, p_out, p_cu, host, N, T, H, Hk, dk, dv, code, scale, flags,
+            p_s0, p_s1, p_ws, n_ws)
     return out, final_state
 
 
@@ -473,15 +470,12 @@ def lin_decode_step(q, k, v, g, state, *, scale=1.0, out=None, stream=None):
     """One token per sequence.  q, k [N, Hk, dk]; v [N, H, dv]; g [N, H] or
     [H]; state [N, H, dk, dv] fp32, updated in place.  Returns out."""
     lib = load()
-    N, H, Hk, dk, dv, flags, code, ptrs = _lin_shapes(q, k, v, g)
+    dev, N, H, Hk, dk, dv, flags, code, ptrs = _lin_shapes(q, k, v, g)
     if out is None:
         out = torch.empty_like(v)
-    p_out = _tensor("out", out, v.shape, q.dtype, q)
-    p_s = _tensor("state", state, (N, H, dk, dv), torch.float32, q)
-    with _on(q) as on:
-        st = lib.kda_lin_decode_step(*ptrs, p_out, p_s, N, H, Hk, dk, dv, code, scale, flags,
-                                     on.stream(stream))
-    _check("kda_lin_decode_step", st)
+    p_out = _tensor("out", out, v.shape, q.dtype, dev)
+    p_s = _tensor("state", state, (N, H, dk, dv), torch.float32, dev)
+    _launch(lib.kda_lin_decode_step, dev, stream, *ptrs, p_out, p_s, N, H, Hk, dk, dv, code, scale, flags)
     return out
 
 
@@ -494,39 +488,33 @@ def lin_bwd(q, k, v, g, dy, cu_seqlens, *, scale=1.0, initial_state=None, d_fina
     """Gradients of lin_chunk_fwd: a dict of dq, dk [T, Hk, dk], dv [T, H, dv],
     dg (the shape of g), all in the inputs' dtype, and ds0 [N, H, dk, dv] fp32."""
     lib = load()
-    T, H, Hk, dk, dv, flags, code, ptrs = _lin_shapes(q, k, v, g)
+    dev, T, H, Hk, dk, dv, flags, code, ptrs = _lin_shapes(q, k, v, g)
     N = cu_seqlens.shape[0] - 1
-    p_cu = _tensor("cu_seqlens", cu_seqlens, (N + 1,), torch.int32, q)
-    p_dy = _tensor("dy", dy, v.shape, q.dtype, q)
+    p_cu = _tensor("cu_seqlens", cu_seqlens, (N + 1,), torch.int32, dev)
+    p_dy = _tensor("dy", dy, v.shape, q.dtype, dev)
     states = (N, H, dk, dv)
-    p_s0 = _opt("initial_state", initial_state, states, torch.float32, q)
-    p_ds = _opt("d_final_state", d_final_state, states, torch.float32, q)
+    p_s0 = _opt("initial_state", initial_state, states, torch.float32, dev)
+    p_ds = _opt("d_final_state", d_final_state, states, torch.float32, dev)
     # tokens outside every sequence keep what is there: zeros only where the
     # offsets are not known to cover every token
     new = torch.empty_like if cu_seqlens_host is not None else torch.zeros_like
     out = {"dq": new(q), "dk": new(k), "dv": new(v), "dg": new(g),
-           "ds0": torch.empty(states, dtype=torch.float32, device=q.device)}
+           "ds0": q.new_empty(states, dtype=torch.float32)}
     host = _host_offsets(cu_seqlens_host, N)
-    with _on(q) as on:
-        ws = _space(workspace, 0 if workspace is not None else lib.kda_lin_bwd_workspace_size(
-            T, N, H, Hk, dk, dv), q)
-        st = lib.kda_lin_bwd(*ptrs, p_dy, p_cu, host, N, T, H, Hk, dk, dv, code, scale, flags, p_s0, p_ds,
-                             out["dq"].data_ptr(), out["dk"].data_ptr(), out["dv"].data_ptr(),
-                             out["dg"].data_ptr(), out["ds0"].data_ptr(), ws.data_ptr(),
-                             ws.numel() * ws.element_size(), on.stream(stream))
-    _check("kda_lin_bwd", st)
+    ws, p_ws, n_ws = _space(workspace, dev, lambda: lib.kda_lin_bwd_workspace_size(T, N, H, Hk, dk, dv))
+    _launch(lib.kda_lin_bwd, dev, stream, *ptrs, p_dy, p_cu, host, N, T, H, Hk, dk, dv, code, scale, flags, p_s0, p_ds,
+            *(x.data_ptr() for x in out.values()), p_ws, n_ws)
     return out
 
 
 # ------------------------------------------------------------ norms around a block
-def _norm_rows(name, t, like):
+def _norm_rows(name, t, shape, dtype, dev):
     """(address, row stride) of a tensor whose rows (last dimension) are contiguous."""
     if t is None:
         return None, 0
-    if t.dtype != like.dtype or t.shape != like.shape or t.device != like.device:
-        raise ValueError(f"{name}: want {like.dtype} {tuple(like.shape)} on {like.device}, got "
-                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
-    D = t.shape[-1]
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape:
+        raise ValueError(f"{name}: want {dtype} {tuple(shape)} on cuda:{dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    D = shape[-1]
     if t.is_contiguous():
         return t.data_ptr(), D
     rows = t.flatten(0, -2) if t.dim() != 2 else t
@@ -554,24 +542,22 @@ def block_norm(y, *, post_norm=True, post_weight=None, gate=None, gate_logits=Fa
     dimension of y [..., D].  Returns (out, normed); normed is None without
     pre_norm.  out and normed may be y, gate or residual themselves."""
     lib = load()
-    if not y.is_cuda:
-        raise ValueError("all tensors must be CUDA tensors")
-    D = y.shape[-1]
+    dev = _device(y)
+    shape = y.shape
+    D = shape[-1]
     code, dt = _code(y), y.dtype
     flags = _norm_flags(post_norm, post_weight, pre_norm, pre_weight, gate, gate_logits, gate_silu)
-    p_y, s_y = _norm_rows("y", y, y)
-    p_g, s_g = _norm_rows("gate", gate, y)
-    p_x, s_x = _norm_rows("residual", residual, y)
-    p_wp, p_wn = _opt("post_weight", post_weight, (D,), dt, y), _opt("pre_weight", pre_weight, (D,), dt, y)
+    p_y, s_y = _norm_rows("y", y, shape, dt, dev)
+    p_g, s_g = _norm_rows("gate", gate, shape, dt, dev)
+    p_x, s_x = _norm_rows("residual", residual, shape, dt, dev)
+    p_wp, p_wn = _opt("post_weight", post_weight, (D,), dt, dev), _opt("pre_weight", pre_weight, (D,), dt, dev)
     if out is None:
-        out = torch.empty(y.shape, dtype=dt, device=y.device)
+        out = y.new_empty(shape)
     if normed is None and pre_norm:
-        normed = torch.empty(y.shape, dtype=dt, device=y.device)
-    p_out, p_n = _tensor("out", out, y.shape, dt, y), _opt("normed", normed, y.shape, dt, y)
-    with _on(y) as on:
-        st = lib.kda_block_norm(p_y, s_y, p_wp, p_g, s_g, p_x, s_x, p_wn, p_out, p_n,
-                                y.numel() // D if D else 0, D, code, res_scale, eps, flags, on.stream(stream))
-    _check("kda_block_norm", st)
+        normed = y.new_empty(shape)
+    p_out, p_n = _tensor("out", out, shape, dt, dev), _opt("normed", normed, shape, dt, dev)
+    _launch(lib.kda_block_norm, dev, stream, p_y, s_y, p_wp, p_g, s_g, p_x, s_x, p_wn, p_out, p_n,
+            y.numel() // D if D else 0, D, code, res_scale, eps, flags)
     return out, normed
 
 
@@ -582,31 +568,26 @@ def block_norm_bwd(dout, dnormed, y, *, post_norm=True, post_weight=None, gate=N
     dict of dy, dgate, dresidual in y's dtype and dpost_weight, dpre_weight [D]
     fp32; None for what was not given."""
     lib = load()
-    if not y.is_cuda:
-        raise ValueError("all tensors must be CUDA tensors")
-    D = y.shape[-1]
+    dev = _device(y)
+    shape = y.shape
+    D = shape[-1]
     code, dt = _code(y), y.dtype
     flags = _norm_flags(post_norm, post_weight, pre_norm, pre_weight, gate, gate_logits, gate_silu)
     if dout is None and dnormed is None:
         raise ValueError("dout and dnormed are both None")
-    p_y, s_y = _norm_rows("y", y, y)
-    p_g, s_g = _norm_rows("gate", gate, y)
-    p_x, s_x = _norm_rows("residual", residual, y)
-    p_wp, p_wn = _opt("post_weight", post_weight, (D,), dt, y), _opt("pre_weight", pre_weight, (D,), dt, y)
-    p_do, p_dn = _opt("dout", dout, y.shape, dt, y), _opt("dnormed", dnormed, y.shape, dt, y)
+    p_y, s_y = _norm_rows("y", y, shape, dt, dev)
+    p_g, s_g = _norm_rows("gate", gate, shape, dt, dev)
+    p_x, s_x = _norm_rows("residual", residual, shape, dt, dev)
+    p_wp, p_wn = _opt("post_weight", post_weight, (D,), dt, dev), _opt("pre_weight", pre_weight, (D,), dt, dev)
+    p_do, p_dn = _opt("dout", dout, shape, dt, dev), _opt("dnormed", dnormed, shape, dt, dev)
     rows = y.numel() // D if D else 0
 
     def like(t, shape=None, dtype=None):
-        return None if t is None else torch.empty(shape or t.shape, dtype=dtype or t.dtype, device=y.device)
+        return None if t is None else y.new_empty(shape or t.shape, dtype=dtype or t.dtype)
 
     got = {"dy": like(y), "dgate": like(gate), "dresidual": like(residual),
            "dpost_weight": like(post_weight, (D,), torch.float32), "dpre_weight": like(pre_weight, (D,), torch.float32)}
-    with _on(y) as on:
-        need = lib.kda_block_norm_bwd_workspace_size(rows, D, code) if workspace is None else 0
-        ws = _space(workspace, need, y)
-        st = lib.kda_block_norm_bwd(p_do, p_dn, p_y, s_y, p_wp, p_g, s_g, p_x, s_x, p_wn,
-                                    *(None if t is None else t.data_ptr() for t in got.values()), rows, D, code,
-                                    res_scale, eps, flags, ws.data_ptr(), ws.numel() * ws.element_size(),
-                                    on.stream(stream))
-    _check("kda_block_norm_bwd", st)
+    ws, p_ws, n_ws = _space(workspace, dev, lambda: lib.kda_block_norm_bwd_workspace_size(rows, D, code))
+    _launch(lib.kda_block_norm_bwd, dev, stream, p_do, p_dn, p_y, s_y, p_wp, p_g, s_g, p_x, s_x, p_wn,
+            *(None if t is None else t.data_ptr() for t in got.values()), rows, D, code, res_scale, eps, flags, p_ws, n_ws)
     return got
