@@ -12,13 +12,13 @@
 namespace kda {
 namespace lin {
 
-cudaError_t launch_rec(const Params &p, int mode, bool is_bf16, int da, int db, cudaStream_t st);
-cudaError_t launch_tc(const Params &p, int mode, int da, int db, cudaStream_t st);
-cudaError_t launch_scan(float *z, const float *gamma, int W, int H, int elems, bool rev, cudaStream_t st);
+cudaError_t rec_forward(const Params &p, int dk, int dv, cudaStream_t st);
+cudaError_t rec_backward(const Params &q, const Params &k, const Params &v, int dk, int dv, cudaStream_t st);
+cudaError_t tc_forward(const Params &p, int dk, int dv, cudaStream_t st);
+cudaError_t tc_backward(const Params &q, const Params &k, const Params &v, int dk, int dv, cudaStream_t st);
 cudaError_t launch_decode(bool bf16, int dk, int dv, const void *q, const void *k, const void *v, const void *g,
                           void *out, float *state, long nh, int H, int rep, int g_per_head, float scale, int sms,
                           cudaStream_t st);
-enum { kFwd, kSum, kSumR, kDq, kDk, kDv };  // launch_rec's modes
 
 int sm_count() {
     static std::atomic<int> cache[64];
@@ -60,7 +60,10 @@ struct Tokens {
 // out[t][hk][i] = sum over r of in[t][hk * rep + r][i]: the gradient of a head
 // shared by rep heads, rounded once.  D a multiple of 4.
 template <typename T>
-__global__ void __launch_bounds__(256) head_sum_kernel(const float4 *in, T *out, const Tokens tk, int Hk, int rep, int d4) {
+__global__ void __launch_bounds__(256) head_sum_kernel(const float4 *in0, T *out0, const float4 *in1, T *out1, const Tokens tk,
+                                                       int Hk, int rep, int d4) {
+    const float4 *in = blockIdx.y ? in1 : in0;
+    T *out = blockIdx.y ? out1 : out0;
     const long row4 = (long)Hk * d4;
     for (long i = tk.first() * row4 + (long)blockIdx.x * 256 + threadIdx.x; i < tk.last() * row4; i += (long)gridDim.x * 256) {
         const long th = i / d4, c = i % d4;
@@ -129,24 +132,22 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 struct Windows {
     int win, W;
 };
-// Windows of a multiple of 64 tokens, as many as fill two CTAs per SM once.
-// A call with more than one window also runs the summary pass (about 0.6 of
-// the time of the main one) and the scan, so short calls stay in one.
-Windows choose_windows(int T, int H, bool tc) {
-    if (tc) {  // one CTA per SM, windows of whole 128-token chunks
-        const long target = std::max(1L, (long)sm_count() / H);
-        const long win = std::max(128L, ((T + target - 1) / target + 127) / 128 * 128);
-        return {(int)win, std::max(1, (int)((T + win - 1) / win))};
-    }
-    const long slots = 2L * sm_count();
-    const long target = std::max(1L, slots / H);
-    long win = ((T + target - 1) / target + 63) / 64 * 64;
-    win = std::max(win, 64L);
-    if (1.6 * win + 40 >= T) win = std::max((T + 63L) / 64 * 64, 64L);
+// As many windows as fill the SMs once: one CTA per SM and whole 128-token
+// chunks on the tensor cores, two CTAs per SM token by token, there in whole
+// 64-token chunks for the gradient and 32 tokens otherwise.  A call with more
+// than one window also runs the summary pass (about 0.6 of the time of the
+// main one) and the scan (about as long as 25 tokens), so what is shorter
+// stays in one.
+enum class Pass { tc, rec_fwd, rec_bwd };
+Windows choose_windows(int T, int H, Pass pass) {
+    const long step = pass == Pass::tc ? 128 : pass == Pass::rec_bwd ? 64 : 32;
+    const long target = std::max(1L, (pass == Pass::tc ? 1L : 2L) * sm_count() / H);
+    long win = std::max(step, ((T + target - 1) / target + step - 1) / step * step);
+    if (pass != Pass::tc && 1.6 * win + 25 >= T) win = std::max(step, (T + step - 1) / step * step);
     return {(int)win, std::max(1, (int)((T + win - 1) / win))};
 }
 
-// bf16 on the tensor cores, fp32 token by token
+// bf16 on the tensor cores, fp32 (and calls with no tokens at all) token by token
 bool use_tc(kda_dtype dtype, int T) { return dtype == KDA_DTYPE_BF16 && T > 0; }
 
 struct FwdLayout {
@@ -225,7 +226,7 @@ extern "C" {
 size_t kda_lin_chunk_fwd_workspace_size(int32_t total_tokens, int32_t num_seqs, int32_t H, int32_t Hk, int32_t dk,
                                         int32_t dv, kda_dtype dtype) {
     if (check_sizes(num_seqs, total_tokens, H, Hk, dk, dv, dtype, 0) != KDA_OK) return 0;
-    return fwd_layout(choose_windows(total_tokens, H, use_tc(dtype, total_tokens)), H, dk, dv).total;
+    return fwd_layout(choose_windows(total_tokens, H, use_tc(dtype, total_tokens) ? Pass::tc : Pass::rec_fwd), H, dk, dv).total;
 }
 
 int kda_lin_chunk_fwd(const void *q, const void *k, const void *v, const void *g, void *out, const int32_t *cu_seqlens,
@@ -245,7 +246,7 @@ int kda_lin_chunk_fwd(const void *q, const void *k, const void *v, const void *g
     if (!in_place && overlap(initial_state, final_state, (size_t)num_seqs * H * dk * dv * sizeof(float)))
         return KDA_ERR_INVALID_ARG;
     const bool tc = use_tc(dtype, total_tokens);
-    const Windows wd = choose_windows(total_tokens, H, tc);
+    const Windows wd = choose_windows(total_tokens, H, tc ? Pass::tc : Pass::rec_fwd);
     const FwdLayout L = fwd_layout(wd, H, dk, dv);
     if (!workspace || workspace_bytes < L.total) return KDA_ERR_WORKSPACE;
     char *ws = (char *)workspace;
@@ -265,14 +266,7 @@ int kda_lin_chunk_fwd(const void *q, const void *k, const void *v, const void *g
     p.win_state = (float *)(ws + L.z);
     p.start_copy = in_place && wd.W > 1 ? (float *)(ws + L.start) : nullptr;
     p.err = (int32_t *)(ws + L.header);
-    auto pass = [&](int mode) {
-        return ok(tc ? kda::lin::launch_tc(p, mode, dk, dv, st) : kda::lin::launch_rec(p, mode, bf16, dk, dv, st));
-    };
-    if (wd.W > 1) {
-        if (!pass(kda::lin::kSum)) return KDA_ERR_CUDA;
-        if (!ok(kda::lin::launch_scan(p.win_state, p.gamma, wd.W, H, dk * dv, false, st))) return KDA_ERR_CUDA;
-    }
-    return pass(kda::lin::kFwd) ? KDA_OK : KDA_ERR_CUDA;
+    return ok(tc ? kda::lin::tc_forward(p, dk, dv, st) : kda::lin::rec_forward(p, dk, dv, st)) ? KDA_OK : KDA_ERR_CUDA;
 }
 
 int kda_lin_decode_step(const void *q, const void *k, const void *v, const void *g, void *out, float *state,
@@ -301,7 +295,7 @@ size_t kda_lin_bwd_workspace_size(int32_t total_tokens, int32_t num_seqs, int32_
     // enough for either element type
     size_t total = 0;
     for (bool tc : {false, true})
-        total = std::max(total, bwd_layout(choose_windows(total_tokens, H, tc), tc, total_tokens, num_seqs, H, Hk, dk, dv).total);
+        total = std::max(total, bwd_layout(choose_windows(total_tokens, H, tc ? Pass::tc : Pass::rec_bwd), tc, total_tokens, num_seqs, H, Hk, dk, dv).total);
     return total;
 }
 
@@ -326,7 +320,7 @@ int kda_lin_bwd(const void *q, const void *k, const void *v, const void *g, cons
     if (overlap(initial_state, d_initial_state, state_bytes) || overlap(d_final_state, d_initial_state, state_bytes))
         return KDA_ERR_INVALID_ARG;
     const bool tc = use_tc(dtype, total_tokens);
-    const Windows wd = choose_windows(total_tokens, H, tc);
+    const Windows wd = choose_windows(total_tokens, H, tc ? Pass::tc : Pass::rec_bwd);
     const BwdLayout L = bwd_layout(wd, tc, total_tokens, num_seqs, H, Hk, dk, dv);
     if (!workspace || workspace_bytes < kda_lin_bwd_workspace_size(total_tokens, num_seqs, H, Hk, dk, dv))
         return KDA_ERR_WORKSPACE;
@@ -386,14 +380,7 @@ int kda_lin_bwd(const void *q, const void *k, const void *v, const void *g, cons
     d.win_t = 1;
     d.gamma = b.gamma;
 
-    auto pass = [&](const Params &p, int mode, int da, int db) {
-        return ok(tc ? launch_tc(p, mode, da, db, st) : launch_rec(p, mode, bf16, da, db, st));
-    };
-    if (wd.W > 1 && (!pass(a, kSum, dv, dk) || !pass(b, kSumR, dv, dk) ||
-                     !ok(launch_scan(a.win_state, a.gamma, wd.W, H, dk * dv, false, st)) ||
-                     !ok(launch_scan(b.win_state, b.gamma, wd.W, H, dk * dv, true, st))))
-        return KDA_ERR_CUDA;
-    if (!pass(a, kDq, dv, dk) || !pass(b, kDk, dv, dk) || !pass(d, kDv, dk, dv)) return KDA_ERR_CUDA;
+    if (!ok(tc ? tc_backward(a, b, d, dk, dv, st) : rec_backward(a, b, d, dk, dv, st))) return KDA_ERR_CUDA;
     if (total_tokens == 0) {
         if (per_head && dg && !ok(cudaMemsetAsync(dg, 0, (size_t)H * esz, st))) return KDA_ERR_CUDA;
         return KDA_OK;
@@ -401,13 +388,12 @@ int kda_lin_bwd(const void *q, const void *k, const void *v, const void *g, cons
     const Tokens tk{cu_seqlens, num_seqs, total_tokens};
     if (rep > 1) {
         const long n4 = (long)total_tokens * Hk * dk / 4;
-        const unsigned blocks = (unsigned)std::min<long>((n4 + 255) / 256, 8L * 148);
-        for (int i = 0; i < 2; ++i) {
-            const float4 *in = (const float4 *)(ws + (i ? L.dk : L.dq));
-            void *out = i ? dk_out : dq;
-            if (bf16) head_sum_kernel<<<blocks, 256, 0, st>>>(in, (__nv_bfloat16 *)out, tk, Hk, rep, dk / 4);
-            else head_sum_kernel<<<blocks, 256, 0, st>>>(in, (float *)out, tk, Hk, rep, dk / 4);
-        }
+        const dim3 grid((unsigned)std::min<long>((n4 + 255) / 256, 4L * 148), 2);
+        const float4 *in0 = (const float4 *)(ws + L.dq), *in1 = (const float4 *)(ws + L.dk);
+        if (bf16)
+            head_sum_kernel<<<grid, 256, 0, st>>>(in0, (__nv_bfloat16 *)dq, in1, (__nv_bfloat16 *)dk_out, tk, Hk, rep, dk / 4);
+        else
+            head_sum_kernel<<<grid, 256, 0, st>>>(in0, (float *)dq, in1, (float *)dk_out, tk, Hk, rep, dk / 4);
     }
     if (per_head) {
         const int parts = (total_tokens + kSumRows - 1) / kSumRows, hb = (H + 31) / 32;

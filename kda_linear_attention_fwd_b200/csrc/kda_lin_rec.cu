@@ -9,13 +9,15 @@
 //   * the decay is one number, so it is kept outside the state: the registers
 //     hold S / e^G with G the log-decay summed since the last renormalisation;
 //     a write adds k (v e^-G)^T and a read is scaled by e^G.  The state is
-//     renormalised (one multiply per element) every 16 tokens, and earlier
-//     when G falls below -20, so e^-G stays in range and G is always a short
+//     renormalised (one multiply per element) every 16 tokens, and at every
+//     token of a group of four over which G falls below -40, so e^-G stays in range and G is always a short
 //     sum (its rounding is what limits the decay's accuracy);
 //   * a warp's 32 lanes are RG row groups x CGW column groups, each thread
 //     holding RT rows x 4 columns, so the vectors come from shared memory as
-//     broadcast 16-byte reads (17 reads for 128 paired FMAs at 128 x 128) and
-//     o needs 3 shuffles per token.
+//     broadcast 16-byte reads (17 reads for 128 paired FMAs at 128 x 128);
+//   * four tokens at a time: their partial outputs are summed over the row
+//     groups together (12 shuffles, after which a lane holds one token's four
+//     columns), so that the sums of one token do not hold up the next.
 // Tokens arrive 16 at a time by cp.async, one block ahead.
 //
 // The gradient in the same form (B_t = dL/dS_t, L = sum o . do + <dS_T, S_T>):
@@ -52,16 +54,16 @@ template <int M> struct ModeOf {
     static constexpr bool xd = M == DQ || M == DK;
 };
 
-template <typename T, int DA, int DB, int M>
-struct Stage {  // one block of 16 tokens in the input type
-    T wr[kSub][DA];
-    T val[kSub][DB];
-    T rd[ModeOf<M>::out ? kSub : 1][ModeOf<M>::out ? DA : 8];
-    T ext[ModeOf<M>::xd ? kSub : 1][ModeOf<M>::xd ? DB : 8];
+template <int DA, int DB, int M>
+struct Stage {  // one block of 16 tokens
+    float wr[kSub][DA];
+    float val[kSub][DB];
+    float rd[ModeOf<M>::out ? kSub : 1][ModeOf<M>::out ? DA : 8];
+    float ext[ModeOf<M>::xd ? kSub : 1][ModeOf<M>::xd ? DB : 8];
 };
-template <typename T, int DA, int DB, int M>
+template <int DA, int DB, int M>
 struct Smem {
-    alignas(16) Stage<T, DA, DB, M> st[2];
+    alignas(16) Stage<DA, DB, M> st[2];
     float g[2][kSub];
     float xp[kCkpt][4];  // per token and warp: partial out . ext
     float xq[kCkpt];
@@ -69,22 +71,17 @@ struct Smem {
 };
 
 KDA_DEVICE float4 ld4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
-KDA_DEVICE float4 ld4(const bf16 *p) {
-    const uint2 u = *reinterpret_cast<const uint2 *>(p);
-    const float2 a = unpack_bf16(u.x), b = unpack_bf16(u.y);
-    return make_float4(a.x, a.y, b.x, b.y);
-}
 
-template <typename T, int DA, int DB, int M>
-__global__ void __launch_bounds__(kThreads, 3) rec_kernel(const Params p) {
+template <int DA, int DB, int M>
+KDA_DEVICE void rec_body(const Params &p, unsigned char *smem_raw) {
+    using T = float;
     using MO = ModeOf<M>;
     constexpr int CGW = DB / 16;        // column groups (of 4) per warp
     constexpr int RG = 32 / CGW;        // row groups
     constexpr int RT = DA / RG;         // rows per thread
     constexpr int NQ = RT / 4;          // in quads: quad i is rows 4 (i RG + rg) .. + 3
     static_assert(NQ >= 1 && CGW * 4 * 4 == DB, "tile shape");
-    extern __shared__ __align__(16) unsigned char smem_raw[];
-    Smem<T, DA, DB, M> &sm = *reinterpret_cast<Smem<T, DA, DB, M> *>(smem_raw);
+    Smem<DA, DB, M> &sm = *reinterpret_cast<Smem<DA, DB, M> *>(smem_raw);
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rg = lane / CGW;
@@ -145,8 +142,7 @@ __global__ void __launch_bounds__(kThreads, 3) rec_kernel(const Params p) {
                 for (int c = 0; c < 4; ++c) s[i][pr][c] = f2mul(s[i][pr][c], f2);
     };
     auto load_g = [&](int t) -> float {
-        const size_t at = p.g_per_head ? (size_t)h : (size_t)t * H + h;
-        return fmaxf(ld((const T *)p.g + at), kMinG);
+        return fmaxf(((const float *)p.g)[p.g_per_head ? (size_t)h : (size_t)t * H + h], kMinG);
     };
 
     // tokens [a, b) of sequence n, whose true range is [qa, qb)
@@ -156,7 +152,7 @@ __global__ void __launch_bounds__(kThreads, 3) rec_kernel(const Params p) {
         const int nsub = (len + kSub - 1) / kSub;
         auto stage = [&](int sb, int buf) {
             const int base = a + sb * kSub, rows = min(kSub, b - base);
-            Stage<T, DA, DB, M> &S = sm.st[buf];
+            Stage<DA, DB, M> &S = sm.st[buf];
             auto copy = [&](T *dst, const T *src, int D, int Hx, int hx) {
                 const int per = D * (int)sizeof(T) / 16;
                 for (int x = tid; x < rows * per; x += kThreads) {
@@ -169,12 +165,9 @@ __global__ void __launch_bounds__(kThreads, 3) rec_kernel(const Params p) {
             copy(&S.val[0][0], val, DB, Hv, hv);
             if constexpr (MO::out) copy(&S.rd[0][0], rd, DA, Hr, hr);
             if constexpr (MO::xd) copy(&S.ext[0][0], ext, DB, He, he);
-            if (tid < rows) {
+            if (tid < kSub) {
                 const int t = base + tid;
-                if (MO::rev)
-                    sm.g[buf][tid] = t + 1 < qb ? load_g(t + 1) : 0.f;
-                else
-                    sm.g[buf][tid] = load_g(t);
+                sm.g[buf][tid] = tid >= rows ? 0.f : !MO::rev ? load_g(t) : t + 1 < qb ? load_g(t + 1) : 0.f;
             }
             cp_async_commit();
         };
@@ -188,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 3) rec_kernel(const Params p) {
                 cp_async_wait<0>();
             }
             __syncthreads();
-            const Stage<T, DA, DB, M> &S = sm.st[buf];
+            const Stage<DA, DB, M> &S = sm.st[buf];
             const int base = a + sb * kSub, rows = min(kSub, b - base);
             const int chunk = sb / (kCkpt / kSub);
             const int in_chunk = (sb % (kCkpt / kSub)) * kSub;
@@ -213,63 +206,107 @@ __global__ void __launch_bounds__(kThreads, 3) rec_kernel(const Params p) {
                 }
             }
             float G = 0.f;
+            const bool hi = lane & 16, mid = lane & 8;
+            const int mine = 2 * hi + mid;  // the token of a group whose output this lane ends up with
 #pragma unroll 1
-            for (int jj = 0; jj < rows; ++jj) {
-                const int j = MO::rev ? rows - 1 - jj : jj;
-                G += sm.g[buf][j];
-                if (G < -20.f) {  // the same branch in every thread
-                    const float f = expf(G);
-                    scale_state(f);
-                    gamma *= f;
-                    G = 0.f;
-                }
-                const float wf = __expf(-G) * p.wr_scale;
-                const float4 v4 = ld4(&S.val[j][col0]);
-                const float vs[4] = {v4.x * wf, v4.y * wf, v4.z * wf, v4.w * wf};
-                float2 o[4];
+            for (int j0 = MO::rev ? (rows - 1) & ~3 : 0; j0 >= 0 && j0 < rows; j0 += MO::rev ? -4 : 4) {
+                // in the order of the pass: token e of the group is j0 + e, or j0 + 3 - e
+                float gs[4];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) o[c] = make_float2(0.f, 0.f);
+                for (int e = 0; e < 4; ++e) gs[e] = sm.g[buf][MO::rev ? j0 + 3 - e : j0 + e];
+                const bool slow = G + ((gs[0] + gs[1]) + (gs[2] + gs[3])) < -40.f;  // the same in every thread
+#pragma unroll 1
+                for (int only = slow ? 0 : 3; only < 4; ++only) {  // slow: one token per round, renormalised at each
+                    float wf[4], rf[4];
+                    if (slow) {
+                        const float f = expf(G + (only == 0 ? gs[0] : only == 1 ? gs[1] : only == 2 ? gs[2] : gs[3]));
+                        scale_state(f);
+                        gamma *= f;
+                        G = 0.f;
+                    }
 #pragma unroll
-                for (int i = 0; i < NQ; ++i) {
-                    const float4 k4 = ld4(&S.wr[j][row_of(i, 0)]);
-                    const float2 k2[2] = {make_float2(k4.x, k4.y), make_float2(k4.z, k4.w)};
+                    for (int e = 0; e < 4; ++e) {
+                        const int j = MO::rev ? j0 + 3 - e : j0 + e;
+                        const bool on = j < rows && (!slow || e == only);
+                        if (!slow) G += gs[e];
+                        wf[e] = on ? (slow ? 1.f : __expf(-G)) * p.wr_scale : 0.f;
+                        rf[e] = (slow ? 1.f : __expf(G)) * p.rd_scale;
+                    }
+                    float o[4][4];
 #pragma unroll
-                    for (int pr = 0; pr < 2; ++pr)
+                    for (int e = 0; e < 4; ++e) {
+                        const int j = MO::rev ? j0 + 3 - e : j0 + e;
+                        const bool on = j < rows;  // (rows behind the end are not staged)
+                        const float4 v4 = on ? ld4(&S.val[j][col0]) : make_float4(0.f, 0.f, 0.f, 0.f);
+                        const float vs[4] = {v4.x * wf[e], v4.y * wf[e], v4.z * wf[e], v4.w * wf[e]};
+                        float2 acc[4];
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) s[i][pr][c] = f2fma(k2[pr], make_float2(vs[c], vs[c]), s[i][pr][c]);
+                        for (int c = 0; c < 4; ++c) acc[c] = make_float2(0.f, 0.f);
+                        if (on) {
+#pragma unroll
+                            for (int i = 0; i < NQ; ++i) {
+                                const float4 k4 = ld4(&S.wr[j][row_of(i, 0)]);
+                                const float2 k2[2] = {make_float2(k4.x, k4.y), make_float2(k4.z, k4.w)};
+#pragma unroll
+                                for (int pr = 0; pr < 2; ++pr)
+#pragma unroll
+                                    for (int c = 0; c < 4; ++c)
+                                        s[i][pr][c] = f2fma(k2[pr], make_float2(vs[c], vs[c]), s[i][pr][c]);
+                                if constexpr (MO::out) {
+                                    const float4 q4 = ld4(&S.rd[j][row_of(i, 0)]);
+                                    const float2 q2[2] = {make_float2(q4.x, q4.y), make_float2(q4.z, q4.w)};
+#pragma unroll
+                                    for (int pr = 0; pr < 2; ++pr)
+#pragma unroll
+                                        for (int c = 0; c < 4; ++c) acc[c] = f2fma(q2[pr], s[i][pr][c], acc[c]);
+                                }
+                            }
+                        }
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) o[e][c] = acc[c].x + acc[c].y;
+                    }
                     if constexpr (MO::out) {
-                        const float4 q4 = ld4(&S.rd[j][row_of(i, 0)]);
-                        const float2 q2[2] = {make_float2(q4.x, q4.y), make_float2(q4.z, q4.w)};
+                        // sums over the row groups: tokens 2 hi, 2 hi + 1, then the one of them with mid
+                        float y[2][4], z[4];
 #pragma unroll
-                        for (int pr = 0; pr < 2; ++pr)
+                        for (int e = 0; e < 2; ++e)
 #pragma unroll
-                            for (int c = 0; c < 4; ++c) o[c] = f2fma(q2[pr], s[i][pr][c], o[c]);
-                    }
-                }
-                if constexpr (MO::out) {
-                    // sum over the row groups, one column left per lane
-                    float x[4];
+                            for (int c = 0; c < 4; ++c)
+                                y[e][c] = (hi ? o[2 + e][c] : o[e][c]) +
+                                          __shfl_xor_sync(0xffffffffu, hi ? o[e][c] : o[2 + e][c], 16);
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) x[c] = o[c].x + o[c].y;
-                    const bool hi = lane & 16, mid = lane & 8;
-                    float y0 = (hi ? x[2] : x[0]) + __shfl_xor_sync(0xffffffffu, hi ? x[0] : x[2], 16);
-                    float y1 = (hi ? x[3] : x[1]) + __shfl_xor_sync(0xffffffffu, hi ? x[1] : x[3], 16);
-                    float z = (mid ? y1 : y0) + __shfl_xor_sync(0xffffffffu, mid ? y0 : y1, 8);
-                    bool keep = true;
-                    if constexpr (RG == 8) {
-                        z += __shfl_xor_sync(0xffffffffu, z, 4);
-                        keep = !(lane & 4);
-                    }
-                    z *= __expf(G) * p.rd_scale;
-                    const int col = col0 + (hi ? 2 : 0) + (mid ? 1 : 0);
-                    const size_t at = ((size_t)(base + j) * H + h) * DB + col;
-                    if (keep) {
-                        if (p.out_f32) ((float *)p.out)[at] = z;
-                        else st((T *)p.out + at, z);
-                    }
-                    if constexpr (MO::xd) {
-                        const float x1 = warp_sum(keep ? z * ld(&S.ext[j][col]) : 0.f);
-                        if (lane == 0) sm.xp[in_chunk + j][warp] = x1;
+                        for (int c = 0; c < 4; ++c)
+                            z[c] = (mid ? y[1][c] : y[0][c]) + __shfl_xor_sync(0xffffffffu, mid ? y[0][c] : y[1][c], 8);
+                        const float r = hi ? (mid ? rf[3] : rf[2]) : (mid ? rf[1] : rf[0]);
+                        const int j = MO::rev ? j0 + 3 - mine : j0 + mine;
+                        const bool on = j < rows && (!slow || mine == only);
+                        const size_t at = ((size_t)(base + j) * H + h) * DB + col0;
+                        float x1 = 0.f;
+                        if constexpr (RG == 8) {
+                            const bool up = lane & 4;
+                            const float a0 = ((up ? z[2] : z[0]) + __shfl_xor_sync(0xffffffffu, up ? z[0] : z[2], 4)) * r;
+                            const float a1 = ((up ? z[3] : z[1]) + __shfl_xor_sync(0xffffffffu, up ? z[1] : z[3], 4)) * r;
+                            const int c = up ? 2 : 0;
+                            if (on) {
+                                *reinterpret_cast<float2 *>((float *)p.out + at + c) = make_float2(a0, a1);
+                                if constexpr (MO::xd) {
+                                    const float2 e2 = *reinterpret_cast<const float2 *>(&S.ext[j][col0 + c]);
+                                    x1 = a0 * e2.x + a1 * e2.y;
+                                }
+                            }
+                        } else if (on) {
+                            const float4 a = make_float4(z[0] * r, z[1] * r, z[2] * r, z[3] * r);
+                            *reinterpret_cast<float4 *>((float *)p.out + at) = a;
+                            if constexpr (MO::xd) {
+                                const float4 e4 = ld4(&S.ext[j][col0]);
+                                x1 = (a.x * e4.x + a.y * e4.y) + (a.z * e4.z + a.w * e4.w);
+                            }
+                        }
+                        if constexpr (MO::xd) {
+#pragma unroll
+                            for (int m = 4; m > 0; m >>= 1) x1 += __shfl_xor_sync(0xffffffffu, x1, m);
+                            if (on && (lane & 7) == 0) sm.xp[in_chunk + j][warp] = x1;
+                        }
                     }
                 }
             }
@@ -310,8 +347,7 @@ __global__ void __launch_bounds__(kThreads, 3) rec_kernel(const Params p) {
                         float dg = F + (e ? tot - d[0] : tot);
                         if (p.zero_first_dg && t == qa) dg = 0.f;
                         if (j < chunk_len) {
-                            if (p.g_per_head) ((float *)p.dg)[(size_t)t * H + h] = dg;
-                            else st((T *)p.dg + (size_t)t * H + h, dg);
+                            ((float *)p.dg)[(size_t)t * H + h] = dg;
                         }
                     }
                 }
@@ -399,30 +435,52 @@ __global__ void __launch_bounds__(kThreads, 3) rec_kernel(const Params p) {
     }
 }
 
+// One pass per CTA layer, or two at once (independent ones, blockIdx.z).
+template <int DA, int DB, int M>
+__global__ void __launch_bounds__(kThreads, 2) rec_kernel(const __grid_constant__ Params p) {
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    rec_body<DA, DB, M>(p, smem_raw);
+}
+template <int DA, int DB, int M, int DA2, int DB2, int M2>
+__global__ void __launch_bounds__(kThreads, 2) rec_pair_kernel(const __grid_constant__ Params p, const __grid_constant__ Params p2) {
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    if (blockIdx.z == 0) rec_body<DA, DB, M>(p, smem_raw);
+    else rec_body<DA2, DB2, M2>(p2, smem_raw);
+}
+
 // The states entering the windows, in place of the windows' Z:
 // S_in(w + 1) = gamma_w S_in(w) + Z_w (reversed: S_in(w - 1)).  One thread per
-// four state elements, the next kAhead windows' Z in flight.
+// four state elements; the next kAhead windows' Z are requested before these
+// are folded.
 constexpr int kAhead = 8;
-__global__ void __launch_bounds__(128) scan_kernel(float4 *z, const float *gamma, int W, int H, int quads, int rev) {
+struct ScanSide {
+    float4 *z;
+    const float *gamma;
+    int rev;
+};
+__global__ void __launch_bounds__(128) scan_kernel(const ScanSide a, const ScanSide b, int W, int H, int quads) {
+    const ScanSide sd = blockIdx.z == 0 ? a : b;
     const int e = blockIdx.x * 128 + threadIdx.x, h = blockIdx.y;
     if (e >= quads) return;
     float4 carry = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int w0 = 0; w0 < W; w0 += kAhead) {
-        float4 zz[kAhead];
-        float gm[kAhead];
+    float4 zz[kAhead], nz[kAhead];
+    float gm[kAhead], ng[kAhead];
+    auto window = [&](int w) { return (size_t)(sd.rev ? W - 1 - w : w) * H + h; };
+    auto load = [&](int w0, float4(&z)[kAhead], float(&g)[kAhead]) {
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
+        for (int i = 0; i < kAhead; ++i)
             if (w0 + i < W) {
-                const int w = rev ? W - 1 - (w0 + i) : w0 + i;
-                gm[i] = gamma[(size_t)w * H + h];
-                zz[i] = z[((size_t)w * H + h) * quads + e];
+                g[i] = sd.gamma[window(w0 + i)];
+                z[i] = sd.z[window(w0 + i) * quads + e];
             }
-        }
+    };
+    load(0, zz, gm);
+    for (int w0 = 0; w0 < W; w0 += kAhead) {
+        load(w0 + kAhead, nz, ng);
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
             if (w0 + i < W) {
-                const int w = rev ? W - 1 - (w0 + i) : w0 + i;
-                z[((size_t)w * H + h) * quads + e] = carry;
+                sd.z[window(w0 + i) * quads + e] = carry;
                 if (gm[i] < 0.f) {
                     carry = make_float4(0.f, 0.f, 0.f, 0.f);
                 } else {
@@ -432,44 +490,68 @@ __global__ void __launch_bounds__(128) scan_kernel(float4 *z, const float *gamma
                     carry.w = fmaf(gm[i], carry.w, zz[i].w);
                 }
             }
+            zz[i] = nz[i];
+            gm[i] = ng[i];
         }
     }
 }
 
-cudaError_t launch_scan(float *z, const float *gamma, int W, int H, int elems, bool rev, cudaStream_t st) {
+// The forward's states, and with `rev` also the reversed pass's.
+cudaError_t launch_scan(const Params &p, const Params *rev, int elems, cudaStream_t st) {
     const int quads = elems / 4;
-    scan_kernel<<<dim3((quads + 127) / 128, H), 128, 0, st>>>((float4 *)z, gamma, W, H, quads, rev);
+    const ScanSide a{(float4 *)p.win_state, p.gamma, 0};
+    const ScanSide b = rev ? ScanSide{(float4 *)rev->win_state, rev->gamma, 1} : a;
+    scan_kernel<<<dim3((quads + 127) / 128, p.H, rev ? 2 : 1), 128, 0, st>>>(a, b, p.W, p.H, quads);
     return cudaGetLastError();
 }
 
-template <typename T, int DA, int DB, int M>
-static cudaError_t launch_rec_t(const Params &p, cudaStream_t st) {
-    constexpr int bytes = (int)sizeof(Smem<T, DA, DB, M>);
+template <int DA, int DB, int M>
+static cudaError_t launch_one(const Params &p, cudaStream_t st) {
+    constexpr int bytes = (int)sizeof(Smem<DA, DB, M>);
     static std::atomic<uint64_t> done;
-    cudaError_t e = allow_smem(done, (const void *)rec_kernel<T, DA, DB, M>, bytes);
+    cudaError_t e = allow_smem(done, (const void *)rec_kernel<DA, DB, M>, bytes);
     if (e != cudaSuccess) return e;
-    rec_kernel<T, DA, DB, M><<<dim3(p.H, p.W), kThreads, bytes, st>>>(p);
+    rec_kernel<DA, DB, M><<<dim3(p.H, p.W), kThreads, bytes, st>>>(p);
     return cudaGetLastError();
 }
-template <typename T, int M>
-static cudaError_t launch_rec_d(const Params &p, int da, int db, cudaStream_t st) {
-    if (da == 128) return db == 128 ? launch_rec_t<T, 128, 128, M>(p, st) : launch_rec_t<T, 128, 64, M>(p, st);
-    return db == 128 ? launch_rec_t<T, 64, 128, M>(p, st) : launch_rec_t<T, 64, 64, M>(p, st);
+template <int DA, int DB, int M, int DA2, int DB2, int M2>
+static cudaError_t launch_two(const Params &p, const Params &p2, cudaStream_t st) {
+    constexpr int b1 = (int)sizeof(Smem<DA, DB, M>), b2 = (int)sizeof(Smem<DA2, DB2, M2>), bytes = b1 > b2 ? b1 : b2;
+    static std::atomic<uint64_t> done;
+    cudaError_t e = allow_smem(done, (const void *)rec_pair_kernel<DA, DB, M, DA2, DB2, M2>, bytes);
+    if (e != cudaSuccess) return e;
+    rec_pair_kernel<DA, DB, M, DA2, DB2, M2><<<dim3(p.H, p.W, 2), kThreads, bytes, st>>>(p, p2);
+    return cudaGetLastError();
 }
-template <int M>
-static cudaError_t launch_rec_m(const Params &p, bool is_bf16, int da, int db, cudaStream_t st) {
-    return is_bf16 ? launch_rec_d<bf16, M>(p, da, db, st) : launch_rec_d<float, M>(p, da, db, st);
-}
-// mode: 0 forward, 1 summary, 2 reversed summary, 3 dq, 4 dk (and dg), 5 dv (and dS0)
-cudaError_t launch_rec(const Params &p, int mode, bool is_bf16, int da, int db, cudaStream_t st) {
-    switch (mode) {
-        case FWD: return launch_rec_m<FWD>(p, is_bf16, da, db, st);
-        case SUM: return launch_rec_m<SUM>(p, is_bf16, da, db, st);
-        case SUMR: return launch_rec_m<SUMR>(p, is_bf16, da, db, st);
-        case DQ: return launch_rec_m<DQ>(p, is_bf16, da, db, st);
-        case DK: return launch_rec_m<DK>(p, is_bf16, da, db, st);
-        default: return launch_rec_m<DV>(p, is_bf16, da, db, st);
+
+template <int DK_, int DV_>
+static cudaError_t fwd_t(const Params &p, cudaStream_t st) {
+    if (p.W > 1) {
+        cudaError_t e = launch_one<DK_, DV_, SUM>(p, st);
+        if (e == cudaSuccess) e = launch_scan(p, nullptr, DK_ * DV_, st);
+        if (e != cudaSuccess) return e;
     }
+    return launch_one<DK_, DV_, FWD>(p, st);
+}
+template <int DK_, int DV_>
+static cudaError_t bwd_t(const Params &a, const Params &b, const Params &d, cudaStream_t st) {
+    if (a.W > 1) {
+        cudaError_t e = launch_two<DV_, DK_, SUM, DV_, DK_, SUMR>(a, b, st);
+        if (e == cudaSuccess) e = launch_scan(a, &b, DK_ * DV_, st);
+        if (e != cudaSuccess) return e;
+    }
+    cudaError_t e = launch_two<DV_, DK_, DQ, DK_, DV_, DV>(a, d, st);
+    return e == cudaSuccess ? launch_one<DV_, DK_, DK>(b, st) : e;
+}
+
+// fp32: the forward (summary, scan, output), and the gradient's passes (dq, dk and dg, dv and dS0).
+cudaError_t rec_forward(const Params &p, int dk, int dv, cudaStream_t st) {
+    if (dk == 128) return dv == 128 ? fwd_t<128, 128>(p, st) : fwd_t<128, 64>(p, st);
+    return dv == 128 ? fwd_t<64, 128>(p, st) : fwd_t<64, 64>(p, st);
+}
+cudaError_t rec_backward(const Params &q, const Params &k, const Params &v, int dk, int dv, cudaStream_t st) {
+    if (dk == 128) return dv == 128 ? bwd_t<128, 128>(q, k, v, st) : bwd_t<128, 64>(q, k, v, st);
+    return dv == 128 ? bwd_t<64, 128>(q, k, v, st) : bwd_t<64, 64>(q, k, v, st);
 }
 
 }  // namespace lin

@@ -61,6 +61,9 @@
 
 namespace kda {
 namespace lin {
+
+cudaError_t launch_scan(const Params &p, const Params *rev, int elems, cudaStream_t st);
+
 namespace tc {
 
 using namespace sm100;
@@ -973,24 +976,39 @@ cudaError_t launch_t(const Params &p, cudaStream_t st) {
     tc_kernel<DA, DB, M><<<dim3(p.H, p.W), kThreads, bytes, st>>>(p, maps);
     return cudaGetLastError();
 }
-template <int M>
-cudaError_t launch_m(const Params &p, int da, int db, cudaStream_t st) {
-    if (da == 128) return db == 128 ? launch_t<128, 128, M>(p, st) : launch_t<128, 64, M>(p, st);
-    return db == 128 ? launch_t<64, 128, M>(p, st) : launch_t<64, 64, M>(p, st);
+template <int DK_, int DV_>
+cudaError_t fwd_t(const Params &p, cudaStream_t st) {
+    if (p.W > 1) {
+        cudaError_t e = launch_t<DK_, DV_, SUM>(p, st);
+        if (e == cudaSuccess) e = launch_scan(p, nullptr, DK_ * DV_, st);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_t<DK_, DV_, FWD>(p, st);
+}
+template <int DK_, int DV_>
+cudaError_t bwd_t(const Params &a, const Params &b, const Params &d, cudaStream_t st) {
+    cudaError_t e = cudaSuccess;
+    if (a.W > 1) {
+        e = launch_t<DV_, DK_, SUM>(a, st);
+        if (e == cudaSuccess) e = launch_t<DV_, DK_, SUMR>(b, st);
+        if (e == cudaSuccess) e = launch_scan(a, &b, DK_ * DV_, st);
+    }
+    if (e == cudaSuccess) e = launch_t<DV_, DK_, DQ>(a, st);
+    if (e == cudaSuccess) e = launch_t<DV_, DK_, DK>(b, st);
+    if (e == cudaSuccess) e = launch_t<DK_, DV_, DV>(d, st);
+    return e;
 }
 
 }  // namespace tc
 
-// The bf16 passes (same modes as launch_rec); T > 0.
-cudaError_t launch_tc(const Params &p, int mode, int da, int db, cudaStream_t st) {
-    switch (mode) {
-        case tc::FWD: return tc::launch_m<tc::FWD>(p, da, db, st);
-        case tc::SUM: return tc::launch_m<tc::SUM>(p, da, db, st);
-        case tc::SUMR: return tc::launch_m<tc::SUMR>(p, da, db, st);
-        case tc::DQ: return tc::launch_m<tc::DQ>(p, da, db, st);
-        case tc::DK: return tc::launch_m<tc::DK>(p, da, db, st);
-        default: return tc::launch_m<tc::DV>(p, da, db, st);
-    }
+// bf16 (T > 0): the same as rec_forward and rec_backward.
+cudaError_t tc_forward(const Params &p, int dk, int dv, cudaStream_t st) {
+    if (dk == 128) return dv == 128 ? tc::fwd_t<128, 128>(p, st) : tc::fwd_t<128, 64>(p, st);
+    return dv == 128 ? tc::fwd_t<64, 128>(p, st) : tc::fwd_t<64, 64>(p, st);
+}
+cudaError_t tc_backward(const Params &q, const Params &k, const Params &v, int dk, int dv, cudaStream_t st) {
+    if (dk == 128) return dv == 128 ? tc::bwd_t<128, 128>(q, k, v, st) : tc::bwd_t<128, 64>(q, k, v, st);
+    return dv == 128 ? tc::bwd_t<64, 128>(q, k, v, st) : tc::bwd_t<64, 64>(q, k, v, st);
 }
 
 }  // namespace lin
