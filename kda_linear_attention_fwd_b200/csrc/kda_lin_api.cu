@@ -133,15 +133,15 @@ struct Windows {
     int win, W;
 };
 // As many windows as fill the SMs once: one CTA per SM and whole 128-token
-// chunks on the tensor cores, two CTAs per SM token by token, there in whole
+// chunks on the tensor cores, two or three CTAs per SM token by token, there in whole
 // 64-token chunks for the gradient and 32 tokens otherwise.  A call with more
 // than one window also runs the summary pass (about 0.6 of the time of the
 // main one) and the scan (about as long as 25 tokens), so what is shorter
 // stays in one.
 enum class Pass { tc, rec_fwd, rec_bwd };
-Windows choose_windows(int T, int H, Pass pass) {
+Windows choose_windows(int T, int H, int dk, int dv, Pass pass) {
     const long step = pass == Pass::tc ? 128 : pass == Pass::rec_bwd ? 64 : 32;
-    const long target = std::max(1L, (pass == Pass::tc ? 1L : 2L) * sm_count() / H);
+    const long target = std::max(1L, (pass == Pass::tc ? 1L : dk * dv > 128 * 64 ? 2L : 3L) * sm_count() / H);
     long win = std::max(step, ((T + target - 1) / target + step - 1) / step * step);
     if (pass != Pass::tc && 1.6 * win + 25 >= T) win = std::max(step, (T + step - 1) / step * step);
     return {(int)win, std::max(1, (int)((T + win - 1) / win))};
@@ -226,7 +226,7 @@ extern "C" {
 size_t kda_lin_chunk_fwd_workspace_size(int32_t total_tokens, int32_t num_seqs, int32_t H, int32_t Hk, int32_t dk,
                                         int32_t dv, kda_dtype dtype) {
     if (check_sizes(num_seqs, total_tokens, H, Hk, dk, dv, dtype, 0) != KDA_OK) return 0;
-    return fwd_layout(choose_windows(total_tokens, H, use_tc(dtype, total_tokens) ? Pass::tc : Pass::rec_fwd), H, dk, dv).total;
+    return fwd_layout(choose_windows(total_tokens, H, dk, dv, use_tc(dtype, total_tokens) ? Pass::tc : Pass::rec_fwd), H, dk, dv).total;
 }
 
 int kda_lin_chunk_fwd(const void *q, const void *k, const void *v, const void *g, void *out, const int32_t *cu_seqlens,
@@ -246,7 +246,7 @@ int kda_lin_chunk_fwd(const void *q, const void *k, const void *v, const void *g
     if (!in_place && overlap(initial_state, final_state, (size_t)num_seqs * H * dk * dv * sizeof(float)))
         return KDA_ERR_INVALID_ARG;
     const bool tc = use_tc(dtype, total_tokens);
-    const Windows wd = choose_windows(total_tokens, H, tc ? Pass::tc : Pass::rec_fwd);
+    const Windows wd = choose_windows(total_tokens, H, dk, dv, tc ? Pass::tc : Pass::rec_fwd);
     const FwdLayout L = fwd_layout(wd, H, dk, dv);
     if (!workspace || workspace_bytes < L.total) return KDA_ERR_WORKSPACE;
     char *ws = (char *)workspace;
@@ -295,7 +295,7 @@ size_t kda_lin_bwd_workspace_size(int32_t total_tokens, int32_t num_seqs, int32_
     // enough for either element type
     size_t total = 0;
     for (bool tc : {false, true})
-        total = std::max(total, bwd_layout(choose_windows(total_tokens, H, tc ? Pass::tc : Pass::rec_bwd), tc, total_tokens, num_seqs, H, Hk, dk, dv).total);
+        total = std::max(total, bwd_layout(choose_windows(total_tokens, H, dk, dv, tc ? Pass::tc : Pass::rec_bwd), tc, total_tokens, num_seqs, H, Hk, dk, dv).total);
     return total;
 }
 
@@ -320,7 +320,7 @@ int kda_lin_bwd(const void *q, const void *k, const void *v, const void *g, cons
     if (overlap(initial_state, d_initial_state, state_bytes) || overlap(d_final_state, d_initial_state, state_bytes))
         return KDA_ERR_INVALID_ARG;
     const bool tc = use_tc(dtype, total_tokens);
-    const Windows wd = choose_windows(total_tokens, H, tc ? Pass::tc : Pass::rec_bwd);
+    const Windows wd = choose_windows(total_tokens, H, dk, dv, tc ? Pass::tc : Pass::rec_bwd);
     const BwdLayout L = bwd_layout(wd, tc, total_tokens, num_seqs, H, Hk, dk, dv);
     if (!workspace || workspace_bytes < kda_lin_bwd_workspace_size(total_tokens, num_seqs, H, Hk, dk, dv))
         return KDA_ERR_WORKSPACE;

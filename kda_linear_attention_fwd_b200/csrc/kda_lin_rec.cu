@@ -5,7 +5,8 @@
 // token, so fp32 inputs, which the tensor cores could only take split into
 // several products, run it directly: the whole state of one head sits in the
 // registers of one CTA of 128 threads and every product is a plain fp32 FMA
-// (pairs, fma.rn.f32x2).  Two things keep it at two FMAs:
+// (the paired instruction has the same rate, and its operands would have to be
+// put together first).  Three things keep it near two FMAs:
 //   * the decay is one number, so it is kept outside the state: the registers
 //     hold S / e^G with G the log-decay summed since the last renormalisation;
 //     a write adds k (v e^-G)^T and a read is scaled by e^G.  The state is
@@ -14,7 +15,7 @@
 //     sum (its rounding is what limits the decay's accuracy);
 //   * a warp's 32 lanes are RG row groups x CGW column groups, each thread
 //     holding RT rows x 4 columns, so the vectors come from shared memory as
-//     broadcast 16-byte reads (17 reads for 128 paired FMAs at 128 x 128);
+//     broadcast 16-byte reads (17 reads for 256 FMAs at 128 x 128);
 //   * four tokens at a time: their partial outputs are summed over the row
 //     groups together (12 shuffles, after which a lane holds one token's four
 //     columns), so that the sums of one token do not hold up the next.
@@ -61,10 +62,16 @@ struct Stage {  // one block of 16 tokens
     float rd[ModeOf<M>::out ? kSub : 1][ModeOf<M>::out ? DA : 8];
     float ext[ModeOf<M>::xd ? kSub : 1][ModeOf<M>::xd ? DB : 8];
 };
+// CTAs per SM (by registers: the state takes DA DB / 128 of each thread's) and
+// blocks in flight: what their shared memory has room for, up to four.
+template <int DA, int DB> constexpr int kCtas = DA * DB > 128 * 64 ? 2 : 3;
 template <int DA, int DB, int M>
 struct Smem {
-    alignas(16) Stage<DA, DB, M> st[2];
-    float g[2][kSub];
+    static constexpr int room = 216 * 1024 / kCtas<DA, DB> / (int)sizeof(Stage<DA, DB, M>);
+    static constexpr int stages = room < 4 ? room : 4;
+    static_assert(stages >= 2, "blocks in flight");
+    alignas(16) Stage<DA, DB, M> st[stages];
+    float g[stages][kSub];
     float xp[kCkpt][4];  // per token and warp: partial out . ext
     float xq[kCkpt];
     float fdot[4];
@@ -95,7 +102,7 @@ KDA_DEVICE void rec_body(const Params &p, unsigned char *smem_raw) {
     const int he = MO::xd ? h / p.ext_div : 0, He = MO::xd ? H / p.ext_div : 1;
     const T *rd = (const T *)p.rd, *wr = (const T *)p.wr, *val = (const T *)p.val, *ext = (const T *)p.ext;
 
-    float2 s[NQ][2][4];  // quad, row pair, column: S / e^G
+    float s[NQ][4][4];  // quad, row, column: S / e^G
 
     auto row_of = [&](int i, int r) { return 4 * (i * RG + rg) + r; };
     // state element access of a [DA][DB] matrix, or its transpose
@@ -113,7 +120,7 @@ KDA_DEVICE void rec_body(const Params &p, unsigned char *smem_raw) {
                     for (int c = 0; c < 4; ++c) x[c] = base[(size_t)(col0 + c) * DA + row_of(i, r)];
                 }
 #pragma unroll
-                for (int c = 0; c < 4; ++c) (r & 1 ? s[i][r >> 1][c].y : s[i][r >> 1][c].x) = x[c];
+                for (int c = 0; c < 4; ++c) s[i][r][c] = x[c];
             }
     };
     auto store_state = [&](float *base, bool transposed, float f) {
@@ -123,7 +130,7 @@ KDA_DEVICE void rec_body(const Params &p, unsigned char *smem_raw) {
             for (int r = 0; r < 4; ++r) {
                 float x[4];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) x[c] = f * (r & 1 ? s[i][r >> 1][c].y : s[i][r >> 1][c].x);
+                for (int c = 0; c < 4; ++c) x[c] = f * s[i][r][c];
                 if (!transposed) {
                     *reinterpret_cast<float4 *>(base + (size_t)row_of(i, r) * DB + col0) = make_float4(x[0], x[1], x[2], x[3]);
                 } else {
@@ -133,13 +140,12 @@ KDA_DEVICE void rec_body(const Params &p, unsigned char *smem_raw) {
             }
     };
     auto scale_state = [&](float f) {
-        const float2 f2 = make_float2(f, f);
 #pragma unroll
         for (int i = 0; i < NQ; ++i)
 #pragma unroll
-            for (int pr = 0; pr < 2; ++pr)
+            for (int r = 0; r < 4; ++r)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) s[i][pr][c] = f2mul(s[i][pr][c], f2);
+                for (int c = 0; c < 4; ++c) s[i][r][c] *= f;
     };
     auto load_g = [&](int t) -> float {
         return fmaxf(((const float *)p.g)[p.g_per_head ? (size_t)h : (size_t)t * H + h], kMinG);
@@ -165,21 +171,27 @@ KDA_DEVICE void rec_body(const Params &p, unsigned char *smem_raw) {
             copy(&S.val[0][0], val, DB, Hv, hv);
             if constexpr (MO::out) copy(&S.rd[0][0], rd, DA, Hr, hr);
             if constexpr (MO::xd) copy(&S.ext[0][0], ext, DB, He, he);
-            if (tid < kSub) {
-                const int t = base + tid;
-                sm.g[buf][tid] = tid >= rows ? 0.f : !MO::rev ? load_g(t) : t + 1 < qb ? load_g(t + 1) : 0.f;
+            if (tid < kSub) {  // (clamped when used)
+                const int t = base + tid + (MO::rev ? 1 : 0);
+                const bool on = tid < rows && (!MO::rev || t < qb);
+                const float *src = (const float *)p.g + (!on ? 0 : p.g_per_head ? (size_t)h : (size_t)t * H + h);
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(smem_u32(&sm.g[buf][tid])), "l"(src),
+                             "r"(on ? 4 : 0)
+                             : "memory");
             }
             cp_async_commit();
         };
-        if (nsub > 0) stage(MO::rev ? nsub - 1 : 0, 0);
+        constexpr int NS = Smem<DA, DB, M>::stages;
+        // a group per block, empty behind the last, so that the wait counts alike
+        auto ahead = [&](int it) {
+            if (it < nsub) stage(MO::rev ? nsub - 1 - it : it, it % NS);
+            else cp_async_commit();
+        };
+        for (int it = 0; it < NS - 1; ++it) ahead(it);
         for (int it = 0; it < nsub; ++it) {
-            const int sb = MO::rev ? nsub - 1 - it : it, buf = it & 1;
-            if (it + 1 < nsub) {
-                stage(MO::rev ? sb - 1 : sb + 1, buf ^ 1);
-                cp_async_wait<1>();
-            } else {
-                cp_async_wait<0>();
-            }
+            const int sb = MO::rev ? nsub - 1 - it : it, buf = it % NS;
+            ahead(it + NS - 1);
+            cp_async_wait<NS - 1>();
             __syncthreads();
             const Stage<DA, DB, M> &S = sm.st[buf];
             const int base = a + sb * kSub, rows = min(kSub, b - base);
@@ -198,9 +210,9 @@ KDA_DEVICE void rec_body(const Params &p, unsigned char *smem_raw) {
                             const float4 v4 = *reinterpret_cast<const float4 *>(ck + (size_t)row_of(i, r) * DB + col0);
                             const float x[4] = {v4.x, v4.y, v4.z, v4.w};
 #pragma unroll
-                            for (int c = 0; c < 4; ++c) d += x[c] * (r & 1 ? s[i][r >> 1][c].y : s[i][r >> 1][c].x);
+                            for (int c = 0; c < 4; ++c) d = fmaf(x[c], s[i][r][c], d);
                         }
-                    d = warp_sum(d) * __expf(sm.g[buf][rows - 1]);
+                    d = warp_sum(d) * __expf(fmaxf(sm.g[buf][rows - 1], kMinG));
                     if (lane == 0) sm.fdot[warp] = d;
                     if (tid < chunk_len) sm.xq[tid] = p.xdot[(size_t)(a + chunk * kCkpt + tid) * H + h];
                 }
@@ -213,7 +225,7 @@ KDA_DEVICE void rec_body(const Params &p, unsigned char *smem_raw) {
                 // in the order of the pass: token e of the group is j0 + e, or j0 + 3 - e
                 float gs[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) gs[e] = sm.g[buf][MO::rev ? j0 + 3 - e : j0 + e];
+                for (int e = 0; e < 4; ++e) gs[e] = fmaxf(sm.g[buf][MO::rev ? j0 + 3 - e : j0 + e], kMinG);
                 const bool slow = G + ((gs[0] + gs[1]) + (gs[2] + gs[3])) < -40.f;  // the same in every thread
 #pragma unroll 1
                 for (int only = slow ? 0 : 3; only < 4; ++only) {  // slow: one token per round, renormalised at each
@@ -239,31 +251,27 @@ KDA_DEVICE void rec_body(const Params &p, unsigned char *smem_raw) {
                         const bool on = j < rows;  // (rows behind the end are not staged)
                         const float4 v4 = on ? ld4(&S.val[j][col0]) : make_float4(0.f, 0.f, 0.f, 0.f);
                         const float vs[4] = {v4.x * wf[e], v4.y * wf[e], v4.z * wf[e], v4.w * wf[e]};
-                        float2 acc[4];
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) acc[c] = make_float2(0.f, 0.f);
+                        for (int c = 0; c < 4; ++c) o[e][c] = 0.f;
                         if (on) {
 #pragma unroll
                             for (int i = 0; i < NQ; ++i) {
                                 const float4 k4 = ld4(&S.wr[j][row_of(i, 0)]);
-                                const float2 k2[2] = {make_float2(k4.x, k4.y), make_float2(k4.z, k4.w)};
+                                const float k[4] = {k4.x, k4.y, k4.z, k4.w};
 #pragma unroll
-                                for (int pr = 0; pr < 2; ++pr)
+                                for (int r = 0; r < 4; ++r)
 #pragma unroll
-                                    for (int c = 0; c < 4; ++c)
-                                        s[i][pr][c] = f2fma(k2[pr], make_float2(vs[c], vs[c]), s[i][pr][c]);
+                                    for (int c = 0; c < 4; ++c) s[i][r][c] = fmaf(k[r], vs[c], s[i][r][c]);
                                 if constexpr (MO::out) {
                                     const float4 q4 = ld4(&S.rd[j][row_of(i, 0)]);
-                                    const float2 q2[2] = {make_float2(q4.x, q4.y), make_float2(q4.z, q4.w)};
+                                    const float q[4] = {q4.x, q4.y, q4.z, q4.w};
 #pragma unroll
-                                    for (int pr = 0; pr < 2; ++pr)
+                                    for (int r = 0; r < 4; ++r)
 #pragma unroll
-                                        for (int c = 0; c < 4; ++c) acc[c] = f2fma(q2[pr], s[i][pr][c], acc[c]);
+                                        for (int c = 0; c < 4; ++c) o[e][c] = fmaf(q[r], s[i][r][c], o[e][c]);
                                 }
                             }
                         }
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) o[e][c] = acc[c].x + acc[c].y;
                     }
                     if constexpr (MO::out) {
                         // sums over the row groups: tokens 2 hi, 2 hi + 1, then the one of them with mid
@@ -437,12 +445,12 @@ KDA_DEVICE void rec_body(const Params &p, unsigned char *smem_raw) {
 
 // One pass per CTA layer, or two at once (independent ones, blockIdx.z).
 template <int DA, int DB, int M>
-__global__ void __launch_bounds__(kThreads, 2) rec_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, kCtas<DA, DB>) rec_kernel(const __grid_constant__ Params p) {
     extern __shared__ __align__(16) unsigned char smem_raw[];
     rec_body<DA, DB, M>(p, smem_raw);
 }
 template <int DA, int DB, int M, int DA2, int DB2, int M2>
-__global__ void __launch_bounds__(kThreads, 2) rec_pair_kernel(const __grid_constant__ Params p, const __grid_constant__ Params p2) {
+__global__ void __launch_bounds__(kThreads, kCtas<DA, DB>) rec_pair_kernel(const __grid_constant__ Params p, const __grid_constant__ Params p2) {
     extern __shared__ __align__(16) unsigned char smem_raw[];
     if (blockIdx.z == 0) rec_body<DA, DB, M>(p, smem_raw);
     else rec_body<DA2, DB2, M2>(p2, smem_raw);
