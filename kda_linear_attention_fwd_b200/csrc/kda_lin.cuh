@@ -14,6 +14,10 @@
 // one number), every window's (gamma, Z) is made in parallel by a summary
 // pass, and a scan over the windows turns Z into the incoming states.
 //
+// When the host knows the sequence lengths and there are enough sequences and
+// heads to fill the SMs evenly, a window is a whole sequence instead
+// (by_seq), the longest first, and neither summary nor scan is needed.
+//
 // Reverse passes (the gradient) run the same recurrence from the last token
 // to the first: the state is dL/dS_t, which step t reaches with the decay of
 // token t + 1.  There "init" is dL/d(final state) and "final" dL/d(initial
@@ -49,6 +53,7 @@ struct Params {
     int out_f32;
     const int32_t *cu;
     int num_seqs, T, H, W, win;
+    int by_seq;             // window w is the sequence with w longer ones (kSortSeqs at most; behind that, sequence w)
     const float *init;      // [num_seqs][H] states or null; transposed ([DB][DA]) when init_t
     float *final_state;     // same layout, or null
     int init_t;
@@ -61,12 +66,77 @@ struct Params {
     int32_t *err;           // [3] words of the workspace's header: [2] bit 0 = a bounded wait gave up
     // gradient passes
     float *xdot;            // [T][H]: q . dq, written by the dq pass, read by the dk pass
-    void *ckpt;             // [slots][H][DA][DB]: fp32 passes, the state after each 64-token chunk (fp32);
-                            // bf16 passes, the state before each 128-token chunk (bf16)
+    void *ckpt;             // [slots][H][DA][DB]: fp32: in fp32 passes the state after each 64-token chunk, in
+                            // bf16 passes, before each 128-token chunk
     float *xstate, *across; // bf16 passes, [T][H]: see kda_lin_tc.cu
     void *dg;               // [T][H], input type, or fp32 when g_per_head
     int zero_first_dg;      // no initial state: d(first log-decay) is exactly 0
 };
+
+constexpr int kSortSeqs = 128;
+
+// The tokens [t0, t1) of window w, and its sequences first .. end - 1, of
+// which those from `lo` on start in it.
+struct Window {
+    int t0, t1, lo, first, end;
+};
+__device__ __forceinline__ int first_at_or_behind(const Params &p, int x) {
+    int lo = 0, hi = p.num_seqs;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (p.cu[mid] < x) lo = mid + 1;
+        else hi = mid;
+    }
+    return lo;
+}
+// Called by all threads of the CTA (at least kSortSeqs); ends with a barrier
+// when by_seq.  `slot`: a shared word.
+__device__ __forceinline__ Window window_of(const Params &p, int w, int *slot) {
+    Window v;
+    if (p.by_seq) {
+        if (p.num_seqs <= kSortSeqs) {
+            const int n = threadIdx.x;
+            if (n < p.num_seqs) {
+                const int len = p.cu[n + 1] - p.cu[n];
+                int rank = 0;
+                for (int m = 0; m < p.num_seqs; ++m) {
+                    const int other = p.cu[m + 1] - p.cu[m];
+                    rank += other > len || (other == len && m < n);
+                }
+                if (rank == w) *slot = n;
+            }
+            __syncthreads();
+            v.first = *slot;
+        } else {
+            v.first = w;
+        }
+        v.lo = v.first;
+        v.end = v.first + 1;
+        v.t0 = min(max(p.cu[v.first], 0), p.T);
+        v.t1 = min(max(p.cu[v.end], v.t0), p.T);
+        return v;
+    }
+    v.t0 = w * p.win;
+    v.t1 = min(p.T, v.t0 + p.win);
+    v.lo = first_at_or_behind(p, v.t0);
+    // the sequence that continues into the window, then those that start in it (the last window also
+    // takes the empty ones at the very end)
+    v.first = v.lo > 0 && p.cu[v.lo] > v.t0 ? v.lo - 1 : v.lo;
+    v.end = w == p.W - 1 ? p.num_seqs : first_at_or_behind(p, v.t1);
+    return v;
+}
+// The sequence whose state a summary carries over the window's outgoing edge, or -1.
+__device__ __forceinline__ int crossing(const Params &p, const Window &v, bool rev) {
+    int n;
+    if (!rev) {
+        n = v.t1 < p.T ? first_at_or_behind(p, v.t1) - 1 : -1;
+        if (n >= 0 && p.cu[n + 1] <= v.t1) n = -1;
+    } else {
+        n = v.t0 > 0 ? v.lo - 1 : -1;
+        if (n >= 0 && p.cu[n + 1] <= v.t0) n = -1;
+    }
+    return n;
+}
 
 // SMs of the current device (148 when there is none).
 int sm_count();

@@ -132,19 +132,51 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 struct Windows {
     int win, W;
 };
-// As many windows as fill the SMs once: one CTA per SM and whole 128-token
-// chunks on the tensor cores, two or three CTAs per SM token by token, there in whole
-// 64-token chunks for the gradient and 32 tokens otherwise.  A call with more
-// than one window also runs the summary pass (about 0.6 of the time of the
-// main one) and the scan (about as long as 25 tokens), so what is shorter
-// stays in one.
+// How the tokens are divided over CTAs.  Each pass runs in rounds of as many
+// CTAs as the device holds (tensor cores: one per SM; token by token: two or
+// three), so its time is about rounds x steps of the longest window (128
+// tokens on the tensor cores, one otherwise) + a start-up per round; more than
+// one window also costs the summary pass, about 0.6 of the main one, and the
+// scan.  The gradient's token-by-token passes keep whole 64-token chunks.
 enum class Pass { tc, rec_fwd, rec_bwd };
+struct Model {
+    long slots, step, unit, start, scan;  // CTAs at once; window granularity; tokens per step; steps per round, per scan
+};
+Model model_of(int dk, int dv, Pass pass) {
+    const long sms = sm_count();
+    if (pass == Pass::tc) return {sms, 128, 128, 1, 2};
+    return {(dk * dv > 128 * 64 ? 2 : 3) * sms, pass == Pass::rec_bwd ? 64 : 32, 1, 15, 25};
+}
+long div_up(long a, long b) { return (a + b - 1) / b; }
+double windows_cost(const Model &m, long T, int H, long W) {
+    const double main = (double)div_up(W * H, m.slots) * (div_up(div_up(T, W), m.unit) + m.start);
+    return W > 1 ? 1.6 * main + m.scan : main;
+}
 Windows choose_windows(int T, int H, int dk, int dv, Pass pass) {
-    const long step = pass == Pass::tc ? 128 : pass == Pass::rec_bwd ? 64 : 32;
-    const long target = std::max(1L, (pass == Pass::tc ? 1L : dk * dv > 128 * 64 ? 2L : 3L) * sm_count() / H);
-    long win = std::max(step, ((T + target - 1) / target + step - 1) / step * step);
-    if (pass != Pass::tc && 1.6 * win + 25 >= T) win = std::max(step, (T + step - 1) / step * step);
-    return {(int)win, std::max(1, (int)((T + win - 1) / win))};
+    const Model m = model_of(dk, dv, pass);
+    // one window, or as many as fill the slots once, twice, three or four times
+    long best = 1;
+    for (long k = 1; k <= 4; ++k) {
+        const long W = std::min(std::max(1L, k * m.slots / H), div_up(std::max(T, 1), m.step));
+        const long win = div_up(div_up(T, W), m.step) * m.step;
+        if (W > 1 && windows_cost(m, T, H, div_up(T, win)) < windows_cost(m, T, H, best)) best = div_up(T, win);
+    }
+    const long win = std::max(m.step, div_up(div_up(T, best), m.step) * m.step);
+    return {(int)win, std::max(1, (int)div_up(T, win))};
+}
+// Whole sequences as windows: no summary, but a CTA per (sequence, head), the
+// longest first, which takes about max(longest, work / slots).
+bool choose_by_seq(int T, int N, int H, int dk, int dv, Pass pass, const int32_t *cu_host, const Windows &wd) {
+    if (!cu_host || N > 65535) return false;
+    const Model m = model_of(dk, dv, pass);
+    long total = 0, longest = 0;
+    for (int n = 0; n < N; ++n) {
+        const long c = div_up(cu_host[n + 1] - cu_host[n], m.unit) + m.start;
+        total += c;
+        longest = std::max(longest, c);
+    }
+    const double cost = std::max((double)longest, (double)total * H / m.slots + (N > kda::lin::kSortSeqs ? longest : 0));
+    return cost < windows_cost(m, T, H, wd.W);
 }
 
 // bf16 on the tensor cores, fp32 (and calls with no tokens at all) token by token
@@ -171,7 +203,7 @@ struct BwdLayout {
 BwdLayout bwd_layout(const Windows &wd, bool tc, int T, int N, int H, int Hk, int dk, int dv) {
     BwdLayout L;
     const size_t states = (size_t)wd.W * H * dk * dv * sizeof(float), th = (size_t)T * H * sizeof(float);
-    const size_t ckpt = tc ? ((size_t)T / 128 + N + 1) * sizeof(__nv_bfloat16) : ((size_t)T / 64 + N + 1) * sizeof(float);
+    const size_t ckpt = ((size_t)T / (tc ? 128 : 64) + N + 1) * sizeof(float);
     size_t o = 0;
     L.header = o;  o = align256(o + 64 * sizeof(int32_t));
     L.gamma_f = o; o = align256(o + (size_t)wd.W * H * sizeof(float));
@@ -260,11 +292,13 @@ int kda_lin_chunk_fwd(const void *q, const void *k, const void *v, const void *g
     p.g_per_head = flags & KDA_LIN_DECAY_PER_HEAD;
     p.cu = cu_seqlens;
     p.num_seqs = num_seqs; p.T = total_tokens; p.H = H; p.W = wd.W; p.win = wd.win;
+    p.by_seq = choose_by_seq(total_tokens, num_seqs, H, dk, dv, tc ? Pass::tc : Pass::rec_fwd, cu_seqlens_host, wd);
+    if (p.by_seq) p.W = num_seqs;
     p.init = initial_state;
     p.final_state = final_state;
     p.gamma = (float *)(ws + L.gamma);
     p.win_state = (float *)(ws + L.z);
-    p.start_copy = in_place && wd.W > 1 ? (float *)(ws + L.start) : nullptr;
+    p.start_copy = in_place && wd.W > 1 && !p.by_seq ? (float *)(ws + L.start) : nullptr;
     p.err = (int32_t *)(ws + L.header);
     return ok(tc ? kda::lin::tc_forward(p, dk, dv, st) : kda::lin::rec_forward(p, dk, dv, st)) ? KDA_OK : KDA_ERR_CUDA;
 }
@@ -332,6 +366,8 @@ int kda_lin_bwd(const void *q, const void *k, const void *v, const void *g, cons
     c.g_per_head = per_head;
     c.cu = cu_seqlens;
     c.num_seqs = num_seqs; c.T = total_tokens; c.H = H; c.W = wd.W; c.win = wd.win;
+    c.by_seq = choose_by_seq(total_tokens, num_seqs, H, dk, dv, tc ? Pass::tc : Pass::rec_bwd, cu_seqlens_host, wd);
+    if (c.by_seq) c.W = num_seqs;
     c.xdot = (float *)(ws + L.xdot);
     c.xstate = (float *)(ws + L.xstate);
     c.across = (float *)(ws + L.across);

@@ -94,8 +94,9 @@ KDA_DEVICE void rec_body(const Params &p, unsigned char *smem_raw) {
     const int rg = lane / CGW;
     const int col0 = (warp * CGW + lane % CGW) * 4;
     const int h = blockIdx.x, w = blockIdx.y;
-    const int H = p.H, N = p.num_seqs;
-    const int t0 = w * p.win, t1 = min(p.T, t0 + p.win);
+    const int H = p.H;
+    const Window wd = window_of(p, w, reinterpret_cast<int *>(&sm.fdot[0]));
+    const int t0 = wd.t0, t1 = wd.t1, lo = wd.lo;
     const int hr = MO::out ? h / p.rd_div : 0, Hr = MO::out ? H / p.rd_div : 1;
     const int hw = h / p.wr_div, Hw = H / p.wr_div;
     const int hv = h / p.val_div, Hv = H / p.val_div;
@@ -367,35 +368,12 @@ KDA_DEVICE void rec_body(const Params &p, unsigned char *smem_raw) {
     auto seq_state = [&](int n) -> size_t { return ((size_t)n * H + h) * (DA * DB); };
     const size_t win_at = ((size_t)w * H + h) * (DA * DB);
 
-    // first sequence that starts at or behind t0
-    int lo = 0, hi_ = N;
-    while (lo < hi_) {
-        const int mid = (lo + hi_) >> 1;
-        if (p.cu[mid] < t0) lo = mid + 1;
-        else hi_ = mid;
-    }
     // sequence n's tokens inside the window
     auto seg_a = [&](int n) { return min(max(p.cu[n], t0), t1); };
     auto seg_b = [&](int n, int a) { return max(a, min(p.cu[n + 1], t1)); };
 
     if constexpr (MO::sum) {
-        // the sequence that crosses the window's outgoing edge, if any
-        int n = -1;
-        if (M == SUM) {
-            if (t1 < p.T) {  // the last sequence that starts before t1
-                int l = lo, u = N;
-                while (l < u) {
-                    const int mid = (l + u) >> 1;
-                    if (p.cu[mid] < t1) l = mid + 1;
-                    else u = mid;
-                }
-                n = l - 1;
-                if (n >= 0 && p.cu[n + 1] <= t1) n = -1;
-            }
-        } else {
-            n = t0 > 0 ? lo - 1 : -1;
-            if (n >= 0 && p.cu[n + 1] <= t0) n = -1;
-        }
+        const int n = crossing(p, wd, MO::rev);
         if (n < 0) {
             if (tid == 0) p.gamma[(size_t)w * H + h] = kNoCarry;
             return;
@@ -408,21 +386,7 @@ KDA_DEVICE void rec_body(const Params &p, unsigned char *smem_raw) {
         store_state(p.win_state + win_at, false, 1.f);
         if (tid == 0) p.gamma[(size_t)w * H + h] = whole ? 0.f : gamma;
     } else {
-        // the sequences of this window: the one that continues into it, then
-        // those that start in it (the last window also takes the empty ones
-        // at the very end)
-        const int first = lo > 0 && lo <= N && p.cu[lo] > t0 ? lo - 1 : lo;
-        int end = lo;
-        if (w == p.W - 1) {
-            end = N;
-        } else {
-            int u = N;
-            while (end < u) {
-                const int mid = (end + u) >> 1;
-                if (p.cu[mid] < t1) end = mid + 1;
-                else u = mid;
-            }
-        }
+        const int first = wd.first, end = wd.end;
         for (int i = first; i < end; ++i) {
             const int n = MO::rev ? end - 1 - (i - first) : i;
             const int a = seg_a(n), b = seg_b(n, a);
@@ -534,7 +498,7 @@ static cudaError_t launch_two(const Params &p, const Params &p2, cudaStream_t st
 
 template <int DK_, int DV_>
 static cudaError_t fwd_t(const Params &p, cudaStream_t st) {
-    if (p.W > 1) {
+    if (p.W > 1 && !p.by_seq) {
         cudaError_t e = launch_one<DK_, DV_, SUM>(p, st);
         if (e == cudaSuccess) e = launch_scan(p, nullptr, DK_ * DV_, st);
         if (e != cudaSuccess) return e;
@@ -543,7 +507,7 @@ static cudaError_t fwd_t(const Params &p, cudaStream_t st) {
 }
 template <int DK_, int DV_>
 static cudaError_t bwd_t(const Params &a, const Params &b, const Params &d, cudaStream_t st) {
-    if (a.W > 1) {
+    if (a.W > 1 && !a.by_seq) {
         cudaError_t e = launch_two<DV_, DK_, SUM, DV_, DK_, SUMR>(a, b, st);
         if (e == cudaSuccess) e = launch_scan(a, &b, DK_ * DV_, st);
         if (e != cudaSuccess) return e;

@@ -43,9 +43,10 @@
 //                              one more product) and takes row sums less column sums
 //   u before the chunk         q . (the state's part of dq)      (dq pass)
 //   s behind the chunk         k . (the state's part of dk)      (dk pass)
-//   u before and s behind      exp(chunk) <S_in, B_in>: the dq pass leaves a bf16 copy
-//                              of the state that enters every chunk in the workspace
-// all four linear in the bf16 operands' roundings.
+//   u before and s behind      exp(chunk) <S_in, B_in>, in fp32: the dq pass leaves the
+//                              state that enters every chunk in the workspace.  (This part
+//                              is the same for a chunk's 128 tokens, so a bf16 copy would
+//                              not average out in the sum over the tokens.)
 //
 // Every wait is bounded (2 s): one that gives up marks the workspace's error
 // word and the CTA, whose remaining waits then return at once; the loads and
@@ -177,9 +178,11 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
     Ctl<M == DQ> &ctl = *reinterpret_cast<Ctl<M == DQ> *>(sm + C::off_ctl);
     const uint32_t sbase = smem_u32(sm);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, role = warp >> 2;
-    const int h = blockIdx.x, w = blockIdx.y, H = p.H, N = p.num_seqs;
-    const int t0 = w * p.win, t1 = min(p.T, t0 + p.win);
+    const int h = blockIdx.x, w = blockIdx.y, H = p.H;
+    const Window wd = window_of(p, w, &ctl.dead);
+    const int t0 = wd.t0, t1 = wd.t1, lo = wd.lo;
     volatile int *dead = &ctl.dead;
+    if (p.by_seq) __syncthreads();  // every thread has read the shared word
 
     if (h == 0 && w == 0 && tid < 3 && p.err) p.err[tid] = 0;
 
@@ -236,33 +239,12 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
         return load_g(t);
     };
 
-    // first sequence that starts at or behind x
-    auto lower = [&](int x) {
-        int lo = 0, hi = N;
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (p.cu[mid] < x) lo = mid + 1;
-            else hi = mid;
-        }
-        return lo;
-    };
-    const int lo = lower(t0);
-    int first, end;
-    if (C::sum) {  // the sequence that crosses the window's outgoing edge, if any
-        int n;
-        if (!C::rev) {
-            n = t1 < p.T ? lower(t1) - 1 : -1;
-            if (n >= 0 && p.cu[n + 1] <= t1) n = -1;
-        } else {
-            n = t0 > 0 ? lo - 1 : -1;
-            if (n >= 0 && p.cu[n + 1] <= t0) n = -1;
-        }
+    int first = wd.first, end = wd.end;
+    if (C::sum) {
+        const int n = crossing(p, wd, C::rev);
         first = n < 0 ? 0 : n;
         end = n < 0 ? 0 : n + 1;
         if (n < 0 && tid == 0) p.gamma[(size_t)w * H + h] = kNoCarry;
-    } else {
-        first = lo > 0 && p.cu[lo] > t0 ? lo - 1 : lo;
-        end = w == p.W - 1 ? N : lower(t1);
     }
 
     // f(n, a, b, qb): tokens [a, b) of sequence n, which ends at qb, in the order of the pass
@@ -453,8 +435,8 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                     wait(ctl.kv_done, (it - 1) & 1);
                     tc_fence_after();
                 }
-                bf16 *ck = nullptr;
-                if (M == DQ || M == DK) ck = (bf16 *)p.ckpt + (((size_t)(base / kC + n)) * H + h) * (DA * DB) + (size_t)row * DB;
+                float *ck = nullptr;
+                if (M == DQ || M == DK) ck = (float *)p.ckpt + (((size_t)(base / kC + n)) * H + h) * (DA * DB) + (size_t)row * DB;
                 float dot = 0.f;
                 if (mine) {
 #pragma unroll 1
@@ -481,24 +463,18 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                         }
                         if constexpr (M == DQ) {
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                *reinterpret_cast<uint4 *>(ck + 32 * cb + 8 * e) =
-                                    make_uint4(pack_bf16(__uint_as_float(r[8 * e]), __uint_as_float(r[8 * e + 1])),
-                                               pack_bf16(__uint_as_float(r[8 * e + 2]), __uint_as_float(r[8 * e + 3])),
-                                               pack_bf16(__uint_as_float(r[8 * e + 4]), __uint_as_float(r[8 * e + 5])),
-                                               pack_bf16(__uint_as_float(r[8 * e + 6]), __uint_as_float(r[8 * e + 7])));
+                            for (int e = 0; e < 8; ++e)
+                                *reinterpret_cast<uint4 *>(ck + 32 * cb + 4 * e) =
+                                    make_uint4(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]);
                         }
                         if constexpr (M == DK) {
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const uint4 v = *reinterpret_cast<const uint4 *>(ck + 32 * cb + 8 * e);
-                                const uint32_t vs[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) {
-                                    const float2 u = unpack_bf16(vs[k]);
-                                    dot = fmaf(u.x, __uint_as_float(r[8 * e + 2 * k]), dot);
-                                    dot = fmaf(u.y, __uint_as_float(r[8 * e + 2 * k + 1]), dot);
-                                }
+                            for (int e = 0; e < 8; ++e) {
+                                const float4 v = *reinterpret_cast<const float4 *>(ck + 32 * cb + 4 * e);
+                                dot = fmaf(v.x, __uint_as_float(r[4 * e]), dot);
+                                dot = fmaf(v.y, __uint_as_float(r[4 * e + 1]), dot);
+                                dot = fmaf(v.z, __uint_as_float(r[4 * e + 2]), dot);
+                                dot = fmaf(v.w, __uint_as_float(r[4 * e + 3]), dot);
                             }
                         }
                         const float2 f2 = make_float2(f, f);
@@ -784,6 +760,12 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                 if (C::out) load(C::tR, maps.rd, hr, DA / 64);
                 load(C::tW, maps.wr, hw, DA / 64);
                 load(C::tV, maps.val, hv, DB / 64);
+                if (M == DK && i + 1 < nch && elect_one_sync())  // the next chunk's checkpoint to L2
+                    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"((const float *)p.ckpt +
+                                     ((size_t)(next_base(base) / kC + n) * H + h) * (DA * DB)),
+                                 "r"((uint32_t)(DA * DB * 4))
+                                 : "memory");
+                __syncwarp();
                 ++it;
             });
         });
@@ -978,7 +960,7 @@ cudaError_t launch_t(const Params &p, cudaStream_t st) {
 }
 template <int DK_, int DV_>
 cudaError_t fwd_t(const Params &p, cudaStream_t st) {
-    if (p.W > 1) {
+    if (p.W > 1 && !p.by_seq) {
         cudaError_t e = launch_t<DK_, DV_, SUM>(p, st);
         if (e == cudaSuccess) e = launch_scan(p, nullptr, DK_ * DV_, st);
         if (e != cudaSuccess) return e;
@@ -988,7 +970,7 @@ cudaError_t fwd_t(const Params &p, cudaStream_t st) {
 template <int DK_, int DV_>
 cudaError_t bwd_t(const Params &a, const Params &b, const Params &d, cudaStream_t st) {
     cudaError_t e = cudaSuccess;
-    if (a.W > 1) {
+    if (a.W > 1 && !a.by_seq) {
         e = launch_t<DV_, DK_, SUM>(a, st);
         if (e == cudaSuccess) e = launch_t<DV_, DK_, SUMR>(b, st);
         if (e == cudaSuccess) e = launch_scan(a, &b, DK_ * DV_, st);

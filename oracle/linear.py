@@ -36,7 +36,8 @@ def forward(q, k, v, g, cu, *, scale=1.0, initial_state=None):
 
 def backward(q, k, v, g, cu, dy, *, scale=1.0, initial_state=None, d_final_state=None):
     """Gradients of sum(dy * o) + sum(d_final_state * final): dict of dq, dk
-    [T, Hk, dk], dv [T, H, dv], dg (the shape of g), ds0 [N, H, dk, dv]."""
+    [T, Hk, dk], dv [T, H, dv], dg (the shape of g), ds0 [N, H, dk, dv], and
+    dg_tokens [T, H], whose sum over the tokens is dg when g is per head."""
     per_head, Hk = np.asarray(g).ndim == 1, np.asarray(q).shape[1]
     q, k, v, g, rep = _heads(q, k, v, g)
     dy = np.asarray(dy, np.float64)
@@ -61,6 +62,7 @@ def backward(q, k, v, g, cu, dy, *, scale=1.0, initial_state=None, d_final_state
         out["ds0"][n] = B
     for x in ("dq", "dk"):
         out[x] = out[x].reshape(T, Hk, rep, dk).sum(2)
+    out["dg_tokens"] = out["dg"]
     if per_head:
         out["dg"] = out["dg"].sum(0)
     return out

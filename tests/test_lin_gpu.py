@@ -12,6 +12,12 @@ Tolerances, as ||err||_2 / ||ref||_2:
     the root mean square by at most 2^-8 / sqrt(3) = 2.3e-3; a result goes
     through three independent ones (the products inside a chunk, the state as
     an operand, the output): sqrt(3) 2.3e-3 = 3.9e-3.
+dg of a decay per head is a sum over the tokens, whose terms have either sign
+and may cancel to any smaller value.  A token's term is itself a sum over the
+pairs of an earlier and a later token around it, of which neighbours share most,
+so their roundings are shared too: a chunk of 128 tokens may be off by its
+terms' tolerance of the sum of their magnitudes, chunks independently, however
+small the whole sum is.
 """
 import numpy as np
 import pytest
@@ -44,11 +50,11 @@ def make(lengths, H, Hk, dk, dv, dtype, per_head=False, s0=True, seed=0):
     return d
 
 
-def near(got, want, tol, what):
+def near(got, want, tol, what, room=0.0):
     a, e = np32(got).astype(np.float64), np.asarray(want, np.float64)
     assert a.shape == e.shape, (what, a.shape, e.shape)
     assert np.isfinite(a).all(), f"{what}: not finite"
-    off = np.linalg.norm(a - e) / max(np.linalg.norm(e), 1e-30) if e.size else 0.0
+    off = max(np.linalg.norm(a - e) - room, 0.0) / max(np.linalg.norm(e), 1e-30) if e.size else 0.0
     assert off <= tol, f"{what}: relative error {off:.2e} > {tol:.1e}"
 
 
@@ -182,7 +188,11 @@ def test_decode_steps_equal_prefill(cuda_lib):
 def check_grads(got, ref, dtype):
     for name in ("dq", "dk", "dv", "dg"):
         assert got[name].dtype == DT[dtype]
-        near(got[name], ref[name], TOL[DT[dtype]], name)
+        terms = 0.0
+        if name == "dg" and ref["dg"].ndim == 1:
+            size = np.abs(ref["dg_tokens"])
+            terms = np.linalg.norm([size[t:t + 128].sum(0) for t in range(0, len(size), 128)])
+        near(got[name], ref[name], TOL[DT[dtype]], name, room=TOL[DT[dtype]] * terms)
     near(got["ds0"], ref["ds0"], 2e-5 if dtype == "bf16" else 1e-5, "ds0")
 
 
