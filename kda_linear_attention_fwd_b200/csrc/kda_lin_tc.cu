@@ -431,12 +431,16 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                 if (i + 1 < nch)
 #pragma unroll
                     for (int x = 0; x < 4; ++x) gx[x] = row_g(next_base(base), min(kC, b - next_base(base)), 32 * x + lane, qb);
+                float *ck = nullptr;
+                if (M == DQ || M == DK) ck = (float *)p.ckpt + (((size_t)(base / kC + n)) * H + h) * (DA * DB) + (size_t)row * DB;
+                float4 cv[M == DK ? 4 : 1];  // DK: 16 columns of the checkpoint, requested one round ahead
+                if (M == DK && mine)
+#pragma unroll
+                    for (int e = 0; e < (M == DK ? 4 : 0); ++e) cv[e] = *reinterpret_cast<const float4 *>(ck + 4 * e);
                 if (i > 0) {
                     wait(ctl.kv_done, (it - 1) & 1);
                     tc_fence_after();
                 }
-                float *ck = nullptr;
-                if (M == DQ || M == DK) ck = (float *)p.ckpt + (((size_t)(base / kC + n)) * H + h) * (DA * DB) + (size_t)row * DB;
                 float dot = 0.f;
                 if (mine) {
 #pragma unroll 1
@@ -469,12 +473,17 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                         }
                         if constexpr (M == DK) {
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                const float4 v = *reinterpret_cast<const float4 *>(ck + 32 * cb + 4 * e);
-                                dot = fmaf(v.x, __uint_as_float(r[4 * e]), dot);
-                                dot = fmaf(v.y, __uint_as_float(r[4 * e + 1]), dot);
-                                dot = fmaf(v.z, __uint_as_float(r[4 * e + 2]), dot);
-                                dot = fmaf(v.w, __uint_as_float(r[4 * e + 3]), dot);
+                            for (int half = 0; half < 2; ++half) {
+                                const int at = 32 * cb + 16 * half;
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const float4 v = cv[e];
+                                    if (at + 16 < DB) cv[e] = *reinterpret_cast<const float4 *>(ck + at + 16 + 4 * e);
+                                    dot = fmaf(v.x, __uint_as_float(r[16 * half + 4 * e]), dot);
+                                    dot = fmaf(v.y, __uint_as_float(r[16 * half + 4 * e + 1]), dot);
+                                    dot = fmaf(v.z, __uint_as_float(r[16 * half + 4 * e + 2]), dot);
+                                    dot = fmaf(v.w, __uint_as_float(r[16 * half + 4 * e + 3]), dot);
+                                }
                             }
                         }
                         const float2 f2 = make_float2(f, f);
@@ -643,25 +652,29 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                         if (C::rev ? j > wl : j < wl) c += ctl.ot[pb][j];
                     const float f = exp2f(c) * p.rd_scale;
                     // the state's part, scaled by its rows' decays before P V is added to it
-                    wait(ctl.qs_done, it & 1);
-                    tc_fence_after();
                     const size_t at = ((size_t)(base + row) * H + h) * DB;
                     const float2 f2 = make_float2(f, f);
                     float xi = 0.f;  // gradient passes: the state's part of out . ext
+                    constexpr bool XD = M == DQ || M == DK;
+                    uint4 e4[XD ? 4 : 1];  // 32 channels of ext, requested one round ahead
+                    auto load_ext = [&](int cb) {
+                        const uint4 *src = reinterpret_cast<const uint4 *>(
+                            (const bf16 *)p.ext + ((size_t)(base + row) * (H / p.ext_div) + h / p.ext_div) * DB + 32 * cb);
+                        if (XD && row < rows)
+#pragma unroll
+                            for (int e = 0; e < (XD ? 4 : 0); ++e) e4[e] = src[e];
+                    };
+                    if (XD) {
+#pragma unroll
+                        for (int e = 0; e < (XD ? 4 : 0); ++e) e4[e] = make_uint4(0u, 0u, 0u, 0u);
+                        load_ext(0);
+                    }
+                    wait(ctl.qs_done, it & 1);
+                    tc_fence_after();
 #pragma unroll 1
                     for (int cb = 0; cb < DB / 32; ++cb) {
                         uint32_t x[32];
-                        tmem_ld32(to + 32 * cb, x);
-                        uint4 e4[(M == DQ || M == DK) ? 4 : 1];
-                        if constexpr (M == DQ || M == DK) {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                e4[e] = row < rows ? *reinterpret_cast<const uint4 *>(
-                                                         (const bf16 *)p.ext +
-                                                         ((size_t)(base + row) * (H / p.ext_div) + h / p.ext_div) * DB + 32 * cb + 8 * e)
-                                                   : make_uint4(0u, 0u, 0u, 0u);
-                        }
-                        tc_wait_ld();
+                        tmem_ld32_wait(to + 32 * cb, x);
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
                             const float2 v = f2mul(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), f2);
@@ -669,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                             x[2 * e + 1] = __float_as_uint(v.y);
                         }
                         tmem_st32(to + 32 * cb, x);
-                        if constexpr (M == DQ || M == DK) {
+                        if constexpr (XD) {
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
                                 const uint32_t es[4] = {e4[e].x, e4[e].y, e4[e].z, e4[e].w};
@@ -680,6 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                                     xi = fmaf(u.y, __uint_as_float(x[8 * e + 2 * k + 1]), xi);
                                 }
                             }
+                            if (cb + 1 < DB / 32) load_ext(cb + 1);
                         }
                     }
                     tc_wait_st();
@@ -760,11 +774,14 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                 if (C::out) load(C::tR, maps.rd, hr, DA / 64);
                 load(C::tW, maps.wr, hw, DA / 64);
                 load(C::tV, maps.val, hv, DB / 64);
-                if (M == DK && i + 1 < nch && elect_one_sync())  // the next chunk's checkpoint to L2
+                if (M == DK && i + 1 < nch && elect_one_sync()) {  // the next chunk's ext and checkpoint to L2
+#pragma unroll
+                    for (int x = 0; x < DB / 64; ++x) tma_prefetch_3d(&maps.ext, 64 * x, h / p.ext_div, next_base(base));
                     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"((const float *)p.ckpt +
                                      ((size_t)(next_base(base) / kC + n) * H + h) * (DA * DB)),
                                  "r"((uint32_t)(DA * DB * 4))
                                  : "memory");
+                }
                 __syncwarp();
                 ++it;
             });
@@ -950,7 +967,7 @@ cudaError_t launch_t(const Params &p, cudaStream_t st) {
     Maps maps;
     if (!encode(&maps.wr, p.wr, p.T, p.H / p.wr_div, DA) || !encode(&maps.val, p.val, p.T, p.H / p.val_div, DB) ||
         !encode(&maps.rd, C::out ? p.rd : p.wr, p.T, C::out ? p.H / p.rd_div : p.H / p.wr_div, DA) ||
-        !encode(&maps.ext, M == DQ ? p.ext : p.val, p.T, M == DQ ? p.H / p.ext_div : p.H / p.val_div, DB))
+        !encode(&maps.ext, M == DQ || M == DK ? p.ext : p.val, p.T, M == DQ || M == DK ? p.H / p.ext_div : p.H / p.val_div, DB))
         return cudaErrorInvalidValue;
     static std::atomic<uint64_t> done;
     cudaError_t e = allow_smem(done, (const void *)tc_kernel<DA, DB, M>, bytes);
