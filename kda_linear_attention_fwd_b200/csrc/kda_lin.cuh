@@ -64,6 +64,7 @@ struct Params {
                             // initial state of the sequence that starts in the window and crosses its end:
                             // its last window overwrites that state in the same launch
     int32_t *err;           // [3] words of the workspace's header: [2] bit 0 = a bounded wait gave up
+    int clear_err;          // this kernel clears them
     // gradient passes
     float *xdot;            // [T][H]: q . dq, written by the dq pass, read by the dk pass
     void *ckpt;             // [slots][H][DA][DB]: fp32: in fp32 passes the state after each 64-token chunk, in
@@ -136,6 +137,27 @@ __device__ __forceinline__ int crossing(const Params &p, const Window &v, bool r
         if (n >= 0 && p.cu[n + 1] <= v.t0) n = -1;
     }
     return n;
+}
+
+// Launches of one call follow each other early: a kernel is started while the
+// one before it drains, does what depends on the call's inputs only (offsets,
+// barriers, tensor memory) and waits in after_previous() until that one's
+// results are there.  The first launch of a call is an ordinary one.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+template <typename... K, typename... A>
+cudaError_t launch(void (*kernel)(K...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st, bool follows, A... args) {
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = follows ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, K(args)...);
 }
 
 // SMs of the current device (148 when there is none).

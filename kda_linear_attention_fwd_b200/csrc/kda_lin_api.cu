@@ -62,6 +62,8 @@ struct Tokens {
 template <typename T>
 __global__ void __launch_bounds__(256) head_sum_kernel(const float4 *in0, T *out0, const float4 *in1, T *out1, const Tokens tk,
                                                        int Hk, int rep, int d4) {
+    let_next_start();
+    after_previous();
     const float4 *in = blockIdx.y ? in1 : in0;
     T *out = blockIdx.y ? out1 : out0;
     const long row4 = (long)Hk * d4;
@@ -79,6 +81,8 @@ __global__ void __launch_bounds__(256) head_sum_kernel(const float4 *in0, T *out
 // out = x + y, rounded
 template <typename T>
 __global__ void __launch_bounds__(256) add_kernel(const float *x, const float *y, T *out, const Tokens tk, int H) {
+    let_next_start();
+    after_previous();
     for (long i = tk.first() * H + (long)blockIdx.x * 256 + threadIdx.x; i < tk.last() * H; i += (long)gridDim.x * 256)
         st(out + i, x[i] + y[i]);
 }
@@ -87,6 +91,8 @@ __global__ void __launch_bounds__(256) add_kernel(const float *x, const float *y
 // kSumRows rows, then over the blocks.
 constexpr int kSumRows = 512;
 __global__ void __launch_bounds__(256) token_sum_kernel(const float *x, const float *y, float *part, const Tokens tk, int H) {
+    let_next_start();
+    after_previous();
     __shared__ float s[8][33];
     const int hx = threadIdx.x & 31, ry = threadIdx.x >> 5, h = blockIdx.y * 32 + hx;
     const long b0 = (long)blockIdx.x * kSumRows, t0 = max(b0, tk.first()), t1 = min(b0 + kSumRows, tk.last());
@@ -103,6 +109,8 @@ __global__ void __launch_bounds__(256) token_sum_kernel(const float *x, const fl
 }
 template <typename T>
 __global__ void __launch_bounds__(256) part_sum_kernel(const float *part, T *out, int parts, int H) {
+    let_next_start();
+    after_previous();
     __shared__ float s[8][33];
     const int hx = threadIdx.x & 31, ry = threadIdx.x >> 5, h = blockIdx.x * 32 + hx;
     float a = 0.f;
@@ -426,22 +434,27 @@ int kda_lin_bwd(const void *q, const void *k, const void *v, const void *g, cons
         const long n4 = (long)total_tokens * Hk * dk / 4;
         const dim3 grid((unsigned)std::min<long>((n4 + 255) / 256, 4L * 148), 2);
         const float4 *in0 = (const float4 *)(ws + L.dq), *in1 = (const float4 *)(ws + L.dk);
-        if (bf16)
-            head_sum_kernel<<<grid, 256, 0, st>>>(in0, (__nv_bfloat16 *)dq, in1, (__nv_bfloat16 *)dk_out, tk, Hk, rep, dk / 4);
-        else
-            head_sum_kernel<<<grid, 256, 0, st>>>(in0, (float *)dq, in1, (float *)dk_out, tk, Hk, rep, dk / 4);
+        const cudaError_t e =
+            bf16 ? launch(head_sum_kernel<__nv_bfloat16>, grid, 256, 0, st, true, in0, (__nv_bfloat16 *)dq, in1,
+                          (__nv_bfloat16 *)dk_out, tk, Hk, rep, dk / 4)
+                 : launch(head_sum_kernel<float>, grid, 256, 0, st, true, in0, (float *)dq, in1, (float *)dk_out, tk, Hk, rep,
+                          dk / 4);
+        if (!ok(e)) return KDA_ERR_CUDA;
     }
     if (per_head) {
         const int parts = (total_tokens + kSumRows - 1) / kSumRows, hb = (H + 31) / 32;
         float *part = (float *)(ws + L.part);
-        token_sum_kernel<<<dim3(parts, hb), 256, 0, st>>>(c.xstate, tc ? c.across : nullptr, part, tk, H);
-        if (bf16) part_sum_kernel<<<hb, 256, 0, st>>>(part, (__nv_bfloat16 *)dg, parts, H);
-        else part_sum_kernel<<<hb, 256, 0, st>>>(part, (float *)dg, parts, H);
+        if (!ok(launch(token_sum_kernel, dim3(parts, hb), 256, 0, st, true, c.xstate, tc ? c.across : nullptr, part, tk, H)))
+            return KDA_ERR_CUDA;
+        if (!ok(bf16 ? launch(part_sum_kernel<__nv_bfloat16>, dim3(hb), 256, 0, st, true, part, (__nv_bfloat16 *)dg, parts, H)
+                     : launch(part_sum_kernel<float>, dim3(hb), 256, 0, st, true, part, (float *)dg, parts, H)))
+            return KDA_ERR_CUDA;
     }
     if (tc && !per_head) {
         const long n = (long)total_tokens * H;
-        add_kernel<<<(unsigned)std::min<long>((n + 255) / 256, 8L * 148), 256, 0, st>>>(c.xstate, c.across,
-                                                                                       (__nv_bfloat16 *)dg, tk, H);
+        if (!ok(launch(add_kernel<__nv_bfloat16>, dim3((unsigned)std::min<long>((n + 255) / 256, 8L * 148)), 256, 0, st, true,
+                       c.xstate, c.across, (__nv_bfloat16 *)dg, tk, H)))
+            return KDA_ERR_CUDA;
     }
     return ok(cudaGetLastError()) ? KDA_OK : KDA_ERR_CUDA;
 }

@@ -97,6 +97,8 @@ KDA_DEVICE void rec_body(const Params &p, unsigned char *smem_raw) {
     const int H = p.H;
     const Window wd = window_of(p, w, reinterpret_cast<int *>(&sm.fdot[0]));
     const int t0 = wd.t0, t1 = wd.t1, lo = wd.lo;
+    let_next_start();
+    after_previous();
     const int hr = MO::out ? h / p.rd_div : 0, Hr = MO::out ? H / p.rd_div : 1;
     const int hw = h / p.wr_div, Hw = H / p.wr_div;
     const int hv = h / p.val_div, Hv = H / p.val_div;
@@ -432,8 +434,9 @@ struct ScanSide {
 };
 __global__ void __launch_bounds__(128) scan_kernel(const ScanSide a, const ScanSide b, int W, int H, int quads) {
     const ScanSide sd = blockIdx.z == 0 ? a : b;
-    const int e = blockIdx.x * 128 + threadIdx.x, h = blockIdx.y;
-    if (e >= quads) return;
+    const int e = blockIdx.x * 128 + threadIdx.x, h = blockIdx.y;  // quads is a multiple of 128
+    let_next_start();
+    after_previous();
     float4 carry = make_float4(0.f, 0.f, 0.f, 0.f);
     float4 zz[kAhead], nz[kAhead];
     float gm[kAhead], ng[kAhead];
@@ -473,47 +476,46 @@ cudaError_t launch_scan(const Params &p, const Params *rev, int elems, cudaStrea
     const int quads = elems / 4;
     const ScanSide a{(float4 *)p.win_state, p.gamma, 0};
     const ScanSide b = rev ? ScanSide{(float4 *)rev->win_state, rev->gamma, 1} : a;
-    scan_kernel<<<dim3((quads + 127) / 128, p.H, rev ? 2 : 1), 128, 0, st>>>(a, b, p.W, p.H, quads);
-    return cudaGetLastError();
+    return launch(scan_kernel, dim3(quads / 128, p.H, rev ? 2 : 1), 128, 0, st, true, a, b, p.W, p.H, quads);
 }
 
 template <int DA, int DB, int M>
-static cudaError_t launch_one(const Params &p, cudaStream_t st) {
+static cudaError_t launch_one(const Params &p, cudaStream_t st, bool follows) {
     constexpr int bytes = (int)sizeof(Smem<DA, DB, M>);
     static std::atomic<uint64_t> done;
     cudaError_t e = allow_smem(done, (const void *)rec_kernel<DA, DB, M>, bytes);
     if (e != cudaSuccess) return e;
-    rec_kernel<DA, DB, M><<<dim3(p.H, p.W), kThreads, bytes, st>>>(p);
-    return cudaGetLastError();
+    return launch(rec_kernel<DA, DB, M>, dim3(p.H, p.W), kThreads, bytes, st, follows, p);
 }
 template <int DA, int DB, int M, int DA2, int DB2, int M2>
-static cudaError_t launch_two(const Params &p, const Params &p2, cudaStream_t st) {
+static cudaError_t launch_two(const Params &p, const Params &p2, cudaStream_t st, bool follows) {
     constexpr int b1 = (int)sizeof(Smem<DA, DB, M>), b2 = (int)sizeof(Smem<DA2, DB2, M2>), bytes = b1 > b2 ? b1 : b2;
     static std::atomic<uint64_t> done;
     cudaError_t e = allow_smem(done, (const void *)rec_pair_kernel<DA, DB, M, DA2, DB2, M2>, bytes);
     if (e != cudaSuccess) return e;
-    rec_pair_kernel<DA, DB, M, DA2, DB2, M2><<<dim3(p.H, p.W, 2), kThreads, bytes, st>>>(p, p2);
-    return cudaGetLastError();
+    return launch(rec_pair_kernel<DA, DB, M, DA2, DB2, M2>, dim3(p.H, p.W, 2), kThreads, bytes, st, follows, p, p2);
 }
 
 template <int DK_, int DV_>
 static cudaError_t fwd_t(const Params &p, cudaStream_t st) {
-    if (p.W > 1 && !p.by_seq) {
-        cudaError_t e = launch_one<DK_, DV_, SUM>(p, st);
+    const bool split = p.W > 1 && !p.by_seq;
+    if (split) {
+        cudaError_t e = launch_one<DK_, DV_, SUM>(p, st, false);
         if (e == cudaSuccess) e = launch_scan(p, nullptr, DK_ * DV_, st);
         if (e != cudaSuccess) return e;
     }
-    return launch_one<DK_, DV_, FWD>(p, st);
+    return launch_one<DK_, DV_, FWD>(p, st, split);
 }
 template <int DK_, int DV_>
 static cudaError_t bwd_t(const Params &a, const Params &b, const Params &d, cudaStream_t st) {
-    if (a.W > 1 && !a.by_seq) {
-        cudaError_t e = launch_two<DV_, DK_, SUM, DV_, DK_, SUMR>(a, b, st);
+    const bool split = a.W > 1 && !a.by_seq;
+    if (split) {
+        cudaError_t e = launch_two<DV_, DK_, SUM, DV_, DK_, SUMR>(a, b, st, false);
         if (e == cudaSuccess) e = launch_scan(a, &b, DK_ * DV_, st);
         if (e != cudaSuccess) return e;
     }
-    cudaError_t e = launch_two<DV_, DK_, DQ, DK_, DV_, DV>(a, d, st);
-    return e == cudaSuccess ? launch_one<DV_, DK_, DK>(b, st) : e;
+    cudaError_t e = launch_two<DV_, DK_, DQ, DK_, DV_, DV>(a, d, st, split);
+    return e == cudaSuccess ? launch_one<DV_, DK_, DK>(b, st, true) : e;
 }
 
 // fp32: the forward (summary, scan, output), and the gradient's passes (dq, dk and dg, dv and dS0).

@@ -184,7 +184,13 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
     volatile int *dead = &ctl.dead;
     if (p.by_seq) __syncthreads();  // every thread has read the shared word
 
-    if (h == 0 && w == 0 && tid < 3 && p.err) p.err[tid] = 0;
+    // (the first kernel of a call clears the error words, long before a wait can give up)
+    if (h == 0 && w == 0 && tid < 3 && p.err && p.clear_err) p.err[tid] = 0;
+    if (warp == 20 && elect_one_sync()) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.wr) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.val) : "memory");
+        if (C::out) asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.rd) : "memory");
+    }
 
     if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ctl.tmem)),
@@ -215,6 +221,8 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = ctl.tmem;
+    let_next_start();
+    after_previous();
 
     auto wait = [&](unsigned long long &bar, uint32_t parity) {
         if (mbar_try_wait(smem_u32(&bar), parity) || *dead) return;
@@ -960,7 +968,7 @@ bool encode(CUtensorMap *m, const void *base, int T, int Hx, int D) {
 }
 
 template <int DA, int DB, int M>
-cudaError_t launch_t(const Params &p, cudaStream_t st) {
+cudaError_t launch_t(const Params &p, cudaStream_t st, bool follows) {
     using C = Cfg<DA, DB, M>;
     constexpr int bytes = C::bytes;
     static_assert(bytes <= 232448 && C::off_ctl % 16 == 0, "shared memory");
@@ -972,29 +980,32 @@ cudaError_t launch_t(const Params &p, cudaStream_t st) {
     static std::atomic<uint64_t> done;
     cudaError_t e = allow_smem(done, (const void *)tc_kernel<DA, DB, M>, bytes);
     if (e != cudaSuccess) return e;
-    tc_kernel<DA, DB, M><<<dim3(p.H, p.W), kThreads, bytes, st>>>(p, maps);
-    return cudaGetLastError();
+    Params q = p;
+    q.clear_err = !follows;
+    return launch(tc_kernel<DA, DB, M>, dim3(p.H, p.W), kThreads, bytes, st, follows, q, maps);
 }
 template <int DK_, int DV_>
 cudaError_t fwd_t(const Params &p, cudaStream_t st) {
-    if (p.W > 1 && !p.by_seq) {
-        cudaError_t e = launch_t<DK_, DV_, SUM>(p, st);
+    const bool split = p.W > 1 && !p.by_seq;
+    if (split) {
+        cudaError_t e = launch_t<DK_, DV_, SUM>(p, st, false);
         if (e == cudaSuccess) e = launch_scan(p, nullptr, DK_ * DV_, st);
         if (e != cudaSuccess) return e;
     }
-    return launch_t<DK_, DV_, FWD>(p, st);
+    return launch_t<DK_, DV_, FWD>(p, st, split);
 }
 template <int DK_, int DV_>
 cudaError_t bwd_t(const Params &a, const Params &b, const Params &d, cudaStream_t st) {
+    const bool split = a.W > 1 && !a.by_seq;
     cudaError_t e = cudaSuccess;
-    if (a.W > 1 && !a.by_seq) {
-        e = launch_t<DV_, DK_, SUM>(a, st);
-        if (e == cudaSuccess) e = launch_t<DV_, DK_, SUMR>(b, st);
+    if (split) {
+        e = launch_t<DV_, DK_, SUM>(a, st, false);
+        if (e == cudaSuccess) e = launch_t<DV_, DK_, SUMR>(b, st, true);
         if (e == cudaSuccess) e = launch_scan(a, &b, DK_ * DV_, st);
     }
-    if (e == cudaSuccess) e = launch_t<DV_, DK_, DQ>(a, st);
-    if (e == cudaSuccess) e = launch_t<DV_, DK_, DK>(b, st);
-    if (e == cudaSuccess) e = launch_t<DK_, DV_, DV>(d, st);
+    if (e == cudaSuccess) e = launch_t<DV_, DK_, DQ>(a, st, split);
+    if (e == cudaSuccess) e = launch_t<DV_, DK_, DK>(b, st, true);
+    if (e == cudaSuccess) e = launch_t<DK_, DV_, DV>(d, st, true);
     return e;
 }
 

@@ -484,6 +484,7 @@ __global__ void __launch_bounds__(MT, kBwdCtas<MT>) bwd_kernel(const __grid_cons
 // parts at a time per CTA, four of each thread's loads in flight.
 __global__ void __launch_bounds__(1024) weight_sum_kernel(const float *part, int parts, int D, float *dpost, float *dpre) {
     __shared__ float s[32][33];
+    lin::after_previous();
     const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5, c = blockIdx.x * 32 + cx;
     float *out = blockIdx.y ? dpre : dpost;
     if (!out) return;
@@ -698,9 +699,9 @@ int kda_block_norm_bwd(const void *dout, const void *dnormed, const void *y, int
         if (e != cudaSuccess) return KDA_ERR_CUDA;
     }
     if (weights) {
-        kda::norm::weight_sum_kernel<<<dim3((D + 31) / 32, 2), 1024, 0, st>>>(p.part, rows > 0 ? parts : 0, D,
-                                                                            dpost_weight, dpre_weight);
-        if (cudaGetLastError() != cudaSuccess) return KDA_ERR_CUDA;
+        if (kda::lin::launch(kda::norm::weight_sum_kernel, dim3((D + 31) / 32, 2), 1024, 0, st, rows > 0, p.part,
+                             rows > 0 ? parts : 0, D, dpost_weight, dpre_weight) != cudaSuccess)
+            return KDA_ERR_CUDA;
     }
     return KDA_OK;
 }
