@@ -30,7 +30,9 @@
 //                     (8-15 in a summary)
 //   warps 12-19  O    the outputs, half of the columns per group (TMEM lane = token)
 //   warp  20     TMA  tiles of 128 tokens x 64 channels, 128-byte swizzle
-//   warp  21     MMA  issues every product
+//   warp  21     MMA  issues A and the state's products
+//   warp  22     MMA  issues R S and P V (one warp for all four kinds spent more on
+//                     its waits, about 150 cycles each, than the tensor pipe on them)
 // Shared memory (128 x 128): W and V tiles twice (128 KB), R, the hi/lo buffers
 // and the state copy (32 KB each).
 //
@@ -72,7 +74,7 @@ using namespace sm100;
 
 constexpr int kC = 128;             // tokens per chunk
 constexpr int kBox = 64 * kC * 2;   // bytes of one TMA box: 64 channels x 128 tokens
-constexpr int kWarps = 22;
+constexpr int kWarps = 23;
 constexpr int kThreads = 32 * kWarps;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -89,6 +91,7 @@ struct Ctl {
     unsigned long long full[kMaxSlots], free[kMaxSlots];  // the ring's slots
     unsigned long long a_full[2];         // A is in TMEM (two buffers)
     unsigned long long p_full[2];         // P is in TMEM, in A's place
+    unsigned long long a_free[2];         // P V has read it
     unsigned long long s_full;            // the scaled state and its copy are in place
     unsigned long long vb_full[2], vb_free[2];  // the hi/lo quarters, alternating
     unsigned long long kv_done;           // the state has this chunk's writes
@@ -204,15 +207,17 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
     if (tid == 32) {
         for (int i = 0; i < C::slots; ++i) {
             mbar_init(smem_u32(&ctl.full[i]), 1);
-            mbar_init(smem_u32(&ctl.free[i]), 1);
+            mbar_init(smem_u32(&ctl.free[i]), 2);  // both MMA warps, or one twice
         }
         for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&ctl.a_free[i]), 1);
             mbar_init(smem_u32(&ctl.vb_full[i]), 128);
             mbar_init(smem_u32(&ctl.vb_free[i]), 1);
             mbar_init(smem_u32(&ctl.a_full[i]), 1);
             mbar_init(smem_u32(&ctl.p_full[i]), 128);
         }
-        unsigned long long *one[] = {&ctl.qs_done, &ctl.kv_done, &ctl.pv_done, &ctl.end};
+        unsigned long long *one[] = {&ctl.qs_done, &ctl.kv_done, &ctl.pv_done};
+        mbar_init(smem_u32(&ctl.end), 2);
         unsigned long long *wg[] = {&ctl.s_full, &ctl.clean[0], &ctl.clean[1]};
         mbar_init(smem_u32(&ctl.o_scaled), 256);
         mbar_init(smem_u32(&ctl.o_free), 256);
@@ -452,6 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                     for (int e = 0; e < (M == DK ? 4 : 0); ++e) cv[e] = *reinterpret_cast<const float4 *>(ck + 4 * e);
                 if (i > 0) {
                     wait(ctl.kv_done, (it - 1) & 1);
+                    if (C::out) wait(ctl.qs_done, (it - 1) & 1);  // the copy has been read
                     tc_fence_after();
                 }
                 float dot = 0.f;
@@ -530,6 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
             const bool dst_t = !C::sum && p.init_t;
             if (b > a) {
                 wait(ctl.kv_done, (it - 1) & 1);
+                if (C::out) wait(ctl.qs_done, (it - 1) & 1);
                 tc_fence_after();
             }
             if (dst && mine) {
@@ -593,9 +600,9 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                 wait(ctl.full[slot(it, C::tV)], phase(it, C::tV));
                 if (rows < kC && (NG == 1 || ((quarters + nq - 1) & 1) == grp)) {
                     // The last quarter's rows behind the end hold other tokens: zero, whatever they are (the
-                    // quarters behind it are not read); each thread the channels that it reads below.  The MMA
-                    // warp has passed its wait for the short chunk two before this one, if that was one: this
-                    // chunk's V lies in a slot (of kMaxSlots at most) whose last tile was released behind it.
+                    // quarters behind it are not read); each thread the channels that it reads below.  Both MMA
+                    // warps have passed their wait for the short chunk two before this one, if that was one:
+                    // this chunk's V lies in a slot (of kMaxSlots at most) whose last tile they released behind it.
                     wait(ctl.full[slot(it, C::tW)], phase(it, C::tW));
                     const int r = 32 * (nq - 1) + lane;
                     if (r >= rows) {
@@ -814,11 +821,12 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
     } else {
         // --------------------------------------------------------------- MMA
         constexpr uint32_t ID_A = idesc_bf16(128, 128, 0, 0);  // R (K-major) x W (K-major)
-        constexpr uint32_t ID_O = idesc_bf16(128, DB, 0, 1);  // R (K-major) x S (MN-major)
+        constexpr uint32_t ID_O = idesc_bf16(128, DB, 0, 1);   // R (K-major) x S (MN-major)
         constexpr uint32_t ID_KV = idesc_bf16(128, DB, 1, 1);  // W^T (MN-major) x w V (MN-major)
         constexpr uint32_t ID_PV = idesc_bf16(128, DB, 0, 1);  // P (TMEM) x V (MN-major)
-        // A of a chunk is issued one chunk ahead (its operands are there by then, and P's warps
-        // need not wait for this chunk's other products); two cursors walk the chunks.
+        auto tile = [&](int c, int j) -> uint32_t { return sbase + (uint32_t)slot(c, j) * C::slot_bytes; };
+        auto release = [&](int c, int j) { tc_commit(smem_u32(&ctl.free[slot(c, j)])); };
+        // a walk over the chunks that can run one ahead of another
         struct Cursor {
             int seg, ci, nch, a, b, base, rows;
         };
@@ -836,59 +844,103 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
             c.rows = min(kC, c.b - c.base);
             return true;
         };
-        Cursor ahead{-1, 0, 0, 0, 0, 0, 0}, cur{-1, 0, 0, 0, 0, 0, 0};
-        int quarters = 0, k = 0;  // k: chunks whose A has been issued
-        uint32_t cleans[2] = {0u, 0u};
-        auto tile = [&](int c, int j) -> uint32_t { return sbase + (uint32_t)slot(c, j) * C::slot_bytes; };
-        auto begin = [&]() {
-            if (!next(ahead)) return;
-            if (C::out) wait(ctl.full[slot(k, C::tR)], phase(k, C::tR));
-            wait(ctl.full[slot(k, C::tW)], phase(k, C::tW));
-            if (M == DQ) {
-                wait(ctl.full[slot(k, C::tE)], phase(k, C::tE));
-                wait(ctl.full[slot(k, C::tV)], phase(k, C::tV));
-            }
-            if (ahead.rows < kC) {
-                const uint32_t seen = k & 1 ? cleans[1] : cleans[0];
-                wait(ctl.clean[k & 1], seen & 1);
-                (k & 1 ? cleans[1] : cleans[0]) = seen + 1;
-            }
-            if (C::out) {
-                // P's columns are A's.  (With two buffers the P V of two chunks before is known to be complete:
-                // O was free again when the chunk between them began.)
-                if (M == DQ && k > 0) wait(ctl.pv_done, (k - 1) & 1);
-                tc_fence_after();
-                const uint32_t tr = tile(k, C::tR), tw = tile(k, C::tW), ab = M == DQ ? 0u : (uint32_t)(k & 1);
-                const uint32_t te = M == DQ ? tile(k, C::tE) : 0u, tv = M == DQ ? tile(k, C::tV) : 0u;
-                if (elect_one_sync()) {
-#pragma unroll
-                    for (int kk = 0; kk < DA / 16; ++kk) {
-                        const uint32_t off = (kk >> 2) * kBox + (kk & 3) * 32;
-                        tc_mma_ss(tmem + C::col_a + 128 * ab, sdesc_sw128(tr + off, 16, 1024), sdesc_sw128(tw + off, 16, 1024),
-                                  ID_A, kk > 0);
-                    }
-                    if constexpr (M == DQ) {  // Q K^T beside it
-#pragma unroll
-                        for (int kk = 0; kk < DB / 16; ++kk) {
-                            const uint32_t off = (kk >> 2) * kBox + (kk & 3) * 32;
-                            tc_mma_ss(tmem + C::col_a + 128, sdesc_sw128(te + off, 16, 1024), sdesc_sw128(tv + off, 16, 1024), ID_A,
-                                      kk > 0);
-                        }
-                        tc_commit(smem_u32(&ctl.free[slot(k, C::tE)]));
-                    }
-                    tc_commit(smem_u32(&ctl.a_full[ab]));
+        Cursor cur{-1, 0, 0, 0, 0, 0, 0};
+        if (warp == 21) {
+            // A, one chunk ahead of the state's products where it has two buffers (P's warps then
+            // never wait for it), and the state's products
+            Cursor ahead = cur;
+            int quarters = 0, k = 0;  // k: chunks whose A has been issued
+            uint32_t cleans[2] = {0u, 0u};
+            auto begin = [&]() {
+                if (!next(ahead)) return;
+                if (C::out) wait(ctl.full[slot(k, C::tR)], phase(k, C::tR));
+                wait(ctl.full[slot(k, C::tW)], phase(k, C::tW));
+                if (M == DQ) {
+                    wait(ctl.full[slot(k, C::tE)], phase(k, C::tE));
+                    wait(ctl.full[slot(k, C::tV)], phase(k, C::tV));
                 }
-                __syncwarp();
+                if (ahead.rows < kC) {
+                    const uint32_t seen = k & 1 ? cleans[1] : cleans[0];
+                    wait(ctl.clean[k & 1], seen & 1);
+                    (k & 1 ? cleans[1] : cleans[0]) = seen + 1;
+                }
+                if (C::out) {
+                    const uint32_t ab = M == DQ ? 0u : (uint32_t)(k & 1);
+                    const int use = M == DQ ? k : k >> 1;  // of this buffer
+                    if (use > 0) wait(ctl.a_free[ab], (use - 1) & 1);
+                    tc_fence_after();
+                    const uint32_t tr = tile(k, C::tR), tw = tile(k, C::tW);
+                    const uint32_t te = M == DQ ? tile(k, C::tE) : 0u, tv = M == DQ ? tile(k, C::tV) : 0u;
+                    if (elect_one_sync()) {
+#pragma unroll
+                        for (int kk = 0; kk < DA / 16; ++kk) {
+                            const uint32_t off = (kk >> 2) * kBox + (kk & 3) * 32;
+                            tc_mma_ss(tmem + C::col_a + 128 * ab, sdesc_sw128(tr + off, 16, 1024),
+                                      sdesc_sw128(tw + off, 16, 1024), ID_A, kk > 0);
+                        }
+                        if constexpr (M == DQ) {  // Q K^T beside it
+#pragma unroll
+                            for (int kk = 0; kk < DB / 16; ++kk) {
+                                const uint32_t off = (kk >> 2) * kBox + (kk & 3) * 32;
+                                tc_mma_ss(tmem + C::col_a + 128, sdesc_sw128(te + off, 16, 1024), sdesc_sw128(tv + off, 16, 1024),
+                                          ID_A, kk > 0);
+                            }
+                            release(k, C::tE);
+                            release(k, C::tE);
+                        }
+                        tc_commit(smem_u32(&ctl.a_full[ab]));
+                        release(k, C::tR);
+                    }
+                    __syncwarp();
+                }
+                ++k;
+            };
+            if (M != DQ) begin();
+            while (next(cur)) {
+                if (M == DQ) begin();
+                const int nq = (cur.rows + 31) / 32;
+                const uint32_t tw = tile(it, C::tW);
+                wait(ctl.s_full, it & 1);
+                auto quarter = [&](int qq) {
+                    const int vbuf = quarters & 1;
+                    wait(ctl.vb_full[vbuf], (quarters >> 1) & 1);
+                    tc_fence_after();
+                    const uint32_t vb = sbase + C::off_vb + vbuf * C::vb_bytes;
+                    if (elect_one_sync()) {
+#pragma unroll
+                        for (int part = 0; part < 2; ++part)
+#pragma unroll
+                            for (int kk = 0; kk < 2; ++kk)
+                                tc_mma_ss(tmem + C::col_s, sdesc_sw128(tw + 4096 * qq + 2048 * kk, kBox, 1024),
+                                          sdesc_sw128(vb + part * C::vb_part + 2048 * kk, 4096, 1024), ID_KV, 1u);
+                        tc_commit(smem_u32(&ctl.vb_free[vbuf]));
+                        if (qq == nq - 1) {
+                            tc_commit(smem_u32(&ctl.kv_done));
+                            release(it, C::tW);
+                            release(it, C::tW);
+                            release(it, C::tV);
+                            if (C::sum) release(it, C::tV);
+                        }
+                    }
+                    __syncwarp();
+                    ++quarters;
+                };
+                const int before = M == DQ ? nq : min(nq, 2);
+                for (int qq = 0; qq < before; ++qq) quarter(qq);
+                if (M != DQ) begin();  // the next chunk's
+                for (int qq = before; qq < nq; ++qq) quarter(qq);
+                ++it;
             }
-            ++k;
-        };
-        if (M != DQ) begin();
-        while (next(cur)) {
-            if (M == DQ) begin();
-            const int rows = cur.rows, nq = (rows + 31) / 32;
-            const uint32_t tw = tile(it, C::tW);
-            wait(ctl.s_full, it & 1);
-            if (C::out) {
+        } else if (C::out) {
+            uint32_t cleans[2] = {0u, 0u};
+            while (next(cur)) {
+                if (cur.rows < kC) {
+                    const uint32_t seen = it & 1 ? cleans[1] : cleans[0];
+                    wait(ctl.clean[it & 1], seen & 1);
+                    (it & 1 ? cleans[1] : cleans[0]) = seen + 1;
+                }
+                wait(ctl.full[slot(it, C::tR)], phase(it, C::tR));
+                wait(ctl.s_full, it & 1);
                 if (it > 0) wait(ctl.o_free, (it - 1) & 1);
                 tc_fence_after();
                 const uint32_t tr = tile(it, C::tR);
@@ -897,58 +949,29 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                     for (int kk = 0; kk < DA / 16; ++kk)
                         tc_mma_ss(tmem + C::col_o, sdesc_sw128(tr + (kk >> 2) * kBox + (kk & 3) * 32, 16, 1024),
                                   sdesc_sw128(sbase + C::off_sb + 2048 * kk, DA * 128, 1024), ID_O, kk > 0);
-                    tc_commit(smem_u32(&ctl.free[slot(it, C::tR)]));
                     tc_commit(smem_u32(&ctl.qs_done));
+                    release(it, C::tR);
                 }
                 __syncwarp();
-            }
-            auto quarter = [&](int qq) {
-                const int vbuf = quarters & 1;
-                wait(ctl.vb_full[vbuf], (quarters >> 1) & 1);
-                tc_fence_after();
-                const uint32_t vb = sbase + C::off_vb + vbuf * C::vb_bytes;
-                if (elect_one_sync()) {
-#pragma unroll
-                    for (int part = 0; part < 2; ++part)
-#pragma unroll
-                        for (int kk = 0; kk < 2; ++kk)
-                            tc_mma_ss(tmem + C::col_s, sdesc_sw128(tw + 4096 * qq + 2048 * kk, kBox, 1024),
-                                      sdesc_sw128(vb + part * C::vb_part + 2048 * kk, 4096, 1024), ID_KV, 1u);
-                    tc_commit(smem_u32(&ctl.vb_free[vbuf]));
-                    if (qq == nq - 1) tc_commit(smem_u32(&ctl.kv_done));
-                }
-                __syncwarp();
-                ++quarters;
-            };
-            // half of the state's products while O is being scaled, P V, then the other half, behind which
-            // O is read and stored
-            const int before = C::sum ? nq : min(nq, 2);
-            for (int qq = 0; qq < before; ++qq) quarter(qq);
-            if (C::out) {
                 const uint32_t ab = M == DQ ? 0u : (uint32_t)(it & 1), tv = tile(it, C::tV);
                 wait(ctl.full[slot(it, C::tV)], phase(it, C::tV));
                 wait(ctl.p_full[ab], (M == DQ ? it : it >> 1) & 1);
                 wait(ctl.o_scaled, it & 1);
                 tc_fence_after();
                 if (elect_one_sync()) {
-                    const int steps = (rows + 15) / 16;
+                    const int steps = (cur.rows + 15) / 16;
 #pragma unroll
                     for (int kk = 0; kk < kC / 16; ++kk)
                         if (kk < steps)
                             tc_mma_ts(tmem + C::col_o, tmem + C::col_a + 128 * ab + 8 * kk, sdesc_sw128(tv + 2048 * kk, kBox, 1024),
                                       ID_PV, 1u);
                     tc_commit(smem_u32(&ctl.pv_done));
+                    tc_commit(smem_u32(&ctl.a_free[ab]));
+                    release(it, C::tV);
                 }
                 __syncwarp();
+                ++it;
             }
-            for (int qq = before; qq < nq; ++qq) quarter(qq);
-            if (elect_one_sync()) {
-                tc_commit(smem_u32(&ctl.free[slot(it, C::tW)]));
-                tc_commit(smem_u32(&ctl.free[slot(it, C::tV)]));
-            }
-            __syncwarp();
-            if (M != DQ) begin();  // the next chunk's
-            ++it;
         }
         if (*dead) {  // the products in flight end before TMEM is released (bounded)
             if (elect_one_sync()) tc_commit(smem_u32(&ctl.end));
