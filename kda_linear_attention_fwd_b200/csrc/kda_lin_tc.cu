@@ -51,6 +51,11 @@
 //                              is the same for a chunk's 128 tokens, so a bf16 copy would
 //                              not average out in the sum over the tokens.)
 //
+// The kernel's code is long for what an SM holds of it close by, and a warp that
+// runs each instruction once per chunk (the MMA warps above all) waits for its
+// code longer than for anything else; so the products are loops, the slow part of
+// a wait is a call, and what a chunk does not need is kept out of its loop.
+//
 // Every wait is bounded (2 s): one that gives up marks the workspace's error
 // word and the CTA, whose remaining waits then return at once; the loads and
 // products in flight are waited for before TMEM is released.
@@ -176,6 +181,35 @@ KDA_DEVICE float scan_down(float x, int lane) {
     return x;
 }
 
+// A wait whose first try failed: bounded, see the file comment.  Out of line, as
+// the kernel's code is what its single warps wait for most (see there).
+__device__ __noinline__ void slow_wait(uint32_t bar, uint32_t parity, volatile int *dead, int32_t *err) {
+    if (*dead || mbar_wait(bar, parity)) return;
+    *dead = 1;
+    if (err) atomicOr(err + 2, 1);
+}
+
+// `n` products of K = 16 each, kept as a loop: A and B advance by the given
+// bytes, and A (B) by `jump` instead after every fourth when it is K-major in
+// 64-channel boxes.
+struct Operand {
+    uint64_t desc;
+    uint32_t step;
+    int32_t jump;  // 0: none
+};
+KDA_DEVICE Operand kmajor(uint32_t at) { return {sdesc_sw128(at, 16, 1024), 32, kBox - 96}; }
+KDA_DEVICE Operand mnmajor(uint32_t at, uint32_t block) { return {sdesc_sw128(at, block, 1024), 2048, 0}; }
+KDA_DEVICE void advance(Operand &o, int kk) { o.desc += (uint64_t)((o.jump && (kk & 3) == 3 ? (uint32_t)o.jump : o.step) >> 4); }
+KDA_DEVICE void products(uint32_t d, Operand a, Operand b, uint32_t idesc, int n, uint32_t accumulate) {
+#pragma unroll 1
+    for (int kk = 0; kk < n; ++kk) {
+        tc_mma_ss(d, a.desc, b.desc, idesc, accumulate);
+        accumulate = 1u;
+        advance(a, kk);
+        advance(b, kk);
+    }
+}
+
 template <int DA, int DB, int M>
 __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__ Params p,
                                                          const __grid_constant__ Maps maps) {
@@ -235,11 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
     after_previous();
 
     auto wait = [&](unsigned long long &bar, uint32_t parity) {
-        if (mbar_try_wait(smem_u32(&bar), parity) || *dead) return;
-        if (!mbar_wait(smem_u32(&bar), parity)) {
-            *dead = 1;
-            if (p.err) atomicOr(p.err + 2, 1);
-        }
+        if (!mbar_try_wait(smem_u32(&bar), parity)) slow_wait(smem_u32(&bar), parity, dead, p.err);
     };
     auto arrive = [&](unsigned long long &bar) { mbar_arrive(smem_u32(&bar)); };
     // tile j of chunk c in the ring
@@ -421,24 +451,34 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                 src = p.init ? p.init + seq_at : nullptr;
                 src_t = p.init_t;
             }
-            // 32 columns of this thread's row of the state before the chunk
-            auto load32 = [&](int cb, bool from_src, uint32_t (&r)[32]) {
-                if (!from_src) {
-                    tmem_ld32_wait(ts + 32 * cb, r);
-                } else if (!src || !mine) {
+            // the state's start to TMEM (the previous segment's products are complete)
+            if (mine) {
+#pragma unroll 1
+                for (int cb = 0; cb < DB / 32; ++cb) {
+                    uint32_t r[32];
+                    if (!src) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) r[e] = 0u;
-                } else if (!src_t) {
+                        for (int e = 0; e < 32; ++e) r[e] = 0u;
+                    } else if (!src_t) {
 #pragma unroll
-                    for (int e4 = 0; e4 < 8; ++e4) {
-                        const uint4 v = *reinterpret_cast<const uint4 *>(src + (size_t)row * DB + 32 * cb + 4 * e4);
-                        r[4 * e4] = v.x; r[4 * e4 + 1] = v.y; r[4 * e4 + 2] = v.z; r[4 * e4 + 3] = v.w;
+                        for (int e4 = 0; e4 < 8; ++e4) {
+                            const uint4 v = *reinterpret_cast<const uint4 *>(src + (size_t)row * DB + 32 * cb + 4 * e4);
+                            r[4 * e4] = v.x; r[4 * e4 + 1] = v.y; r[4 * e4 + 2] = v.z; r[4 * e4 + 3] = v.w;
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(src[(size_t)(32 * cb + e) * DA + row]);
                     }
-                } else {
+                    tmem_st32(ts + 32 * cb, r);
+                    if (C::sum && p.start_copy && !from_win) {
+                        float *dst = p.start_copy + win_at + (size_t)row * DB + 32 * cb;
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(src[(size_t)(32 * cb + e) * DA + row]);
+                        for (int e4 = 0; e4 < 8; ++e4)
+                            reinterpret_cast<uint4 *>(dst)[e4] = make_uint4(r[4 * e4], r[4 * e4 + 1], r[4 * e4 + 2], r[4 * e4 + 3]);
+                    }
                 }
-            };
+                tc_wait_st();
+            }
             float gx[4] = {0.f, 0.f, 0.f, 0.f};
             chunks(a, b, [&](int base, int rows, int i, int nch) {
                 if (i == 0)
@@ -465,13 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
 #pragma unroll 1
                     for (int cb = 0; cb < DB / 32; ++cb) {
                         uint32_t r[32];
-                        load32(cb, i == 0, r);
-                        if (C::sum && i == 0 && p.start_copy && !from_win) {
-                            float *dst = p.start_copy + win_at + (size_t)row * DB + 32 * cb;
-#pragma unroll
-                            for (int e4 = 0; e4 < 8; ++e4)
-                                reinterpret_cast<uint4 *>(dst)[e4] = make_uint4(r[4 * e4], r[4 * e4 + 1], r[4 * e4 + 2], r[4 * e4 + 3]);
-                        }
+                        tmem_ld32_wait(ts + 32 * cb, r);
                         if (C::out) {  // the copy that R reads: [DA rows][64 channels] boxes, 128-byte swizzle
                             unsigned char *box = sm + C::off_sb + (cb >> 1) * (DA * 128) + row * 128;
 #pragma unroll
@@ -544,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
 #pragma unroll 1
                 for (int cb = 0; cb < DB / 32; ++cb) {
                     uint32_t r[32];
-                    load32(cb, b == a, r);
+                    tmem_ld32_wait(ts + 32 * cb, r);
 #pragma unroll
                     for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
                     if (!dst_t) {
@@ -872,19 +906,9 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                     const uint32_t tr = tile(k, C::tR), tw = tile(k, C::tW);
                     const uint32_t te = M == DQ ? tile(k, C::tE) : 0u, tv = M == DQ ? tile(k, C::tV) : 0u;
                     if (elect_one_sync()) {
-#pragma unroll
-                        for (int kk = 0; kk < DA / 16; ++kk) {
-                            const uint32_t off = (kk >> 2) * kBox + (kk & 3) * 32;
-                            tc_mma_ss(tmem + C::col_a + 128 * ab, sdesc_sw128(tr + off, 16, 1024),
-                                      sdesc_sw128(tw + off, 16, 1024), ID_A, kk > 0);
-                        }
+                        products(tmem + C::col_a + 128 * ab, kmajor(tr), kmajor(tw), ID_A, DA / 16, 0u);
                         if constexpr (M == DQ) {  // Q K^T beside it
-#pragma unroll
-                            for (int kk = 0; kk < DB / 16; ++kk) {
-                                const uint32_t off = (kk >> 2) * kBox + (kk & 3) * 32;
-                                tc_mma_ss(tmem + C::col_a + 128, sdesc_sw128(te + off, 16, 1024), sdesc_sw128(tv + off, 16, 1024),
-                                          ID_A, kk > 0);
-                            }
+                            products(tmem + C::col_a + 128, kmajor(te), kmajor(tv), ID_A, DB / 16, 0u);
                             release(k, C::tE);
                             release(k, C::tE);
                         }
@@ -907,12 +931,9 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                     tc_fence_after();
                     const uint32_t vb = sbase + C::off_vb + vbuf * C::vb_bytes;
                     if (elect_one_sync()) {
-#pragma unroll
+#pragma unroll 1
                         for (int part = 0; part < 2; ++part)
-#pragma unroll
-                            for (int kk = 0; kk < 2; ++kk)
-                                tc_mma_ss(tmem + C::col_s, sdesc_sw128(tw + 4096 * qq + 2048 * kk, kBox, 1024),
-                                          sdesc_sw128(vb + part * C::vb_part + 2048 * kk, 4096, 1024), ID_KV, 1u);
+                            products(tmem + C::col_s, mnmajor(tw + 4096 * qq, kBox), mnmajor(vb + part * C::vb_part, 4096), ID_KV, 2, 1u);
                         tc_commit(smem_u32(&ctl.vb_free[vbuf]));
                         if (qq == nq - 1) {
                             tc_commit(smem_u32(&ctl.kv_done));
@@ -945,10 +966,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                 tc_fence_after();
                 const uint32_t tr = tile(it, C::tR);
                 if (elect_one_sync()) {
-#pragma unroll
-                    for (int kk = 0; kk < DA / 16; ++kk)
-                        tc_mma_ss(tmem + C::col_o, sdesc_sw128(tr + (kk >> 2) * kBox + (kk & 3) * 32, 16, 1024),
-                                  sdesc_sw128(sbase + C::off_sb + 2048 * kk, DA * 128, 1024), ID_O, kk > 0);
+                    products(tmem + C::col_o, kmajor(tr), mnmajor(sbase + C::off_sb, DA * 128), ID_O, DA / 16, 0u);
                     tc_commit(smem_u32(&ctl.qs_done));
                     release(it, C::tR);
                 }
@@ -959,12 +977,12 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                 wait(ctl.o_scaled, it & 1);
                 tc_fence_after();
                 if (elect_one_sync()) {
-                    const int steps = (cur.rows + 15) / 16;
-#pragma unroll
-                    for (int kk = 0; kk < kC / 16; ++kk)
-                        if (kk < steps)
-                            tc_mma_ts(tmem + C::col_o, tmem + C::col_a + 128 * ab + 8 * kk, sdesc_sw128(tv + 2048 * kk, kBox, 1024),
-                                      ID_PV, 1u);
+                    Operand v = mnmajor(tv, kBox);
+#pragma unroll 1
+                    for (int kk = 0; kk < (cur.rows + 15) / 16; ++kk) {
+                        tc_mma_ts(tmem + C::col_o, tmem + C::col_a + 128 * ab + 8 * kk, v.desc, ID_PV, 1u);
+                        advance(v, kk);
+                    }
                     tc_commit(smem_u32(&ctl.pv_done));
                     tc_commit(smem_u32(&ctl.a_free[ab]));
                     release(it, C::tV);
