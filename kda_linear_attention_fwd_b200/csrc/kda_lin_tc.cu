@@ -275,16 +275,15 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
     // tile j of chunk c in the ring
     auto slot = [&](int c, int j) { return (c * C::tiles + j) % C::slots; };
     auto phase = [&](int c, int j) -> uint32_t { return (uint32_t)((c * C::tiles + j) / C::slots) & 1u; };
+    const bf16 *gp = (const bf16 *)p.g + h;
+    const uint32_t gs = p.g_per_head ? 0u : (uint32_t)H;
     auto load_g = [&](int t) -> float {  // in powers of two
-        const size_t at = p.g_per_head ? (size_t)h : (size_t)t * H + h;
-        return fmaxf(__bfloat162float(((const bf16 *)p.g)[at]), kMinG) * kLog2e;
+        return fmaxf(__bfloat162float(gp[(size_t)(uint32_t)t * gs]), kMinG) * kLog2e;
     };
     // the decay that row `row` of the chunk of `rows` tokens at `base` multiplies the running state with
     auto row_g = [&](int base, int rows, int row, int qb) -> float {
-        if (row >= rows) return 0.f;
-        const int t = base + row;
-        if (C::rev) return t + 1 < qb ? load_g(t + 1) : 0.f;
-        return load_g(t);
+        const int t = base + row + (C::rev ? 1 : 0);
+        return row < rows && (!C::rev || t < qb) ? load_g(t) : 0.f;
     };
 
     int first = wd.first, end = wd.end;
@@ -676,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                             const float2 v = f2mul(unpack_bf16(xs[e]), f2);
                             hi[e] = pack_bf16(v);
                             const float2 k2 = unpack_bf16(hi[e]);
-                            lw[e] = pack_bf16(v.x - k2.x, v.y - k2.y);
+                            lw[e] = pack_bf16(f2fma(k2, make_float2(-1.f, -1.f), v));
                         }
                         unsigned char *dst = sm + C::off_vb + vb * C::vb_bytes + box * 4096 + lane * 128 + off;
                         *reinterpret_cast<uint4 *>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
