@@ -206,7 +206,7 @@ FwdLayout fwd_layout(const Windows &wd, int H, int dk, int dv) {
 }
 
 struct BwdLayout {
-    size_t header, gamma_f, gamma_r, zf, zr, xdot, xstate, xstate2, across, ckpt, part, dq, dk, total;
+    size_t header, gamma_f, gamma_r, zf, zr, xdot, xstate, across, ckpt, part, dq, dk, total;
 };
 BwdLayout bwd_layout(const Windows &wd, bool tc, int T, int N, int H, int Hk, int dk, int dv) {
     BwdLayout L;
@@ -220,7 +220,6 @@ BwdLayout bwd_layout(const Windows &wd, bool tc, int T, int N, int H, int Hk, in
     L.zr = o;      o = align256(o + states);
     L.xdot = o;    o = align256(o + th);
     L.xstate = o;  o = align256(o + th);
-    L.xstate2 = o; o = align256(o + (tc ? th : 0));
     L.across = o;  o = align256(o + (tc ? th : 0));
     L.ckpt = o;    o = align256(o + ckpt * H * dk * dv);
     L.part = o;    o = align256(o + ((size_t)T / kda::lin::kSumRows + 1) * H * sizeof(float));
@@ -379,7 +378,6 @@ int kda_lin_bwd(const void *q, const void *k, const void *v, const void *g, cons
     if (c.by_seq) c.W = num_seqs;
     c.xdot = (float *)(ws + L.xdot);
     c.xstate = (float *)(ws + L.xstate);
-    c.xstate2 = (float *)(ws + L.xstate2);
     c.across = (float *)(ws + L.across);
     c.err = (int32_t *)(ws + L.header);
     c.ckpt = ws + L.ckpt;

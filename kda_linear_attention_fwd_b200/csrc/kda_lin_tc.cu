@@ -26,9 +26,9 @@
 // step has its own warpgroup, one chunk apart at most, joined by mbarriers:
 //   warps  0- 3  P    the decayed products           (TMEM lane = token)
 //   warps  4- 7  S    the state: scaled in TMEM, bf16 copy to shared memory
-//   warps  8-11  V    w V as hi and lo parts, 32 tokens at a time into two alternating buffers
-//                     (8-15 in a summary)
-//   warps 12-19  O    the outputs, half of the columns per group (TMEM lane = token)
+//   warps  8-15  V    w V as hi and lo parts, 32 tokens at a time into two alternating buffers,
+//                     one group each (with one group for both this is what a chunk waits for)
+//   warps 16-19  O    the outputs                    (TMEM lane = token)
 //   warp  20     TMA  tiles of 128 tokens x 64 channels, 128-byte swizzle
 //   warp  21     MMA  issues A and the state's products
 //   warp  22     MMA  issues R S and P V (one warp for all four kinds spent more on
@@ -112,9 +112,8 @@ struct Ctl {
     // buffers where no barrier of the warpgroup follows their last use
     alignas(16) float pc[DQ ? 1 : 2][kC], pe[DQ ? 1 : 2][kC];
     float pt[2][4];
-    float ot[2][2][4];                     // O, per group: block sums
+    float ot[2][4];                        // O: block sums
     float sd[2][4];                        // DK, S: partial products with the checkpoint
-    float xo[DQ ? 1 : kC];                 // DK: out . ext of the second group's columns
     float xs[2][4];                        // DK, O: block sums
 };
 
@@ -252,9 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
         }
         unsigned long long *one[] = {&ctl.qs_done, &ctl.kv_done, &ctl.pv_done};
         mbar_init(smem_u32(&ctl.end), 2);
-        unsigned long long *wg[] = {&ctl.s_full, &ctl.clean[0], &ctl.clean[1]};
-        mbar_init(smem_u32(&ctl.o_scaled), 256);
-        mbar_init(smem_u32(&ctl.o_free), 256);
+        unsigned long long *wg[] = {&ctl.s_full, &ctl.o_scaled, &ctl.o_free, &ctl.clean[0], &ctl.clean[1]};
         for (auto *b : one) mbar_init(smem_u32(b), 1);
         for (auto *b : wg) mbar_init(smem_u32(b), 128);
         ctl.dead = (sbase & 1023u) != 0;  // never: the tiles would be read wrongly
@@ -556,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                     // pairs whose tokens lie on either side of the chunk: the same for its every token
                     dot = warp_sum(dot);
                     if (lane == 0) ctl.sd[it & 1][wl] = dot;
-                    bar_sync(5, 128);
+                    bar_sync(3, 128);
                     if (row < rows) {
                         const float *d = ctl.sd[it & 1];
                         p.across[(size_t)(base + row) * H + h] = ((d[0] + d[1]) + (d[2] + d[3])) * f * exp2f(load_g(base));
@@ -594,10 +591,8 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
             if (C::sum && row == 0) p.gamma[(size_t)w * H + h] = from_win ? gamma : 0.f;
         });
         tc_fence_before();
-    } else if (role == 2 || (C::sum && role == 3)) {
-        // --------------------------------------------------------------- V
-        // (a summary has no outputs: two groups, every other quarter each)
-        constexpr int NG = C::sum ? 2 : 1, NQ = 4 / NG;
+    } else if (role == 2 || role == 3) {
+        // --------------------------------------------------------------- V (two groups, every other quarter each)
         const int grp = role - 2, wl = warp & 3;
         int quarters = 0;
         segments([&](int n, int a, int b, int qa, int qb) {
@@ -607,22 +602,22 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
 #pragma unroll
                     for (int x = 0; x < 4; ++x) gx[x] = row_g(base, rows, 32 * x + lane, qb);
                 const int nq = (rows + 31) / 32;
-                // this group's quarters: f0, f0 + NG, ...; the decays behind their rows, in the order of the pass
-                const int f0 = NG == 2 ? (quarters & 1) ^ grp : 0;
-                float wq[NQ];
+                // this group's quarters: f0 and f0 + 2; the decays behind their rows, in the order of the pass
+                const int f0 = (quarters & 1) ^ grp;
+                float wq[2];
                 {
                     float tot[4];
 #pragma unroll
                     for (int x = 0; x < 4; ++x) tot[x] = warp_sum(gx[x]);
 #pragma unroll
-                    for (int e = 0; e < NQ; ++e) {
-                        const float g1 = NG == 1 ? gx[e] : f0 ? gx[2 * e + 1 < 4 ? 2 * e + 1 : 3] : gx[2 * e < 4 ? 2 * e : 3];
+                    for (int e = 0; e < 2; ++e) {
+                        const float g1 = f0 ? gx[2 * e + 1] : gx[2 * e];
                         const float inc = C::rev ? scan_up(g1, lane) : scan_down(g1, lane);
                         float exc = C::rev ? __shfl_up_sync(0xffffffffu, inc, 1) : __shfl_down_sync(0xffffffffu, inc, 1);
                         if (lane == (C::rev ? 0 : 31)) exc = 0.f;
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            if (C::rev ? j < f0 + NG * e : j > f0 + NG * e) exc += tot[j];
+                            if (C::rev ? j < f0 + 2 * e : j > f0 + 2 * e) exc += tot[j];
                         wq[e] = exp2f(exc) * p.wr_scale;
                     }
                 }
@@ -631,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                     for (int x = 0; x < 4; ++x) gx[x] = row_g(next_base(base), min(kC, b - next_base(base)), 32 * x + lane, qb);
                 unsigned char *tw = sm + slot(it, C::tW) * C::slot_bytes, *tv = sm + slot(it, C::tV) * C::slot_bytes;
                 wait(ctl.full[slot(it, C::tV)], phase(it, C::tV));
-                if (rows < kC && (NG == 1 || ((quarters + nq - 1) & 1) == grp)) {
+                if (rows < kC && ((quarters + nq - 1) & 1) == grp) {
                     // The last quarter's rows behind the end hold other tokens: zero, whatever they are (the
                     // quarters behind it are not read); each thread the channels that it reads below.  Both MMA
                     // warps have passed their wait for the short chunk two before this one, if that was one:
@@ -657,11 +652,10 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                 // 32 tokens at a time: lane = token, warp = quarter of the channels
                 for (int qq = 0; qq < nq; ++qq, ++quarters) {
                     const int vb = quarters & 1;
-                    if (NG == 2 && vb != grp) continue;
+                    if (vb != grp) continue;
                     if (quarters > 1) wait(ctl.vb_free[vb], ((quarters >> 1) - 1) & 1);
                     const int r = 32 * qq + lane;
-                    const int e = qq / NG;
-                    const float f = e == 0 ? wq[0] : e == 1 ? wq[1] : wq[e == 2 ? NQ / 2 : NQ - 1];
+                    const float f = (qq >> 1) ? wq[1] : wq[0];
                     const float2 f2 = make_float2(f, f);
                     constexpr int CH = DB / 32;  // 16-byte pieces
 #pragma unroll
@@ -687,11 +681,10 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                 ++it;
             });
         });
-    } else if (role == 3 || role == 4) {
-        // --------------------------------------------------------------- O (two groups of columns)
+    } else if (role == 4) {
+        // --------------------------------------------------------------- O
         if (C::out) {
-            const int grp = role - 3, row = tid - 384 - 128 * grp, wl = warp & 3;
-            const int cb0 = grp * (DB / 64), cb1 = cb0 + DB / 64;
+            const int row = tid - 512, wl = warp & 3;
             const uint32_t lane_off = (uint32_t)(32 * wl) << 16;
             const bool al32 = ((uintptr_t)p.out & 31) == 0;
             const uint32_t to = tmem + lane_off + C::col_o;
@@ -701,12 +694,12 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                     if (i == 0) gx = row_g(base, rows, row, qb);
                     const int pb = it & 1;
                     float c = C::rev ? scan_down(gx, lane) : scan_up(gx, lane);
-                    if (lane == (C::rev ? 0 : 31)) ctl.ot[grp][pb][wl] = c;
+                    if (lane == (C::rev ? 0 : 31)) ctl.ot[pb][wl] = c;
                     if (i + 1 < nch) gx = row_g(next_base(base), min(kC, b - next_base(base)), row, qb);
-                    bar_sync(3 + grp, 128);
+                    bar_sync(2, 128);
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        if (C::rev ? j > wl : j < wl) c += ctl.ot[grp][pb][j];
+                        if (C::rev ? j > wl : j < wl) c += ctl.ot[pb][j];
                     const float f = exp2f(c) * p.rd_scale;
                     // the state's part, scaled by its rows' decays before P V is added to it
                     const size_t at = ((size_t)(base + row) * H + h) * DB;
@@ -724,12 +717,12 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                     if (XD) {
 #pragma unroll
                         for (int e = 0; e < (XD ? 4 : 0); ++e) e4[e] = make_uint4(0u, 0u, 0u, 0u);
-                        load_ext(cb0);
+                        load_ext(0);
                     }
                     wait(ctl.qs_done, it & 1);
                     tc_fence_after();
 #pragma unroll 1
-                    for (int cb = cb0; cb < cb1; ++cb) {
+                    for (int cb = 0; cb < DB / 32; ++cb) {
                         uint32_t x[32];
                         tmem_ld32_wait(to + 32 * cb, x);
 #pragma unroll
@@ -750,24 +743,19 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                                     xi = fmaf(u.y, __uint_as_float(x[8 * e + 2 * k + 1]), xi);
                                 }
                             }
-                            if (cb + 1 < cb1) load_ext(cb + 1);
+                            if (cb + 1 < DB / 32) load_ext(cb + 1);
                         }
                     }
                     tc_wait_st();
                     tc_fence_before();
                     arrive(ctl.o_scaled);
-                    if constexpr (M == DK) {  // the other group's columns of out . ext
-                        if (grp == 1) ctl.xo[row] = xi;
-                        bar_sync(6, 256);
-                        if (grp == 0) xi += ctl.xo[row];
-                    }
                     wait(ctl.pv_done, it & 1);
                     tc_fence_after();
 #pragma unroll 1
-                    for (int cb = cb0; cb < cb1; ++cb) {
+                    for (int cb = 0; cb < DB / 32; ++cb) {
                         uint32_t x[32];
                         tmem_ld32_wait(to + 32 * cb, x);
-                        if (cb == cb1 - 1) {
+                        if (cb == DB / 32 - 1) {
                             tc_fence_before();
                             arrive(ctl.o_free);
                         }
@@ -790,19 +778,19 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                         }
                     }
                     if constexpr (M == DQ) {
-                        if (row < rows) (grp ? p.xstate2 : p.xstate)[(size_t)(base + row) * H + h] = xi;
+                        if (row < rows) p.xstate[(size_t)(base + row) * H + h] = xi;
                     }
-                    if (M == DK && grp == 0) {
+                    if constexpr (M == DK) {
                         // dg but for the pairs across the chunk: the pairs inside it and those with an
                         // earlier state from this token on, those with a later state before it
                         float u = 0.f;
                         const size_t th = (size_t)(base + row) * H + h;
-                        if (row < rows) u = p.xdot[th] + (p.xstate[th] + p.xstate2[th]);
+                        if (row < rows) u = p.xdot[th] + p.xstate[th];
                         const float ik = row < rows ? xi : 0.f;
                         float suf = scan_down(u, lane), pre = scan_up(ik, lane) - ik;
                         if (lane == 0) ctl.xs[0][wl] = suf;
                         if (lane == 31) ctl.xs[1][wl] = pre + ik;
-                        bar_sync(3, 128);
+                        bar_sync(2, 128);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             if (j > wl) suf += ctl.xs[0][j];
