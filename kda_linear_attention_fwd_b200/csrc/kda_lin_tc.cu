@@ -8,7 +8,7 @@
 //   P   = scale D (.) A          fp32 from TMEM, rounded to bf16 once, back to TMEM
 //   O1  = R S                    S: bf16 copy of the state entering the chunk
 //   O   = scale exp(c_t) O1 + P V
-//   S   = exp(c_last) S + W^T (w V)
+//   S   = exp(c_last) S + W^T (w V)      (the decay kept aside, see carried)
 // The state stays in TMEM in fp32 for the whole window.  w V is split into two
 // bf16 parts (hi + lo, 2^-16 of the value), so the state that is carried and
 // returned has fp32-like accuracy; only the copy that R reads is one bf16.
@@ -25,9 +25,10 @@
 // cycles, 1.4 us).  So the chunk's serial chains have to stay hidden: every
 // step has its own warpgroup, one chunk apart at most, joined by mbarriers:
 //   warps  0- 3  P    the decayed products           (TMEM lane = token)
-//   warps  4- 7  S    the state: scaled in TMEM, bf16 copy to shared memory
-//   warps  8-15  V    w V as hi and lo parts, 32 tokens at a time into two alternating buffers,
-//                     one group each (with one group for both this is what a chunk waits for)
+//   warps  4- 7  S    the state: bf16 copy to shared memory, scaled in TMEM now and then
+//   warps  8-15  V    w V as hi and lo parts, 32 tokens at a time, every group into a buffer of
+//                     its own (with fewer groups this is what a chunk waits for; a summary,
+//                     which has no P and O, takes their warps for it too: four groups)
 //   warps 16-19  O    the outputs                    (TMEM lane = token)
 //   warp  20     TMA  tiles of 128 tokens x 64 channels, 128-byte swizzle
 //   warp  21     MMA  issues A and the state's products
@@ -98,7 +99,7 @@ struct Ctl {
     unsigned long long p_full[2];         // P is in TMEM, in A's place
     unsigned long long a_free[2];         // P V has read it
     unsigned long long s_full;            // the scaled state and its copy are in place
-    unsigned long long vb_full[2], vb_free[2];  // the hi/lo quarters, alternating
+    unsigned long long vb_full[4], vb_free[4];  // the hi/lo quarters, in turn
     unsigned long long kv_done;           // the state has this chunk's writes
     unsigned long long qs_done;           // R S is in O
     unsigned long long o_scaled;          // and multiplied by its rows' decays
@@ -131,13 +132,14 @@ struct Cfg {
     static constexpr int slot_bytes = a_bytes > b_bytes ? a_bytes : b_bytes;
     static constexpr int vb_part = DB / 64 * (32 * 128);  // 32 tokens of hi or lo
     static constexpr int vb_bytes = 2 * vb_part;
+    static constexpr int groups = sum ? 4 : 2;            // warpgroups making them, a buffer each
     static constexpr int sb_bytes = out ? DB / 64 * (DA * 128) : 0;
     static constexpr int xc_bytes = M == DQ ? 10 * 32 * 4 : 0;  // DQ: column sums of X, per warp and block
-    static constexpr int fit = (232448 - 2 * vb_bytes - sb_bytes - xc_bytes - (int)sizeof(Ctl<M == DQ>)) / slot_bytes;
+    static constexpr int fit = (232448 - groups * vb_bytes - sb_bytes - xc_bytes - (int)sizeof(Ctl<M == DQ>)) / slot_bytes;
     static constexpr int slots = fit < kMaxSlots ? fit : kMaxSlots;
     static_assert(slots > tiles, "ring");
     static constexpr int off_vb = slots * slot_bytes;
-    static constexpr int off_sb = off_vb + 2 * vb_bytes;
+    static constexpr int off_sb = off_vb + groups * vb_bytes;
     static constexpr int off_xc = off_sb + sb_bytes;
     static constexpr int off_ctl = off_xc + xc_bytes;
     static constexpr int bytes = off_ctl + (int)sizeof(Ctl<M == DQ>);
@@ -242,10 +244,12 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
             mbar_init(smem_u32(&ctl.full[i]), 1);
             mbar_init(smem_u32(&ctl.free[i]), 2);  // both MMA warps, or one twice
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&ctl.a_free[i]), 1);
+        for (int i = 0; i < C::groups; ++i) {
             mbar_init(smem_u32(&ctl.vb_full[i]), 128);
             mbar_init(smem_u32(&ctl.vb_free[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&ctl.a_free[i]), 1);
             mbar_init(smem_u32(&ctl.a_full[i]), 1);
             mbar_init(smem_u32(&ctl.p_full[i]), 128);
         }
@@ -310,10 +314,19 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
     };
     auto next_base = [&](int base) { return C::rev ? base - kC : base + kC; };
 
+    // The state in TMEM is S / 2^G: its decay is kept in G (every role that needs it computes the same) and
+    // multiplied in only when G would fall below -24, so most chunks leave the accumulator where it is.
+    // carried: G behind a chunk with the decays gx (row 32 x + lane in gx[x]); 0 when it is multiplied in.
+    auto chunk_sum = [&](const float(&gx)[4]) { return warp_sum((gx[0] + gx[1]) + (gx[2] + gx[3])); };
+    auto carried = [&](float G, const float(&gx)[4]) {
+        const float g = G + chunk_sum(gx);
+        return g < -24.f ? 0.f : g;
+    };
+
     int it = 0;  // chunks done by this role
-    if (role == 0) {
+    if (C::out && role == 0) {
         // --------------------------------------------------------------- P
-        if (C::out) {
+        {
             const int row = tid;  // 32 * warp + lane
             const uint32_t ta0 = tmem + ((uint32_t)(32 * warp) << 16) + C::col_a;
             const float sc = p.rd_scale * p.wr_scale;
@@ -475,12 +488,14 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                 }
                 tc_wait_st();
             }
-            float gx[4] = {0.f, 0.f, 0.f, 0.f};
+            float gx[4] = {0.f, 0.f, 0.f, 0.f}, G = 0.f;
             chunks(a, b, [&](int base, int rows, int i, int nch) {
                 if (i == 0)
 #pragma unroll
                     for (int x = 0; x < 4; ++x) gx[x] = row_g(base, rows, 32 * x + lane, qb);
-                const float f = exp2f(warp_sum((gx[0] + gx[1]) + (gx[2] + gx[3])));
+                const float total = chunk_sum(gx), f = exp2f(total), before = exp2f(G);
+                G = carried(G, gx);
+                const bool fold = G == 0.f && total < 0.f;  // multiply the decays so far and this chunk's in
                 gamma *= f;
                 if (i + 1 < nch)
 #pragma unroll
@@ -497,11 +512,20 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                     tc_fence_after();
                 }
                 float dot = 0.f;
-                if (mine) {
+                if (mine && (C::out || fold)) {
+                    auto scale = [](uint32_t(&r)[32], float x) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const float2 v = f2mul(make_float2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])), make_float2(x, x));
+                            r[2 * e] = __float_as_uint(v.x);
+                            r[2 * e + 1] = __float_as_uint(v.y);
+                        }
+                    };
 #pragma unroll 1
                     for (int cb = 0; cb < DB / 32; ++cb) {
                         uint32_t r[32];
                         tmem_ld32_wait(ts + 32 * cb, r);
+                        scale(r, before);
                         if (C::out) {  // the copy that R reads: [DA rows][64 channels] boxes, 128-byte swizzle
                             unsigned char *box = sm + C::off_sb + (cb >> 1) * (DA * 128) + row * 128;
 #pragma unroll
@@ -535,14 +559,10 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                                 }
                             }
                         }
-                        const float2 f2 = make_float2(f, f);
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const float2 v = f2mul(make_float2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])), f2);
-                            r[2 * e] = __float_as_uint(v.x);
-                            r[2 * e + 1] = __float_as_uint(v.y);
+                        if (fold) {
+                            scale(r, f);
+                            tmem_st32(ts + 32 * cb, r);
                         }
-                        tmem_st32(ts + 32 * cb, r);
                     }
                     tc_wait_st();
                 }
@@ -570,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                 tc_fence_after();
             }
             if (dst && mine) {
-                const float f = !C::sum && C::rev && b > a ? exp2f(load_g(a)) : 1.f;
+                const float f = exp2f(!C::sum && C::rev && b > a ? G + load_g(a) : G);
 #pragma unroll 1
                 for (int cb = 0; cb < DB / 32; ++cb) {
                     uint32_t r[32];
@@ -591,10 +611,12 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
             if (C::sum && row == 0) p.gamma[(size_t)w * H + h] = from_win ? gamma : 0.f;
         });
         tc_fence_before();
-    } else if (role == 2 || role == 3) {
-        // --------------------------------------------------------------- V (two groups, every other quarter each)
-        const int grp = role - 2, wl = warp & 3;
+    } else if (role == 2 || role == 3 || (C::sum && role < 5)) {
+        // --------------------------------------------------------------- V (each group every NG-th quarter)
+        constexpr int NG = C::groups;
+        const int grp = NG == 2 ? role - 2 : role == 0 ? 0 : role - 1, wl = warp & 3;
         int quarters = 0;
+        float G = 0.f;
         segments([&](int n, int a, int b, int qa, int qb) {
             float gx[4] = {0.f, 0.f, 0.f, 0.f};
             chunks(a, b, [&](int base, int rows, int i, int nch) {
@@ -602,23 +624,26 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
 #pragma unroll
                     for (int x = 0; x < 4; ++x) gx[x] = row_g(base, rows, 32 * x + lane, qb);
                 const int nq = (rows + 31) / 32;
-                // this group's quarters: f0 and f0 + 2; the decays behind their rows, in the order of the pass
-                const int f0 = (quarters & 1) ^ grp;
-                float wq[2];
+                if (i == 0) G = 0.f;
+                G = carried(G, gx);
+                // this group's quarters: f0, f0 + NG; the decays behind their rows, in the order of the pass
+                const int f0 = (grp - quarters) & (NG - 1);
+                float wq[4 / NG];
                 {
                     float tot[4];
 #pragma unroll
                     for (int x = 0; x < 4; ++x) tot[x] = warp_sum(gx[x]);
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float g1 = f0 ? gx[2 * e + 1] : gx[2 * e];
+                    for (int e = 0; e < 4 / NG; ++e) {
+                        const float g1 = NG == 2 ? (f0 ? gx[2 * e + 1] : gx[2 * e])
+                                                 : f0 == 0 ? gx[0] : f0 == 1 ? gx[1] : f0 == 2 ? gx[2] : gx[3];
                         const float inc = C::rev ? scan_up(g1, lane) : scan_down(g1, lane);
                         float exc = C::rev ? __shfl_up_sync(0xffffffffu, inc, 1) : __shfl_down_sync(0xffffffffu, inc, 1);
                         if (lane == (C::rev ? 0 : 31)) exc = 0.f;
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            if (C::rev ? j < f0 + 2 * e : j > f0 + 2 * e) exc += tot[j];
-                        wq[e] = exp2f(exc) * p.wr_scale;
+                            if (C::rev ? j < f0 + NG * e : j > f0 + NG * e) exc += tot[j];
+                        wq[e] = exp2f(exc - G) * p.wr_scale;
                     }
                 }
                 if (i + 1 < nch)
@@ -626,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                     for (int x = 0; x < 4; ++x) gx[x] = row_g(next_base(base), min(kC, b - next_base(base)), 32 * x + lane, qb);
                 unsigned char *tw = sm + slot(it, C::tW) * C::slot_bytes, *tv = sm + slot(it, C::tV) * C::slot_bytes;
                 wait(ctl.full[slot(it, C::tV)], phase(it, C::tV));
-                if (rows < kC && ((quarters + nq - 1) & 1) == grp) {
+                if (rows < kC && ((quarters + nq - 1) & (NG - 1)) == grp) {
                     // The last quarter's rows behind the end hold other tokens: zero, whatever they are (the
                     // quarters behind it are not read); each thread the channels that it reads below.  Both MMA
                     // warps have passed their wait for the short chunk two before this one, if that was one:
@@ -651,11 +676,11 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                 }
                 // 32 tokens at a time: lane = token, warp = quarter of the channels
                 for (int qq = 0; qq < nq; ++qq, ++quarters) {
-                    const int vb = quarters & 1;
+                    const int vb = quarters & (NG - 1);
                     if (vb != grp) continue;
-                    if (quarters > 1) wait(ctl.vb_free[vb], ((quarters >> 1) - 1) & 1);
+                    if (quarters >= NG) wait(ctl.vb_free[vb], (quarters / NG - 1) & 1);
                     const int r = 32 * qq + lane;
-                    const float f = (qq >> 1) ? wq[1] : wq[0];
+                    const float f = qq < NG ? wq[0] : wq[4 / NG - 1];
                     const float2 f2 = make_float2(f, f);
                     constexpr int CH = DB / 32;  // 16-byte pieces
 #pragma unroll
@@ -913,8 +938,8 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                 const uint32_t tw = tile(it, C::tW);
                 wait(ctl.s_full, it & 1);
                 auto quarter = [&](int qq) {
-                    const int vbuf = quarters & 1;
-                    wait(ctl.vb_full[vbuf], (quarters >> 1) & 1);
+                    const int vbuf = quarters & (C::groups - 1);
+                    wait(ctl.vb_full[vbuf], (quarters / C::groups) & 1);
                     tc_fence_after();
                     const uint32_t vb = sbase + C::off_vb + vbuf * C::vb_bytes;
                     if (elect_one_sync()) {
