@@ -377,6 +377,14 @@ int kda_bwd(const void *q, const void *k, const void *v, const void *g, const vo
  * Tokens outside every sequence (behind cu_seqlens[num_seqs], when the host
  * copy is not given) are neither read nor written; device offsets that are
  * not monotone are clamped into [0, total_tokens] and give undefined values.
+ * Every device wait is bounded; one that gave up is recorded in the first
+ * words of the workspace, which kda_chunk_fwd_check reads (KDA_ERR_TIMEOUT).
+ *
+ * Rounding (BF16): fp32 accumulation throughout; the products inside a
+ * 128-token chunk and the state that q reads are rounded to bf16 once as
+ * operands (outputs within about 2.6e-3 of exact in the 2-norm), the carried
+ * and returned states are fp32 with products of two bf16 parts (about 4e-6).
+ * F32 inputs are computed in fp32 throughout.
  */
 #define KDA_LIN_DECAY_PER_HEAD 1 /* g is [H] (and dg [H]): the same decay at every token */
 

@@ -95,6 +95,7 @@ KDA_DEVICE void rec_body(const Params &p, unsigned char *smem_raw) {
     const int col0 = (warp * CGW + lane % CGW) * 4;
     const int h = blockIdx.x, w = blockIdx.y;
     const int H = p.H;
+    if (h == 0 && w == 0 && tid < 3 && p.clear_err) p.err[tid] = 0;  // no wait here can give up
     const Window wd = window_of(p, w, reinterpret_cast<int *>(&sm.fdot[0]));
     const int t0 = wd.t0, t1 = wd.t1, lo = wd.lo;
     let_next_start();
@@ -485,7 +486,9 @@ static cudaError_t launch_one(const Params &p, cudaStream_t st, bool follows) {
     static std::atomic<uint64_t> done;
     cudaError_t e = allow_smem(done, (const void *)rec_kernel<DA, DB, M>, bytes);
     if (e != cudaSuccess) return e;
-    return launch(rec_kernel<DA, DB, M>, dim3(p.H, p.W), kThreads, bytes, st, follows, p);
+    Params q = p;
+    q.clear_err = !follows;
+    return launch(rec_kernel<DA, DB, M>, dim3(p.H, p.W), kThreads, bytes, st, follows, q);
 }
 template <int DA, int DB, int M, int DA2, int DB2, int M2>
 static cudaError_t launch_two(const Params &p, const Params &p2, cudaStream_t st, bool follows) {
@@ -493,7 +496,9 @@ static cudaError_t launch_two(const Params &p, const Params &p2, cudaStream_t st
     static std::atomic<uint64_t> done;
     cudaError_t e = allow_smem(done, (const void *)rec_pair_kernel<DA, DB, M, DA2, DB2, M2>, bytes);
     if (e != cudaSuccess) return e;
-    return launch(rec_pair_kernel<DA, DB, M, DA2, DB2, M2>, dim3(p.H, p.W, 2), kThreads, bytes, st, follows, p, p2);
+    Params q = p;
+    q.clear_err = !follows;
+    return launch(rec_pair_kernel<DA, DB, M, DA2, DB2, M2>, dim3(p.H, p.W, 2), kThreads, bytes, st, follows, q, p2);
 }
 
 template <int DK_, int DV_>

@@ -372,6 +372,15 @@ def _launch(fn, dev, stream, *args):
         _check(fn.__name__, st)
 
 
+def _keep(stream, *tensors):
+    """Tensors made here for a call on another stream than their own: not to be
+    given out again before that stream has passed the call."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
 def _tensor(name, t, shape, dtype, dev):
     """Address of a tensor, refused when the kernels could not read it as it is."""
     if t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous():
@@ -461,8 +470,9 @@ def lin_chunk_fwd(q, k, v, g, cu_seqlens, *, scale=1.0, initial_state=None, fina
     p_s1 = _opt("final_state", final_state, states, torch.float32, dev)
     host = _host_offsets(cu_seqlens_host, N)
     ws, p_ws, n_ws = _space(workspace, dev, lambda: lib.kda_lin_chunk_fwd_workspace_size(T, N, H, Hk, dk, dv, code))
-    _launch(lib.kda_lin_chunk_fwd, dev, stream, *ptrs, p_out, p_cu, host, N, T, H, Hk, dk, dv, code, scale, flags,
+    _launch(lib.kda_lin_chunk_fwd, dev, stream, *ptrs, p_out, p_cu, host, N, T, H, Hk, dk, dv, code, float(scale), flags,
             p_s0, p_s1, p_ws, n_ws)
+    _keep(stream, ws, out, final_state)
     return out, final_state
 
 
@@ -475,7 +485,8 @@ def lin_decode_step(q, k, v, g, state, *, scale=1.0, out=None, stream=None):
         out = torch.empty_like(v)
     p_out = _tensor("out", out, v.shape, q.dtype, dev)
     p_s = _tensor("state", state, (N, H, dk, dv), torch.float32, dev)
-    _launch(lib.kda_lin_decode_step, dev, stream, *ptrs, p_out, p_s, N, H, Hk, dk, dv, code, scale, flags)
+    _launch(lib.kda_lin_decode_step, dev, stream, *ptrs, p_out, p_s, N, H, Hk, dk, dv, code, float(scale), flags)
+    _keep(stream, out)
     return out
 
 
@@ -502,8 +513,9 @@ def lin_bwd(q, k, v, g, dy, cu_seqlens, *, scale=1.0, initial_state=None, d_fina
            "ds0": q.new_empty(states, dtype=torch.float32)}
     host = _host_offsets(cu_seqlens_host, N)
     ws, p_ws, n_ws = _space(workspace, dev, lambda: lib.kda_lin_bwd_workspace_size(T, N, H, Hk, dk, dv))
-    _launch(lib.kda_lin_bwd, dev, stream, *ptrs, p_dy, p_cu, host, N, T, H, Hk, dk, dv, code, scale, flags, p_s0, p_ds,
+    _launch(lib.kda_lin_bwd, dev, stream, *ptrs, p_dy, p_cu, host, N, T, H, Hk, dk, dv, code, float(scale), flags, p_s0, p_ds,
             *(x.data_ptr() for x in out.values()), p_ws, n_ws)
+    _keep(stream, ws, *out.values())
     return out
 
 
@@ -557,7 +569,8 @@ def block_norm(y, *, post_norm=True, post_weight=None, gate=None, gate_logits=Fa
         normed = y.new_empty(shape)
     p_out, p_n = _tensor("out", out, shape, dt, dev), _opt("normed", normed, shape, dt, dev)
     _launch(lib.kda_block_norm, dev, stream, p_y, s_y, p_wp, p_g, s_g, p_x, s_x, p_wn, p_out, p_n,
-            y.numel() // D if D else 0, D, code, res_scale, eps, flags)
+            y.numel() // D if D else 0, D, code, float(res_scale), float(eps), flags)
+    _keep(stream, out, normed)
     return out, normed
 
 
@@ -589,5 +602,6 @@ def block_norm_bwd(dout, dnormed, y, *, post_norm=True, post_weight=None, gate=N
            "dpost_weight": like(post_weight, (D,), torch.float32), "dpre_weight": like(pre_weight, (D,), torch.float32)}
     ws, p_ws, n_ws = _space(workspace, dev, lambda: lib.kda_block_norm_bwd_workspace_size(rows, D, code))
     _launch(lib.kda_block_norm_bwd, dev, stream, p_do, p_dn, p_y, s_y, p_wp, p_g, s_g, p_x, s_x, p_wn,
-            *(None if t is None else t.data_ptr() for t in got.values()), rows, D, code, res_scale, eps, flags, p_ws, n_ws)
+            *(None if t is None else t.data_ptr() for t in got.values()), rows, D, code, float(res_scale), float(eps), flags, p_ws, n_ws)
+    _keep(stream, ws, *got.values())
     return got

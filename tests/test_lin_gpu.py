@@ -380,8 +380,56 @@ def test_gradients_of_rows_behind_the_last_sequence(cuda_lib, dtype, per_head):
         near(g, np32(want[name]), TOL[DT[dtype]], name)
 
 
-def test_the_workspace_reports_no_error(cuda_lib):
-    d = make((300, 40), 2, 2, 64, 128, "bf16", seed=24)
-    ws = torch.full((kda.lin_workspace_size(340, 2, 2, 2, 64, 128),), 255, dtype=torch.uint8, device="cuda")
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_the_workspace_reports_no_error(cuda_lib, dtype):
+    d = make((300, 40), 2, 2, 64, 128, dtype, seed=24)
+    ws = torch.full((kda.lin_workspace_size(340, 2, 2, 2, 64, 128, DT[dtype]),), 255, dtype=torch.uint8, device="cuda")
     kda.lin_chunk_fwd(d["q"], d["k"], d["v"], d["g"], d["cu"], workspace=ws)
     assert kda.chunk_fwd_check(ws) == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_no_tokens_at_all(cuda_lib, dtype):
+    """Empty sequences only: states pass through, forward and backward."""
+    d = make((0, 0, 0), 2, 1, 64, 128, dtype, per_head=True, seed=25)
+    out, fin = kda.lin_chunk_fwd(d["q"], d["k"], d["v"], d["g"], d["cu"], initial_state=d["s0"])
+    assert out.shape == (0, 2, 128) and torch.equal(fin, d["s0"])
+    got = kda.lin_bwd(d["q"], d["k"], d["v"], d["g"], d["dy"], d["cu"], initial_state=d["s0"], d_final_state=d["dsf"])
+    assert torch.equal(got["ds0"], d["dsf"]) and (got["dg"] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_sequences_as_windows(cuda_lib, dtype):
+    """Enough sequences and heads that a CTA takes a whole sequence when the host
+    knows the lengths: the same results as through windows, and the oracle's."""
+    lengths = (257, 0, 64, 500, 1, 130, 128, 300, 90, 411, 2, 350)
+    d = make(lengths, 48, 24, 64, 64, dtype, seed=26)
+    kw = dict(scale=0.5, initial_state=d["s0"])
+    a = kda.lin_chunk_fwd(d["q"], d["k"], d["v"], d["g"], d["cu"], cu_seqlens_host=d["host"], **kw)
+    b = kda.lin_chunk_fwd(d["q"], d["k"], d["v"], d["g"], d["cu"], **kw)
+    for x, y, tol in zip(a, b, (TOL[DT[dtype]], 2e-5)):
+        near(x, np32(y), tol, "by sequence")
+    o, S = O.forward(np32(d["q"]), np32(d["k"]), np32(d["v"]), np32(d["g"]), d["host"], scale=0.5, initial_state=np32(d["s0"]))
+    near(a[0], o, TOL[DT[dtype]], "out")
+    near(a[1], S, 2e-5, "state")
+    args = (d["q"], d["k"], d["v"], d["g"], d["dy"], d["cu"])
+    a = kda.lin_bwd(*args, d_final_state=d["dsf"], cu_seqlens_host=d["host"], **kw)
+    b = kda.lin_bwd(*args, d_final_state=d["dsf"], **kw)
+    for name in a:
+        near(a[name], np32(b[name]), 2e-5 if name == "ds0" else 2 * TOL[DT[dtype]], name)
+
+
+def test_a_call_on_another_stream_keeps_its_memory(cuda_lib):
+    """Workspace and results made inside a call on a given stream are not handed
+    out to the current one before that stream has passed the call."""
+    d = make((3000,), 8, 8, 128, 128, "bf16", seed=27)
+    want, fin = kda.lin_chunk_fwd(d["q"], d["k"], d["v"], d["g"], d["cu"], initial_state=d["s0"])
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(5):
+        out, s = kda.lin_chunk_fwd(d["q"], d["k"], d["v"], d["g"], d["cu"], initial_state=d["s0"], stream=side)
+        junk = [torch.full((1 << 22,), float("nan"), device="cuda") for _ in range(4)]  # on the current stream
+        side.synchronize()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(s, fin)
+        del junk, out, s
