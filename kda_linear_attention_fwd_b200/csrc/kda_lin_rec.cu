@@ -11,15 +11,16 @@
 //     hold S / e^G with G the log-decay summed since the last renormalisation;
 //     a write adds k (v e^-G)^T and a read is scaled by e^G.  The state is
 //     renormalised (one multiply per element) every 16 tokens, and at every
-//     token of a group of four over which G falls below -40, so e^-G stays in range and G is always a short
-//     sum (its rounding is what limits the decay's accuracy);
+//     token of a group of four over which G falls below -40, so e^-G stays in
+//     range and G is always a short sum (its rounding is what limits the
+//     decay's accuracy);
 //   * a warp's 32 lanes are RG row groups x CGW column groups, each thread
 //     holding RT rows x 4 columns, so the vectors come from shared memory as
 //     broadcast 16-byte reads (17 reads for 256 FMAs at 128 x 128);
 //   * four tokens at a time: their partial outputs are summed over the row
 //     groups together (12 shuffles, after which a lane holds one token's four
 //     columns), so that the sums of one token do not hold up the next.
-// Tokens arrive 16 at a time by cp.async, one block ahead.
+// Tokens arrive 16 at a time by cp.async, up to three blocks ahead.
 //
 // The gradient in the same form (B_t = dL/dS_t, L = sum o . do + <dS_T, S_T>):
 //   B_t = exp(g_{t+1}) B_{t+1} + scale q_t do_t^T
@@ -29,8 +30,10 @@
 // reversed one with (read v, write do, value q), dv with (read k, write q,
 // value do), so one kernel makes all three.  dg uses
 //   <exp(g_t) S_{t-1}, B_t> = <S_e, exp(g_{e+1}) B_{e+1}>
-//                             + sum_{t<=s<=e} (q_s . dq_s - k_s . dk_s),
-// e being the last token of t's 64-token chunk: the dq pass leaves S_e of
+//                             + sum_{t<=s<=e} (q_s . dq'_s - k_s . dk'_s),
+// dq', dk' without the term of the token itself (q_s . k_s)(do_s . v_s), which
+// both have: they read the state before the write, so that for strong decays
+// both are as small as dg and nothing cancels.  e being the last token of t's 64-token chunk: the dq pass leaves S_e of
 // every chunk in the workspace and the dk pass takes the product with its own
 // state there, so the sums that cancel are at most 64 tokens long.
 #include "kda_common.cuh"
@@ -248,7 +251,7 @@ KDA_DEVICE void rec_body(const Params &p, unsigned char *smem_raw) {
                         wf[e] = on ? (slow ? 1.f : __expf(-G)) * p.wr_scale : 0.f;
                         rf[e] = (slow ? 1.f : __expf(G)) * p.rd_scale;
                     }
-                    float o[4][4];
+                    float o[4][4], dd[4] = {0.f, 0.f, 0.f, 0.f};  // dd: rd . wr of the token (gradient passes)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int j = MO::rev ? j0 + 3 - e : j0 + e;
@@ -262,13 +265,21 @@ KDA_DEVICE void rec_body(const Params &p, unsigned char *smem_raw) {
                             for (int i = 0; i < NQ; ++i) {
                                 const float4 k4 = ld4(&S.wr[j][row_of(i, 0)]);
                                 const float k[4] = {k4.x, k4.y, k4.z, k4.w};
+                                const float4 q4 = MO::out ? ld4(&S.rd[j][row_of(i, 0)]) : k4;
+                                const float q[4] = {q4.x, q4.y, q4.z, q4.w};
+                                if constexpr (MO::xd) {  // read before the write
+#pragma unroll
+                                    for (int r = 0; r < 4; ++r) {
+                                        dd[e] = fmaf(q[r], k[r], dd[e]);
+#pragma unroll
+                                        for (int c = 0; c < 4; ++c) o[e][c] = fmaf(q[r], s[i][r][c], o[e][c]);
+                                    }
+                                }
 #pragma unroll
                                 for (int r = 0; r < 4; ++r)
 #pragma unroll
                                     for (int c = 0; c < 4; ++c) s[i][r][c] = fmaf(k[r], vs[c], s[i][r][c]);
-                                if constexpr (MO::out) {
-                                    const float4 q4 = ld4(&S.rd[j][row_of(i, 0)]);
-                                    const float q[4] = {q4.x, q4.y, q4.z, q4.w};
+                                if constexpr (MO::out && !MO::xd) {
 #pragma unroll
                                     for (int r = 0; r < 4; ++r)
 #pragma unroll
@@ -293,26 +304,37 @@ KDA_DEVICE void rec_body(const Params &p, unsigned char *smem_raw) {
                         const int j = MO::rev ? j0 + 3 - mine : j0 + mine;
                         const bool on = j < rows && (!slow || mine == only);
                         const size_t at = ((size_t)(base + j) * H + h) * DB + col0;
-                        float x1 = 0.f;
+                        float x1 = 0.f, own = 0.f;  // own: the token's write as it reads it
+                        if constexpr (MO::xd) {
+                            const float d0 = (hi ? dd[2] : dd[0]) + __shfl_xor_sync(0xffffffffu, hi ? dd[0] : dd[2], 16);
+                            const float d1 = (hi ? dd[3] : dd[1]) + __shfl_xor_sync(0xffffffffu, hi ? dd[1] : dd[3], 16);
+                            own = (mid ? d1 : d0) + __shfl_xor_sync(0xffffffffu, mid ? d0 : d1, 8);
+                            if constexpr (RG == 8) own += __shfl_xor_sync(0xffffffffu, own, 4);
+                            own *= p.rd_scale * p.wr_scale;
+                        }
                         if constexpr (RG == 8) {
                             const bool up = lane & 4;
                             const float a0 = ((up ? z[2] : z[0]) + __shfl_xor_sync(0xffffffffu, up ? z[0] : z[2], 4)) * r;
                             const float a1 = ((up ? z[3] : z[1]) + __shfl_xor_sync(0xffffffffu, up ? z[1] : z[3], 4)) * r;
                             const int c = up ? 2 : 0;
                             if (on) {
-                                *reinterpret_cast<float2 *>((float *)p.out + at + c) = make_float2(a0, a1);
+                                float2 a = make_float2(a0, a1);
                                 if constexpr (MO::xd) {
                                     const float2 e2 = *reinterpret_cast<const float2 *>(&S.ext[j][col0 + c]);
-                                    x1 = a0 * e2.x + a1 * e2.y;
+                                    const float2 v2 = *reinterpret_cast<const float2 *>(&S.val[j][col0 + c]);
+                                    x1 = a.x * e2.x + a.y * e2.y;
+                                    a = make_float2(fmaf(own, v2.x, a.x), fmaf(own, v2.y, a.y));
                                 }
+                                *reinterpret_cast<float2 *>((float *)p.out + at + c) = a;
                             }
                         } else if (on) {
-                            const float4 a = make_float4(z[0] * r, z[1] * r, z[2] * r, z[3] * r);
-                            *reinterpret_cast<float4 *>((float *)p.out + at) = a;
+                            float4 a = make_float4(z[0] * r, z[1] * r, z[2] * r, z[3] * r);
                             if constexpr (MO::xd) {
-                                const float4 e4 = ld4(&S.ext[j][col0]);
+                                const float4 e4 = ld4(&S.ext[j][col0]), v4 = ld4(&S.val[j][col0]);
                                 x1 = (a.x * e4.x + a.y * e4.y) + (a.z * e4.z + a.w * e4.w);
+                                a = make_float4(fmaf(own, v4.x, a.x), fmaf(own, v4.y, a.y), fmaf(own, v4.z, a.z), fmaf(own, v4.w, a.w));
                             }
+                            *reinterpret_cast<float4 *>((float *)p.out + at) = a;
                         }
                         if constexpr (MO::xd) {
 #pragma unroll

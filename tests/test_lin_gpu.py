@@ -433,3 +433,16 @@ def test_a_call_on_another_stream_keeps_its_memory(cuda_lib):
         torch.cuda.synchronize()
         assert torch.equal(out, want) and torch.equal(s, fin)
         del junk, out, s
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("g", [-5.0, -1.0, -0.05])
+def test_dg_of_strong_and_weak_decays(cuda_lib, dtype, g):
+    """Every head alike, so that no head with a long memory hides the others: with
+    g = -5 dg is 150 times smaller than the terms q . dq and k . dk themselves."""
+    d = make((300, 70), 2, 2, 64, 128, dtype, s0=False, seed=28)
+    d["g"] = torch.full_like(d["g"], g)
+    got = kda.lin_bwd(d["q"], d["k"], d["v"], d["g"], d["dy"], d["cu"], scale=0.5)
+    ref = O.backward(np32(d["q"]), np32(d["k"]), np32(d["v"]), np32(d["g"]), d["host"], np32(d["dy"]), scale=0.5)
+    near(got["dg"], ref["dg"], TOL[DT[dtype]], "dg")
+    assert (got["dg"][[0, 300]] == 0).all()
