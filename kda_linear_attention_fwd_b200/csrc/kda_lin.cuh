@@ -68,7 +68,7 @@ struct Params {
     // gradient passes
     float *xdot;            // [T][H]: q . dq, written by the dq pass, read by the dk pass
     void *ckpt;             // [slots][H][DA][DB]: fp32: in fp32 passes the state after each 64-token chunk, in
-                            // bf16 passes, before each 128-token chunk
+                            // bf16 passes, before each 128-token chunk, as [DB / 4][DA][4]
     float *xstate, *across;  // bf16 passes, [T][H]: see kda_lin_tc.cu
     void *dg;               // [T][H], input type, or fp32 when g_per_head
     int zero_first_dg;      // no initial state: d(first log-decay) is exactly 0

@@ -31,11 +31,19 @@
 // value do), so one kernel makes all three.  dg uses
 //   <exp(g_t) S_{t-1}, B_t> = <S_e, exp(g_{e+1}) B_{e+1}>
 //                             + sum_{t<=s<=e} (q_s . dq'_s - k_s . dk'_s),
-// dq', dk' without the term of the token itself (q_s . k_s)(do_s . v_s), which
-// both have: they read the state before the write, so that for strong decays
-// both are as small as dg and nothing cancels.  e being the last token of t's 64-token chunk: the dq pass leaves S_e of
-// every chunk in the workspace and the dk pass takes the product with its own
-// state there, so the sums that cancel are at most 64 tokens long.
+// e being the last token of t's 64-token chunk, and dq', dk' being without the
+// term of the token itself, (q_s . k_s)(do_s . v_s), which both have: they read
+// the state before the write, so that for strong decays both are as small as dg
+// and nothing cancels.  The dq pass leaves S_e of every chunk in the workspace
+// and the dk pass takes the product with its own state there, so the sums that
+// cancel are at most 64 tokens long.
+//
+// What bounds it: the fp32 FMAs.  Two per state element and token are
+// 2 x 128 x 64 x 148 SMs' share of the 74 TFLOP/s that plain FMAs reach; the
+// ragged gradient (1023 tokens of 9 sequences x 16 heads over 4, 128 x 64: about
+// 1.5 GFLOP of them) takes 175 us (floor of its bytes 7 us), the longest
+// sequence being cut into windows for the SMs; the rest is the latency of a
+// token group's chain: read, sum over the lanes, store.
 #include "kda_common.cuh"
 #include "kda_lin.cuh"
 #include "kda_sm100.cuh"

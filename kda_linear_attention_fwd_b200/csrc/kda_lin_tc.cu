@@ -6,8 +6,8 @@
 // D[t][s] = exp(c_t - c_s) for s <= t and w_s = exp(c_last - c_s), a chunk is
 //   A   = R W^T                  R: the read vectors (q), W: the write vectors (k)
 //   P   = scale D (.) A          fp32 from TMEM, rounded to bf16 once, back to TMEM
-//   O1  = R S                    S: bf16 copy of the state entering the chunk
-//   O   = scale exp(c_t) O1 + P V
+//   O   = R S                    S: bf16 copy of the state entering the chunk
+//   O   = scale exp(c_t) O + P V (scaled in TMEM, then added to)
 //   S   = exp(c_last) S + W^T (w V)      (the decay kept aside, see carried)
 // The state stays in TMEM in fp32 for the whole window.  w V is split into two
 // bf16 parts (hi + lo, 2^-16 of the value), so the state that is carried and
@@ -32,10 +32,19 @@
 //   warps 16-19  O    the outputs                    (TMEM lane = token)
 //   warp  20     TMA  tiles of 128 tokens x 64 channels, 128-byte swizzle
 //   warp  21     MMA  issues A and the state's products
-//   warp  22     MMA  issues R S and P V (one warp for all four kinds spent more on
-//                     its waits, about 150 cycles each, than the tensor pipe on them)
-// Shared memory (128 x 128): W and V tiles twice (128 KB), R, the hi/lo buffers
-// and the state copy (32 KB each).
+//   warp  22     MMA  issues R S and P V, whose waits are other ones than the state's
+// Shared memory (128 x 128): a ring of five tiles of 32 KB (R, W, V of the
+// chunks in turn), two hi/lo buffers of 16 KB (four in a summary, with the
+// place of the state's copy) and the copy of the state (32 KB).  TMEM: the state 128
+// columns, A (P in its place) two buffers of 128, O 128.
+//
+// Measured on one B200 (6531 GB/s copied, 1653 TFLOP/s): 131072 x 32 heads of
+// 128 x 128 in 1715 us (floor 658: summary 680, scan, outputs 1030), at the
+// 1000 W cap (1.75 GHz); 65536 tokens in 40 ragged sequences x 16 heads 292 us
+// (floor 119).  A chunk takes about 4.5 us where its products take 1.4 and its
+// bytes 3.0: DRAM is at a third, the tensor pipe at 22%; what is left is the
+// chain w V -> state -> its copy -> R S -> scaling -> P V -> O of a chunk, a
+// third of it instruction fetch and barrier latency.
 //
 // The gradient (kda_lin_rec.cu has the formulas) is three such passes: dq
 // (read do, write v, value k), dk and dv reversed.  Its dg_t is the sum of
@@ -55,7 +64,8 @@
 // The kernel's code is long for what an SM holds of it close by, and a warp that
 // runs each instruction once per chunk (the MMA warps above all) waits for its
 // code longer than for anything else; so the products are loops, the slow part of
-// a wait is a call, and what a chunk does not need is kept out of its loop.
+// a wait is a call, and what a chunk does not need is kept out of its loop (with
+// these three 131072 x 32 went from 1904 to 1736 us).
 //
 // Every wait is bounded (2 s): one that gives up marks the workspace's error
 // word and the CTA, whose remaining waits then return at once; the loads and
@@ -158,6 +168,17 @@ KDA_DEVICE void st_global32(void *p, const uint32_t (&r)[8], bool aligned32) {
     asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
                  "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
+}
+KDA_DEVICE void ld_global32(uint4 (&r)[2], const void *p, bool aligned32) {
+    if (!aligned32) {
+        r[0] = reinterpret_cast<const uint4 *>(p)[0];
+        r[1] = reinterpret_cast<const uint4 *>(p)[1];
+        return;
+    }
+    asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0].x), "=r"(r[0].y), "=r"(r[0].z), "=r"(r[0].w), "=r"(r[1].x), "=r"(r[1].y), "=r"(r[1].z),
+                   "=r"(r[1].w)
+                 : "l"(p));
 }
 KDA_DEVICE float exp2_fast(float x) {
     float y;
@@ -501,11 +522,12 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
 #pragma unroll
                     for (int x = 0; x < 4; ++x) gx[x] = row_g(next_base(base), min(kC, b - next_base(base)), 32 * x + lane, qb);
                 float *ck = nullptr;
-                if (M == DQ || M == DK) ck = (float *)p.ckpt + (((size_t)(base / kC + n)) * H + h) * (DA * DB) + (size_t)row * DB;
+                // four columns of all rows, then the next four: a warp's 16-byte accesses are 512 bytes in a row
+                if (M == DQ || M == DK) ck = (float *)p.ckpt + (((size_t)(base / kC + n)) * H + h) * (DA * DB) + 4 * row;
                 float4 cv[M == DK ? 4 : 1];  // DK: 16 columns of the checkpoint, requested one round ahead
                 if (M == DK && mine)
 #pragma unroll
-                    for (int e = 0; e < (M == DK ? 4 : 0); ++e) cv[e] = *reinterpret_cast<const float4 *>(ck + 4 * e);
+                    for (int e = 0; e < (M == DK ? 4 : 0); ++e) cv[e] = *reinterpret_cast<const float4 *>(ck + 4 * DA * e);
                 if (i > 0) {
                     wait(ctl.kv_done, (it - 1) & 1);
                     if (C::out) wait(ctl.qs_done, (it - 1) & 1);  // the copy has been read
@@ -541,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                         if constexpr (M == DQ) {
 #pragma unroll
                             for (int e = 0; e < 8; ++e)
-                                *reinterpret_cast<uint4 *>(ck + 32 * cb + 4 * e) =
+                                *reinterpret_cast<uint4 *>(ck + DA * (32 * cb + 4 * e)) =
                                     make_uint4(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]);
                         }
                         if constexpr (M == DK) {
@@ -551,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
 #pragma unroll
                                 for (int e = 0; e < 4; ++e) {
                                     const float4 v = cv[e];
-                                    if (at + 16 < DB) cv[e] = *reinterpret_cast<const float4 *>(ck + at + 16 + 4 * e);
+                                    if (at + 16 < DB) cv[e] = *reinterpret_cast<const float4 *>(ck + DA * (at + 16 + 4 * e));
                                     dot = fmaf(v.x, __uint_as_float(r[16 * half + 4 * e]), dot);
                                     dot = fmaf(v.y, __uint_as_float(r[16 * half + 4 * e + 1]), dot);
                                     dot = fmaf(v.z, __uint_as_float(r[16 * half + 4 * e + 2]), dot);
@@ -731,17 +753,18 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                     const float2 f2 = make_float2(f, f);
                     float xi = 0.f;  // gradient passes: the state's part of out . ext
                     constexpr bool XD = M == DQ || M == DK;
-                    uint4 e4[XD ? 4 : 1];  // 32 channels of ext, requested one round ahead
+                    const bool ext32 = ((uintptr_t)p.ext & 31) == 0;
+                    uint4 e4[XD ? 2 : 1][2];  // 32 channels of ext, requested one round ahead
                     auto load_ext = [&](int cb) {
-                        const uint4 *src = reinterpret_cast<const uint4 *>(
-                            (const bf16 *)p.ext + ((size_t)(base + row) * (H / p.ext_div) + h / p.ext_div) * DB + 32 * cb);
+                        const bf16 *src =
+                            (const bf16 *)p.ext + ((size_t)(base + row) * (H / p.ext_div) + h / p.ext_div) * DB + 32 * cb;
                         if (XD && row < rows)
 #pragma unroll
-                            for (int e = 0; e < (XD ? 4 : 0); ++e) e4[e] = src[e];
+                            for (int e = 0; e < (XD ? 2 : 0); ++e) ld_global32(e4[e], src + 16 * e, ext32);
                     };
                     if (XD) {
 #pragma unroll
-                        for (int e = 0; e < (XD ? 4 : 0); ++e) e4[e] = make_uint4(0u, 0u, 0u, 0u);
+                        for (int e = 0; e < (XD ? 4 : 0); ++e) e4[e >> 1][e & 1] = make_uint4(0u, 0u, 0u, 0u);
                         load_ext(0);
                     }
                     wait(ctl.qs_done, it & 1);
@@ -760,7 +783,8 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                         if constexpr (XD) {
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                const uint32_t es[4] = {e4[e].x, e4[e].y, e4[e].z, e4[e].w};
+                                const uint4 u4 = e4[e >> 1][e & 1];
+                                const uint32_t es[4] = {u4.x, u4.y, u4.z, u4.w};
 #pragma unroll
                                 for (int k = 0; k < 4; ++k) {
                                     const float2 u = unpack_bf16(es[k]);
@@ -786,9 +810,13 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                         }
                         if (row < rows) {
                             if ((M == DQ || M == DK) && p.out_f32) {
-                                uint4 *dst = reinterpret_cast<uint4 *>((float *)p.out + at + 32 * cb);
+                                float *dst = (float *)p.out + at + 32 * cb;
 #pragma unroll
-                                for (int q = 0; q < 8; ++q) dst[q] = make_uint4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
+                                for (int q = 0; q < 4; ++q) {
+                                    const uint32_t v[8] = {x[8 * q], x[8 * q + 1], x[8 * q + 2], x[8 * q + 3],
+                                                           x[8 * q + 4], x[8 * q + 5], x[8 * q + 6], x[8 * q + 7]};
+                                    st_global32(dst + 8 * q, v, al32);
+                                }
                             } else {
                                 bf16 *dst = (bf16 *)p.out + at + 32 * cb;
 #pragma unroll
