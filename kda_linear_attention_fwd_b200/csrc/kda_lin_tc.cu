@@ -94,6 +94,9 @@ constexpr int kWarps = 23;
 constexpr int kThreads = 32 * kWarps;
 constexpr float kLog2e = 1.4426950408889634f;
 
+constexpr float kForgotten = -280.f;  // 2^-280 times the largest fp32 number is under half the smallest
+constexpr int kSkipFrom = 16;         // a summary of fewer chunks takes them all
+
 enum Mode { FWD, SUM, SUMR, DQ, DK, DV };
 
 struct Maps {
@@ -316,12 +319,51 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
         if (n < 0 && tid == 0) p.gamma[(size_t)w * H + h] = kNoCarry;
     }
 
+    // A summary leaves out the tokens that the decays behind them have multiplied by less than 2^kForgotten,
+    // which takes any finite fp32 state to 0: whole chunks at the pass's beginning, `last` of them staying.
+    int last = 1 << 30;
+    if (C::sum && first < end) {
+        const int qa = p.cu[first], qb = min(p.cu[first + 1], p.T);
+        const int a = min(max(qa, t0), t1), b = max(a, min(qb, t1)), nch = (b - a + kC - 1) / kC;
+        constexpr int kRound = 2 * kC;  // chunks at a time; their decays in pc
+        float *tot = &ctl.pc[0][0], sum = 0.f;
+        for (int r0 = 0; nch >= kSkipFrom && r0 < nch && last > nch; r0 += kRound) {
+            const int here = min(kRound, nch - r0);
+#pragma unroll 4
+            for (int x = warp; x < here; x += kWarps) {
+                const int base = a + (C::rev ? r0 + x : nch - 1 - r0 - x) * kC, rows = min(kC, b - base);
+                float g[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) g[e] = row_g(base, rows, 32 * e + lane, qb);
+                const float t = warp_sum((g[0] + g[1]) + (g[2] + g[3]));
+                if (lane == 0) tot[x] = t;
+            }
+            __syncthreads();
+            for (int x0 = 0; x0 < here; x0 += 32) {
+                const float run = sum + scan_up(x0 + lane < here ? tot[x0 + lane] : 0.f, lane);
+                const unsigned gone = __ballot_sync(0xffffffffu, run < kForgotten);
+                if (gone) {
+                    last = r0 + x0 + __ffs(gone);
+                    break;
+                }
+                sum = __shfl_sync(0xffffffffu, run, 31);
+            }
+            __syncthreads();
+        }
+        last = min(last, nch);
+    }
+    auto leave_out = [&](int &a, int &b) {
+        if (C::sum && C::rev) b = min(b, a + last * kC);
+        if (C::sum && !C::rev) a += ((b - a + kC - 1) / kC - last) * kC;
+    };
+
     // f(n, a, b, qb): tokens [a, b) of sequence n, which ends at qb, in the order of the pass
     auto segments = [&](auto f) {
         for (int i = first; i < end; ++i) {
             const int n = C::rev ? end - 1 - (i - first) : i;
             const int qa = p.cu[n], qb = min(p.cu[n + 1], p.T);
-            const int a = min(max(qa, t0), t1), b = max(a, min(qb, t1));
+            int a = min(max(qa, t0), t1), b = max(a, min(qb, t1));
+            leave_out(a, b);
             f(n, a, b, qa, qb);
         }
     };
@@ -911,6 +953,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                 const int n = C::rev ? end - 1 - c.seg : first + c.seg;
                 c.a = min(max(p.cu[n], t0), t1);
                 c.b = max(c.a, min(min(p.cu[n + 1], p.T), t1));
+                leave_out(c.a, c.b);
                 c.nch = (c.b - c.a + kC - 1) / kC;
                 c.ci = 0;
             }

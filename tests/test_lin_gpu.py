@@ -446,3 +446,42 @@ def test_dg_of_strong_and_weak_decays(cuda_lib, dtype, g):
     ref = O.backward(np32(d["q"]), np32(d["k"]), np32(d["v"]), np32(d["g"]), d["host"], np32(d["dy"]), scale=0.5)
     near(got["dg"], ref["dg"], TOL[DT[dtype]], "dg")
     assert (got["dg"][[0, 300]] == 0).all()
+
+
+@pytest.mark.parametrize("where", ["all", "far"])
+@pytest.mark.parametrize("per_head", [False, True])
+def test_long_windows(cuda_lib, where, per_head):
+    """Windows of 17 and 16 chunks, whose summaries leave out what the decays have
+    forgotten: the state behind the last token and the gradient of the one before
+    the first, against their sums in 64 bits.  far: only tokens at the far end have
+    values, 1e30 of them, so that what remains of them is all there is.
+    The exponents are sums of up to 33 chunks' decays, each rounded at 2^-19 at
+    most (under 32 in absolute value, in powers of two): 33 x 2^-19 x ln 2 = 5e-5."""
+    T, H, D = 4200, 74, 64
+    gen = torch.Generator().manual_seed(31)
+    randn = lambda *s: torch.randn(*s, generator=gen).to(torch.bfloat16).cuda()  # noqa: E731
+    q, k, v, dy = randn(T, H, D), randn(T, H, D), randn(T, H, D), randn(T, H, D)
+    # from 1 (forgotten at once) down to nothing forgotten in the whole sequence
+    slope = torch.logspace(0, -5, H).cuda()
+    slope[-1] = 0.0
+    g = (-slope if per_head else -slope * torch.rand(T, H, generator=gen).cuda()).to(torch.bfloat16)
+    if where == "far":
+        v[20:], dy[:T - 20] = 0, 0
+        v[:20] *= 1e30
+        dy[T - 20:] *= 1e30
+    cu = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    o, S = kda.lin_chunk_fwd(q, k, v, g, cu)
+    ds0 = kda.lin_bwd(q, k, v, g, dy, cu)["ds0"]
+    gd = g.double().expand(T, H)
+    through = gd.cumsum(0)
+    want = torch.einsum("thk,th,thv->hkv", k.double(), (through[-1] - through).exp(), v.double())
+    dwant = torch.einsum("thk,th,thv->hkv", q.double(), through.exp(), dy.double())
+    for got, exact, what in ((S[0], want, "state"), (ds0[0], dwant, "ds0")):
+        assert torch.isfinite(got).all()
+        size = exact.abs().amax((1, 2))
+        err = (got.double() - exact).norm(dim=(1, 2)) / exact.norm(dim=(1, 2)).clamp_min(1e-300)
+        bad = (err > 6e-5) & (size > 1e-30)
+        assert not bad.any(), f"{what}: heads {bad.nonzero().flatten().tolist()} off by {err[bad].tolist()}"
+        assert (got.abs().amax((1, 2))[size < 1e-46] == 0).all(), what
+    if where == "all":
+        near(o[-1], np32(torch.einsum("hk,hkv->hv", q[-1].double(), want)), 1e-2, "last output")
