@@ -9,7 +9,7 @@
 // (512 bytes); with few heads the columns are split over DV / DVS CTAs so
 // that more SMs load at once (launch_decode below).  Measured on one B200
 // (6531 GB/s copied): 256 sequences x 32 heads of 128 x 128 (1.07 GB) 160 us;
-// one sequence x 32 heads 3.6 us, bound by the latency of one round trip.
+// one sequence x 16 heads 3.6 us, bound by the latency of one round trip.
 #include "kda_common.cuh"
 
 namespace kda {

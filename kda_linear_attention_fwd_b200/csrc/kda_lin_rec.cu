@@ -38,12 +38,10 @@
 // and the dk pass takes the product with its own state there, so the sums that
 // cancel are at most 64 tokens long.
 //
-// What bounds it: the fp32 FMAs.  Two per state element and token are
-// 2 x 128 x 64 x 148 SMs' share of the 74 TFLOP/s that plain FMAs reach; the
-// ragged gradient (1023 tokens of 9 sequences x 16 heads over 4, 128 x 64: about
-// 1.5 GFLOP of them) takes 175 us (floor of its bytes 7 us), the longest
-// sequence being cut into windows for the SMs; the rest is the latency of a
-// token group's chain: read, sum over the lanes, store.
+// What bounds it: short calls (2345 tokens of 5 sequences x 8 heads, 64 x 128,
+// gradient 175 us; 256 tokens x 2 heads of 64 x 64 forward 26 us; the floors of
+// their bytes 7 and 0.1 us) the latency of a token group's chain: read, sum over
+// the lanes, store; long ones the FMAs, two per state element and token.
 #include "kda_common.cuh"
 #include "kda_lin.cuh"
 #include "kda_sm100.cuh"

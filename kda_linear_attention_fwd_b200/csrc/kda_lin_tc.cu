@@ -39,12 +39,12 @@
 // columns, A (P in its place) two buffers of 128, O 128.
 //
 // Measured on one B200 (6531 GB/s copied, 1653 TFLOP/s): 131072 x 32 heads of
-// 128 x 128 in 1715 us (floor 658: summary 680, scan, outputs 1030), at the
-// 1000 W cap (1.75 GHz); 65536 tokens in 40 ragged sequences x 16 heads 292 us
-// (floor 119).  A chunk takes about 4.5 us where its products take 1.4 and its
-// bytes 3.0: DRAM is at a third, the tensor pipe at 22%; what is left is the
-// chain w V -> state -> its copy -> R S -> scaling -> P V -> O of a chunk, a
-// third of it instruction fetch and barrier latency.
+// 128 x 128 in 1570 us (floor 658; summary 345, scan 10, outputs 1000) at the
+// 1000 W cap (1.75 GHz); 30202 tokens in 8 ragged sequences x 32 heads 300 us
+// (floor 119).  A chunk of the outputs' pass takes 4.4 us (its products 1.4, its
+// bytes 3.0), one of a summary 2.4; the tensor pipe is active 22% of the time.  What is
+// left is the chain of a chunk: w V -> state -> its copy -> R S -> scaling ->
+// P V -> O, with the waits and the code of each step.
 //
 // The gradient (kda_lin_rec.cu has the formulas) is three such passes: dq
 // (read do, write v, value k), dk and dv reversed.  Its dg_t is the sum of
@@ -95,7 +95,7 @@ constexpr int kThreads = 32 * kWarps;
 constexpr float kLog2e = 1.4426950408889634f;
 
 constexpr float kForgotten = -280.f;  // 2^-280 times the largest fp32 number is under half the smallest
-constexpr int kSkipFrom = 16;         // a summary of fewer chunks takes them all
+constexpr int kSkipFrom = 16;         // a summary of fewer takes all (8 chunks: 79.2 us as such a call, 79.9 us with the look at the decays)
 
 enum Mode { FWD, SUM, SUMR, DQ, DK, DV };
 
