@@ -7,7 +7,7 @@
 #include "../../include/kda.h"
 #include "kda_args.h"
 #include "kda_common.cuh"
-#include "kda_lin.cuh"
+#include "kda_lin.h"
 
 namespace kda {
 namespace lin {

@@ -1,7 +1,7 @@
 // Linear attention with one decay per head, token by token in fp32: the
 // forward, its window summaries and the gradient's three passes.
 //
-// The recurrence itself (kda_lin.cuh) costs two FMAs per state element and
+// The recurrence itself (kda_lin.h) costs two FMAs per state element and
 // token, so fp32 inputs, which the tensor cores could only take split into
 // several products, run it directly: the whole state of one head sits in the
 // registers of one CTA of 128 threads and every product is a plain fp32 FMA
@@ -43,7 +43,7 @@
 // their bytes 7 and 0.1 us) the latency of a token group's chain: read, sum over
 // the lanes, store; long ones the FMAs, two per state element and token.
 #include "kda_common.cuh"
-#include "kda_lin.cuh"
+#include "kda_lin.h"
 #include "kda_sm100.cuh"
 
 namespace kda {

@@ -1,7 +1,7 @@
 // Linear attention with one decay per head on the 5th-generation tensor
 // cores: bf16 inputs, chunks of 128 tokens.
 //
-// One CTA runs the tokens of one (window, head) (kda_lin.cuh), chunk after
+// One CTA runs the tokens of one (window, head) (kda_lin.h), chunk after
 // chunk.  With c_t the log-decay summed from the chunk's first token to t,
 // D[t][s] = exp(c_t - c_s) for s <= t and w_s = exp(c_last - c_s), a chunk is
 //   A   = R W^T                  R: the read vectors (q), W: the write vectors (k)
@@ -76,7 +76,7 @@
 #include <type_traits>
 
 #include "kda_common.cuh"
-#include "kda_lin.cuh"
+#include "kda_lin.h"
 #include "kda_sm100.cuh"
 
 namespace kda {

@@ -34,7 +34,7 @@
 #include "../../include/kda.h"
 #include "kda_args.h"
 #include "kda_common.cuh"
-#include "kda_lin.cuh"
+#include "kda_lin.h"
 #include "kda_sm100.cuh"
 
 namespace kda {
