@@ -104,10 +104,23 @@ struct Maps {
 };
 
 constexpr int kMaxSlots = 8;  // of the ring; more would let a chunk's V arrive too early (see clean)
+constexpr int kVBars = 4;     // a summary's ring of eight slots holds the V of four chunks
+
+// A wait by parity is right only while its barrier is in the phase waited for or
+// the next.  The waits on a slot's `full` are: the tile before it in the slot has
+// been waited for by then (R and W by the MMA warps, which take part in every
+// tile's release), and none behind it can come before the waiter has released it.
+// The groups that make w V have neither: they take no part in the release, and
+// where a chunk has fewer quarters than there are groups some run ahead through
+// it without waiting for anything else.  So V has barriers by chunk instead,
+// whose every phase each group sees, and v_seen holds back the load that would
+// begin the next phase until all of them have.  (The V's slot then counts as full
+// as soon as it is asked for, so that its phases go on as the ring does.)
 
 template <bool DQ>
 struct Ctl {
     unsigned long long full[kMaxSlots], free[kMaxSlots];  // the ring's slots
+    unsigned long long v_full[kVBars], v_seen[kVBars];    // V of chunk c in c % kVBars
     unsigned long long a_full[2];         // A is in TMEM (two buffers)
     unsigned long long p_full[2];         // P is in TMEM, in A's place
     unsigned long long a_free[2];         // P V has read it
@@ -150,7 +163,8 @@ struct Cfg {
     static constexpr int xc_bytes = M == DQ ? 10 * 32 * 4 : 0;  // DQ: column sums of X, per warp and block
     static constexpr int fit = (232448 - groups * vb_bytes - sb_bytes - xc_bytes - (int)sizeof(Ctl<M == DQ>)) / slot_bytes;
     static constexpr int slots = fit < kMaxSlots ? fit : kMaxSlots;
-    static_assert(slots > tiles, "ring");
+    // the state's products still hold W(c) when A(c + 1), issued in their middle, waits for V(c + 1)'s cleared rows
+    static_assert(slots >= (M == DQ ? tiles + 1 : tiles + 2), "ring");
     static constexpr int off_vb = slots * slot_bytes;
     static constexpr int off_sb = off_vb + groups * vb_bytes;
     static constexpr int off_xc = off_sb + sb_bytes;
@@ -268,6 +282,10 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
             mbar_init(smem_u32(&ctl.full[i]), 1);
             mbar_init(smem_u32(&ctl.free[i]), 2);  // both MMA warps, or one twice
         }
+        for (int i = 0; i < kVBars; ++i) {
+            mbar_init(smem_u32(&ctl.v_full[i]), 1);
+            mbar_init(smem_u32(&ctl.v_seen[i]), 4 * C::groups);  // their warps
+        }
         for (int i = 0; i < C::groups; ++i) {
             mbar_init(smem_u32(&ctl.vb_full[i]), 128);
             mbar_init(smem_u32(&ctl.vb_free[i]), 1);
@@ -300,6 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
     // tile j of chunk c in the ring
     auto slot = [&](int c, int j) { return (c * C::tiles + j) % C::slots; };
     auto phase = [&](int c, int j) -> uint32_t { return (uint32_t)((c * C::tiles + j) / C::slots) & 1u; };
+    auto wait_v = [&](int c) { wait(ctl.v_full[c % kVBars], (uint32_t)(c / kVBars) & 1u); };
     const bf16 *gp = (const bf16 *)p.g + h;
     const uint32_t gs = p.g_per_head ? 0u : (uint32_t)H;
     auto load_g = [&](int t) -> float {  // in powers of two
@@ -714,7 +733,9 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
 #pragma unroll
                     for (int x = 0; x < 4; ++x) gx[x] = row_g(next_base(base), min(kC, b - next_base(base)), 32 * x + lane, qb);
                 unsigned char *tw = sm + slot(it, C::tW) * C::slot_bytes, *tv = sm + slot(it, C::tV) * C::slot_bytes;
-                wait(ctl.full[slot(it, C::tV)], phase(it, C::tV));
+                wait_v(it);
+                __syncwarp();
+                if (lane == 0) arrive(ctl.v_seen[it % kVBars]);
                 if (rows < kC && ((quarters + nq - 1) & (NG - 1)) == grp) {
                     // The last quarter's rows behind the end hold other tokens: zero, whatever they are (the
                     // quarters behind it are not read); each thread the channels that it reads below.  Both MMA
@@ -903,11 +924,13 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
         segments([&](int n, int a, int b, int qa, int qb) {
             chunks(a, b, [&](int base, int rows, int i, int nch) {
                 auto load = [&](int j, const CUtensorMap &map, int head, int boxes) {
-                    const int sl = slot(it, j);
+                    const int sl = slot(it, j), vb = it % kVBars;
                     if (it * C::tiles + j >= C::slots) wait(ctl.free[sl], phase(it, j) ^ 1u);
+                    if (j == C::tV && it >= kVBars) wait(ctl.v_seen[vb], (uint32_t)(it / kVBars - 1) & 1u);
                     if (elect_one_sync() && !*dead) {
-                        const uint32_t bar = smem_u32(&ctl.full[sl]), dst = sbase + sl * C::slot_bytes;
+                        const uint32_t bar = smem_u32(j == C::tV ? &ctl.v_full[vb] : &ctl.full[sl]), dst = sbase + sl * C::slot_bytes;
                         mbar_arrive_expect_tx(bar, boxes * kBox);
+                        if (j == C::tV) arrive(ctl.full[sl]);
                         for (int x = 0; x < boxes; ++x) {
                             tma_load_3d(dst + x * kBox, &map, 64 * x, head, base, bar);
                             if (i + 1 < nch) tma_prefetch_3d(&map, 64 * x, head, next_base(base));
@@ -932,8 +955,11 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
             });
         });
         if (*dead)  // loads in flight land before the CTA ends (bounded)
-            for (int x = max(0, it * C::tiles - C::slots); x < it * C::tiles; ++x)
-                mbar_wait(smem_u32(&ctl.full[x % C::slots]), (uint32_t)(x / C::slots) & 1u);
+            for (int x = max(0, it * C::tiles - C::slots); x < it * C::tiles; ++x) {
+                const int c = x / C::tiles;
+                if (x % C::tiles == C::tV) mbar_wait(smem_u32(&ctl.v_full[c % kVBars]), (uint32_t)(c / kVBars) & 1u);
+                else mbar_wait(smem_u32(&ctl.full[x % C::slots]), (uint32_t)(x / C::slots) & 1u);
+            }
     } else {
         // --------------------------------------------------------------- MMA
         constexpr uint32_t ID_A = idesc_bf16(128, 128, 0, 0);  // R (K-major) x W (K-major)
@@ -974,7 +1000,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                 wait(ctl.full[slot(k, C::tW)], phase(k, C::tW));
                 if (M == DQ) {
                     wait(ctl.full[slot(k, C::tE)], phase(k, C::tE));
-                    wait(ctl.full[slot(k, C::tV)], phase(k, C::tV));
+                    wait_v(k);
                 }
                 if (ahead.rows < kC) {
                     const uint32_t seen = k & 1 ? cleans[1] : cleans[0];
@@ -1055,7 +1081,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                 }
                 __syncwarp();
                 const uint32_t ab = M == DQ ? 0u : (uint32_t)(it & 1), tv = tile(it, C::tV);
-                wait(ctl.full[slot(it, C::tV)], phase(it, C::tV));
+                wait_v(it);
                 wait(ctl.p_full[ab], (M == DQ ? it : it >> 1) & 1);
                 wait(ctl.o_scaled, it & 1);
                 tc_fence_after();

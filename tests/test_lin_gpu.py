@@ -485,3 +485,39 @@ def test_long_windows(cuda_lib, where, per_head):
         assert (got.abs().amax((1, 2))[size < 1e-46] == 0).all(), what
     if where == "all":
         near(o[-1], np32(torch.einsum("hk,hkv->hv", q[-1].double(), want)), 1e-2, "last output")
+
+
+def off_by(got, want):
+    """||err||_2 / ||want||_2 on the device, for tensors too large to bring to the host."""
+    assert torch.isfinite(got).all()
+    return float((got.double() - want.double()).norm() / want.double().norm())
+
+
+@pytest.mark.parametrize("lengths,H,Hk", [
+    # a CTA runs whole sequences whose last chunk (the first one of the reversed passes) has one quarter of 32 tokens
+    (tuple(128 * (3 * i % 11) + 1 + 5 * i % 32 for i in range(36)), 32, 4),
+    # nothing but such chunks
+    (tuple(1 + 7 * i % 32 for i in range(600)), 32, 32),
+    # one, two and three quarters in turn
+    (tuple(1 + 37 * i % 128 for i in range(700)), 16, 16)], ids=("tails", "short", "mixed"))
+def test_short_chunks_of_large_batches(cuda_lib, lengths, H, Hk):
+    """q, k, v and dy together beyond the size of the L2 cache, so that a chunk's
+    loads arrive at different times: bf16 against the fp32 path on the same values
+    (the oracle would take minutes), and against itself."""
+    d = make(lengths, H, Hk, 128, 128, "bf16", seed=32)
+    kw = dict(scale=0.5, initial_state=d["s0"], cu_seqlens_host=d["host"])
+    args = [d[x] for x in ("q", "k", "v", "g")]
+    ref = kda.lin_chunk_fwd(*(x.float() for x in args), d["cu"], **kw)
+    rgrad = kda.lin_bwd(*(x.float() for x in args), d["dy"].float(), d["cu"], d_final_state=d["dsf"], **kw)
+    first = None
+    for _ in range(3):
+        out, fin = kda.lin_chunk_fwd(*args, d["cu"], **kw)
+        got = kda.lin_bwd(*args, d["dy"], d["cu"], d_final_state=d["dsf"], **kw)
+        # (the fp32 results' own 1e-5 on top of the operator's tolerances)
+        assert off_by(out, ref[0]) <= 4e-3 + 1e-5 and off_by(fin, ref[1]) <= 2e-5 + 1e-5
+        for name in ("dq", "dk", "dv", "dg"):
+            assert off_by(got[name], rgrad[name]) <= 4e-3 + 1e-5, name
+        assert off_by(got["ds0"], rgrad["ds0"]) <= 2e-5 + 1e-5
+        all_of = [out, fin, *got.values()]
+        assert first is None or all(torch.equal(a, b) for a, b in zip(all_of, first))
+        first = all_of
