@@ -358,6 +358,8 @@ def chunk_fwd_check(workspace, stream=None, lib=None) -> int:
 
 
 # ---------------------------------------------- linear attention, one decay per head
+# `stream`: another stream than the current one.  Results and workspaces made here
+# belong to it; that the inputs are ready there is the caller's part.
 _CODES = {torch.bfloat16: KDA_DTYPE_BF16, torch.float32: KDA_DTYPE_F32}
 
 
@@ -372,13 +374,24 @@ def _launch(fn, dev, stream, *args):
         _check(fn.__name__, st)
 
 
-def _keep(stream, *tensors):
-    """Tensors made here for a call on another stream than their own: not to be
-    given out again before that stream has passed the call."""
+def _make(stream, make):
+    """make()'s tensors, in the memory of the call's stream and filled on it: what
+    the current stream has yet to do can neither use that memory nor come between."""
+    if stream is None:
+        return make()
+    with torch.cuda.stream(stream):
+        return make()
+
+
+def _keep(stream, dev, *tensors):
+    """The tensors of a call on a given stream: not to be given out again before
+    that stream has passed the call and the current one has passed their use."""
     if stream is not None:
+        here = torch.cuda.current_stream(dev)
         for t in tensors:
             if t is not None:
                 t.record_stream(stream)
+                t.record_stream(here)
 
 
 def _tensor(name, t, shape, dtype, dev):
@@ -408,13 +421,13 @@ def _code(t):
         raise TypeError(f"unsupported dtype {t.dtype}") from None
 
 
-def _space(workspace, dev, need):
+def _space(workspace, dev, stream, need):
     """(tensor, address, bytes); need() sizes a new one."""
     if workspace is None:
         if torch._C._cuda_getDevice() != dev:  # the plan is the device's
             with torch.cuda.device(dev):
-                return _space(None, dev, need)
-        workspace = torch.empty(max(need(), 16), dtype=torch.uint8, device="cuda")
+                return _space(None, dev, stream, need)
+        workspace = _make(stream, lambda: torch.empty(max(need(), 16), dtype=torch.uint8, device="cuda"))
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace: want a contiguous tensor on cuda:{dev}")
     # too small a one is refused by the library
@@ -462,17 +475,17 @@ def lin_chunk_fwd(q, k, v, g, cu_seqlens, *, scale=1.0, initial_state=None, fina
     p_cu = _tensor("cu_seqlens", cu_seqlens, (N + 1,), torch.int32, dev)
     states = (N, H, dk, dv)
     if out is None:
-        out = torch.empty_like(v)
+        out = _make(stream, lambda: torch.empty_like(v))
     if final_state is None and output_final_state:
-        final_state = q.new_empty(states, dtype=torch.float32)
+        final_state = _make(stream, lambda: q.new_empty(states, dtype=torch.float32))
     p_out = _tensor("out", out, v.shape, q.dtype, dev)
     p_s0 = _opt("initial_state", initial_state, states, torch.float32, dev)
     p_s1 = _opt("final_state", final_state, states, torch.float32, dev)
     host = _host_offsets(cu_seqlens_host, N)
-    ws, p_ws, n_ws = _space(workspace, dev, lambda: lib.kda_lin_chunk_fwd_workspace_size(T, N, H, Hk, dk, dv, code))
+    ws, p_ws, n_ws = _space(workspace, dev, stream, lambda: lib.kda_lin_chunk_fwd_workspace_size(T, N, H, Hk, dk, dv, code))
     _launch(lib.kda_lin_chunk_fwd, dev, stream, *ptrs, p_out, p_cu, host, N, T, H, Hk, dk, dv, code, float(scale), flags,
             p_s0, p_s1, p_ws, n_ws)
-    _keep(stream, ws, out, final_state)
+    _keep(stream, dev, ws, out, final_state)
     return out, final_state
 
 
@@ -482,11 +495,11 @@ def lin_decode_step(q, k, v, g, state, *, scale=1.0, out=None, stream=None):
     lib = load()
     dev, N, H, Hk, dk, dv, flags, code, ptrs = _lin_shapes(q, k, v, g)
     if out is None:
-        out = torch.empty_like(v)
+        out = _make(stream, lambda: torch.empty_like(v))
     p_out = _tensor("out", out, v.shape, q.dtype, dev)
     p_s = _tensor("state", state, (N, H, dk, dv), torch.float32, dev)
     _launch(lib.kda_lin_decode_step, dev, stream, *ptrs, p_out, p_s, N, H, Hk, dk, dv, code, float(scale), flags)
-    _keep(stream, out)
+    _keep(stream, dev, out)
     return out
 
 
@@ -509,13 +522,13 @@ def lin_bwd(q, k, v, g, dy, cu_seqlens, *, scale=1.0, initial_state=None, d_fina
     # tokens outside every sequence keep what is there: zeros only where the
     # offsets are not known to cover every token
     new = torch.empty_like if cu_seqlens_host is not None else torch.zeros_like
-    out = {"dq": new(q), "dk": new(k), "dv": new(v), "dg": new(g),
-           "ds0": q.new_empty(states, dtype=torch.float32)}
+    out = _make(stream, lambda: {"dq": new(q), "dk": new(k), "dv": new(v), "dg": new(g),
+                                 "ds0": q.new_empty(states, dtype=torch.float32)})
     host = _host_offsets(cu_seqlens_host, N)
-    ws, p_ws, n_ws = _space(workspace, dev, lambda: lib.kda_lin_bwd_workspace_size(T, N, H, Hk, dk, dv))
+    ws, p_ws, n_ws = _space(workspace, dev, stream, lambda: lib.kda_lin_bwd_workspace_size(T, N, H, Hk, dk, dv))
     _launch(lib.kda_lin_bwd, dev, stream, *ptrs, p_dy, p_cu, host, N, T, H, Hk, dk, dv, code, float(scale), flags, p_s0, p_ds,
             *(x.data_ptr() for x in out.values()), p_ws, n_ws)
-    _keep(stream, ws, *out.values())
+    _keep(stream, dev, ws, *out.values())
     return out
 
 
@@ -564,13 +577,13 @@ def block_norm(y, *, post_norm=True, post_weight=None, gate=None, gate_logits=Fa
     p_x, s_x = _norm_rows("residual", residual, shape, dt, dev)
     p_wp, p_wn = _opt("post_weight", post_weight, (D,), dt, dev), _opt("pre_weight", pre_weight, (D,), dt, dev)
     if out is None:
-        out = y.new_empty(shape)
+        out = _make(stream, lambda: y.new_empty(shape))
     if normed is None and pre_norm:
-        normed = y.new_empty(shape)
+        normed = _make(stream, lambda: y.new_empty(shape))
     p_out, p_n = _tensor("out", out, shape, dt, dev), _opt("normed", normed, shape, dt, dev)
     _launch(lib.kda_block_norm, dev, stream, p_y, s_y, p_wp, p_g, s_g, p_x, s_x, p_wn, p_out, p_n,
             y.numel() // D if D else 0, D, code, float(res_scale), float(eps), flags)
-    _keep(stream, out, normed)
+    _keep(stream, dev, out, normed)
     return out, normed
 
 
@@ -598,10 +611,11 @@ def block_norm_bwd(dout, dnormed, y, *, post_norm=True, post_weight=None, gate=N
     def like(t, shape=None, dtype=None):
         return None if t is None else y.new_empty(shape or t.shape, dtype=dtype or t.dtype)
 
-    got = {"dy": like(y), "dgate": like(gate), "dresidual": like(residual),
-           "dpost_weight": like(post_weight, (D,), torch.float32), "dpre_weight": like(pre_weight, (D,), torch.float32)}
-    ws, p_ws, n_ws = _space(workspace, dev, lambda: lib.kda_block_norm_bwd_workspace_size(rows, D, code))
+    got = _make(stream, lambda: {"dy": like(y), "dgate": like(gate), "dresidual": like(residual),
+                                 "dpost_weight": like(post_weight, (D,), torch.float32),
+                                 "dpre_weight": like(pre_weight, (D,), torch.float32)})
+    ws, p_ws, n_ws = _space(workspace, dev, stream, lambda: lib.kda_block_norm_bwd_workspace_size(rows, D, code))
     _launch(lib.kda_block_norm_bwd, dev, stream, p_do, p_dn, p_y, s_y, p_wp, p_g, s_g, p_x, s_x, p_wn,
             *(None if t is None else t.data_ptr() for t in got.values()), rows, D, code, float(res_scale), float(eps), flags, p_ws, n_ws)
-    _keep(stream, ws, *got.values())
+    _keep(stream, dev, ws, *got.values())
     return got

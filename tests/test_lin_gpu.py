@@ -521,3 +521,49 @@ def test_short_chunks_of_large_batches(cuda_lib, lengths, H, Hk):
         all_of = [out, fin, *got.values()]
         assert first is None or all(torch.equal(a, b) for a, b in zip(all_of, first))
         first = all_of
+
+
+def long_work():
+    """Some ten milliseconds for the current stream."""
+    a = torch.randn(8192, 8192, device="cuda")
+    for _ in range(10):
+        a = a @ a * 1e-4
+    return a
+
+
+def on_a_side_stream(call):
+    """call(stream), made while the current stream is busy and has freed memory of
+    the results' sizes that it still writes, as a dict; and call(None), beforehand."""
+    as_dict = lambda x: x if isinstance(x, dict) else dict(enumerate(x if isinstance(x, tuple) else (x,)))  # noqa: E731
+    want = as_dict(call(None))
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(2):
+        busy = long_work()
+        for t in [torch.empty_like(x) for x in want.values() if x is not None]:
+            t.fill_(float("nan"))  # behind the long work; the memory goes back to the allocator here
+        got = as_dict(call(side))
+        side.synchronize()
+        torch.cuda.synchronize()
+        del busy
+        for name, x in want.items():
+            assert (x is None) == (got[name] is None) and (x is None or torch.equal(x, got[name])), name
+
+
+@pytest.mark.parametrize("host", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_results_on_a_given_stream_wait_for_no_other(cuda_lib, dtype, host):
+    """Nothing that the current stream has yet to do, the call's own fills among
+    them, reaches the results of a call on another stream."""
+    d = make((300, 50), 4, 2, 64, 64, dtype, seed=33)
+    kw = dict(scale=0.5, initial_state=d["s0"], cu_seqlens_host=d["host"] if host else None)
+    args = [d[x] for x in ("q", "k", "v", "g")]
+    on_a_side_stream(lambda s: kda.lin_chunk_fwd(*args, d["cu"], stream=s, **kw))
+    on_a_side_stream(lambda s: kda.lin_bwd(*args, d["dy"], d["cu"], d_final_state=d["dsf"], stream=s, **kw))
+    gate, w = torch.randn_like(d["v"]), torch.ones(64, device="cuda", dtype=DT[dtype])
+    norm = dict(post_weight=w, gate=gate, gate_logits=True, residual=d["dy"], pre_norm=True, pre_weight=w)
+    on_a_side_stream(lambda s: kda.block_norm(d["v"], stream=s, **norm))
+    on_a_side_stream(lambda s: kda.block_norm_bwd(d["dy"], gate, d["v"], stream=s, **norm))
+    step = [x[:2].contiguous() for x in args]
+    states = iter([d["s0"].clone() for _ in range(3)])  # one for each call
+    on_a_side_stream(lambda s: kda.lin_decode_step(*step, next(states), stream=s))
