@@ -37,8 +37,10 @@ namespace lin {
 // fp32), so clamping there changes no result; it keeps sums of -inf finite.
 constexpr float kMinG = -110.f;
 
-// A window whose outgoing state nobody reads (no sequence crosses its end).
-constexpr float kNoCarry = -1.f;
+// In place of a window's gamma: nobody reads its outgoing state (no sequence
+// crosses its end), and that state begins in the window, so that nothing of what
+// enters it may reach it (not even times 0, which inf would survive as NaN).
+constexpr float kNoCarry = -1.f, kBegins = -2.f;
 
 struct Params {
     // one pass of the recurrence: state [DA][DB] += wr (x) val, out = state^T rd

@@ -415,7 +415,7 @@ KDA_DEVICE void rec_body(const Params &p, unsigned char *smem_raw) {
         if (whole && p.start_copy) store_state(p.start_copy + win_at, false, 1.f);
         run_segment(n, a, b, p.cu[n], min(p.cu[n + 1], p.T));
         store_state(p.win_state + win_at, false, 1.f);
-        if (tid == 0) p.gamma[(size_t)w * H + h] = whole ? 0.f : gamma;
+        if (tid == 0) p.gamma[(size_t)w * H + h] = whole ? kBegins : gamma;
     } else {
         const int first = wd.first, end = wd.end;
         for (int i = first; i < end; ++i) {
@@ -486,7 +486,7 @@ __global__ void __launch_bounds__(128) scan_kernel(const ScanSide a, const ScanS
             if (w0 + i < W) {
                 sd.z[window(w0 + i) * quads + e] = carry;
                 if (gm[i] < 0.f) {
-                    carry = make_float4(0.f, 0.f, 0.f, 0.f);
+                    carry = gm[i] == kBegins ? zz[i] : make_float4(0.f, 0.f, 0.f, 0.f);
                 } else {
                     carry.x = fmaf(gm[i], carry.x, zz[i].x);
                     carry.y = fmaf(gm[i], carry.y, zz[i].y);

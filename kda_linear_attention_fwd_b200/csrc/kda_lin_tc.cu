@@ -691,7 +691,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                     }
                 }
             }
-            if (C::sum && row == 0) p.gamma[(size_t)w * H + h] = from_win ? gamma : 0.f;
+            if (C::sum && row == 0) p.gamma[(size_t)w * H + h] = from_win ? gamma : kBegins;
         });
         tc_fence_before();
     } else if (role == 2 || role == 3 || (C::sum && role < 5)) {

@@ -567,3 +567,29 @@ def test_results_on_a_given_stream_wait_for_no_other(cuda_lib, dtype, host):
     step = [x[:2].contiguous() for x in args]
     states = iter([d["s0"].clone() for _ in range(3)])  # one for each call
     on_a_side_stream(lambda s: kda.lin_decode_step(*step, next(states), stream=s))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_an_overflowing_sequence_leaves_its_neighbours_alone(cuda_lib, dtype):
+    """Finite inputs whose state overflows, in sequences that cross windows: the
+    sequence behind (in the gradient: before) them has the oracle's results."""
+    d = make((1500, 1500), 2, 2, 64, 64, dtype, s0=False, seed=34)
+    args = lambda: [d[x] for x in ("q", "k", "v", "g")]  # noqa: E731
+    ref, S = O.forward(*(np32(x) for x in args()), d["host"], scale=0.5)
+    rgrad = O.backward(*(np32(x) for x in args()), d["host"], np32(d["dy"]), scale=0.5)
+    tol, stol = TOL[DT[dtype]], 2e-5 if dtype == "bf16" else 1e-5
+    kept = {x: d[x].clone() for x in ("q", "k", "v", "dy")}
+    d["k"][:1500], d["v"][:1500] = 1e25, 1e25
+    for host in (None, d["host"]):
+        out, fin = kda.lin_chunk_fwd(*args(), d["cu"], scale=0.5, cu_seqlens_host=host)
+        assert not torch.isfinite(fin[0]).all()
+        near(out[1500:], ref[1500:], tol, "out")
+        near(fin[1], S[1], stol, "final state")
+    d.update({x: t.clone() for x, t in kept.items()})
+    d["q"][1500:], d["dy"][1500:] = 1e25, 1e25
+    for host in (None, d["host"]):
+        got = kda.lin_bwd(*args(), d["dy"], d["cu"], scale=0.5, cu_seqlens_host=host)
+        assert not torch.isfinite(got["ds0"][1]).all()
+        for name in ("dq", "dk", "dv", "dg"):
+            near(got[name][:1500], rgrad[name][:1500], tol, name)
+        near(got["ds0"][0], rgrad["ds0"][0], stol, "ds0")
