@@ -371,7 +371,10 @@ int kda_bwd(const void *q, const void *k, const void *v, const void *g, const vo
  *             log-decay, g <= 0.  There is no floor; -inf forgets everything.
  *   states    [num_seqs][H][dk][dv] fp32
  * dk, dv in {64, 128}; dtype BF16 or F32, shared by q, k, v, g, out and the
- * gradients (states are fp32).  Inputs must be finite (g may be -inf).
+ * gradients (states are fp32).  Inputs must be finite (g may be -inf) and g <= 0;
+ * neither build checks that.  A NaN log-decay gives NaN in what depends on it
+ * (but where decays behind it multiply by less than 2^-280 inside a window, it
+ * may be forgotten with the rest).
  * Alignment: q, k, v, out, states, workspace 16 bytes, g its element size.
  *
  * Tokens outside every sequence (behind cu_seqlens[num_seqs], when the host

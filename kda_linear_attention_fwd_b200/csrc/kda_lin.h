@@ -36,6 +36,12 @@ namespace lin {
 // Log-decays below this leave nothing of an fp32 state (exp(-104) is 0 in
 // fp32), so clamping there changes no result; it keeps sums of -inf finite.
 constexpr float kMinG = -110.f;
+// (NaN stays NaN, as it is in the single-token step, which does not clamp)
+__device__ __forceinline__ float clamp_g(float g) {
+    float x;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(x) : "f"(g), "f"(kMinG));
+    return x;
+}
 
 // In place of a window's gamma: nobody reads its outgoing state (no sequence
 // crosses its end), and that state begins in the window, so that nothing of what

@@ -161,7 +161,7 @@ KDA_DEVICE void rec_body(const Params &p, unsigned char *smem_raw) {
                 for (int c = 0; c < 4; ++c) s[i][r][c] *= f;
     };
     auto load_g = [&](int t) -> float {
-        return fmaxf(((const float *)p.g)[p.g_per_head ? (size_t)h : (size_t)t * H + h], kMinG);
+        return clamp_g(((const float *)p.g)[p.g_per_head ? (size_t)h : (size_t)t * H + h]);
     };
 
     // tokens [a, b) of sequence n, whose true range is [qa, qb)
@@ -225,7 +225,7 @@ KDA_DEVICE void rec_body(const Params &p, unsigned char *smem_raw) {
 #pragma unroll
                             for (int c = 0; c < 4; ++c) d = fmaf(x[c], s[i][r][c], d);
                         }
-                    d = warp_sum(d) * __expf(fmaxf(sm.g[buf][rows - 1], kMinG));
+                    d = warp_sum(d) * __expf(clamp_g(sm.g[buf][rows - 1]));
                     if (lane == 0) sm.fdot[warp] = d;
                     if (tid < chunk_len) sm.xq[tid] = p.xdot[(size_t)(a + chunk * kCkpt + tid) * H + h];
                 }
@@ -238,7 +238,7 @@ KDA_DEVICE void rec_body(const Params &p, unsigned char *smem_raw) {
                 // in the order of the pass: token e of the group is j0 + e, or j0 + 3 - e
                 float gs[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) gs[e] = fmaxf(sm.g[buf][MO::rev ? j0 + 3 - e : j0 + e], kMinG);
+                for (int e = 0; e < 4; ++e) gs[e] = clamp_g(sm.g[buf][MO::rev ? j0 + 3 - e : j0 + e]);
                 const bool slow = G + ((gs[0] + gs[1]) + (gs[2] + gs[3])) < -40.f;  // the same in every thread
 #pragma unroll 1
                 for (int only = slow ? 0 : 3; only < 4; ++only) {  // slow: one token per round, renormalised at each

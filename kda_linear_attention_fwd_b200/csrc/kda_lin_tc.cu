@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
     const bf16 *gp = (const bf16 *)p.g + h;
     const uint32_t gs = p.g_per_head ? 0u : (uint32_t)H;
     auto load_g = [&](int t) -> float {  // in powers of two
-        return fmaxf(__bfloat162float(gp[(size_t)(uint32_t)t * gs]), kMinG) * kLog2e;
+        return clamp_g(__bfloat162float(gp[(size_t)(uint32_t)t * gs])) * kLog2e;
     };
     // the decay that row `row` of the chunk of `rows` tokens at `base` multiplies the running state with
     auto row_g = [&](int base, int rows, int row, int qb) -> float {

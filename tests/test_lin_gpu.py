@@ -593,3 +593,30 @@ def test_an_overflowing_sequence_leaves_its_neighbours_alone(cuda_lib, dtype):
         for name in ("dq", "dk", "dv", "dg"):
             near(got[name][:1500], rgrad[name][:1500], tol, name)
         near(got["ds0"][0], rgrad["ds0"][0], stol, "ds0")
+
+
+@pytest.mark.parametrize("host", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_nan_decays_are_not_hidden(cuda_lib, dtype, host):
+    """A NaN log-decay is NaN in what depends on it, as in the single-token step,
+    and nothing else."""
+    d = make((400, 300), 2, 2, 64, 64, dtype, seed=35)
+    args = [d[x] for x in ("q", "k", "v", "g")]
+    kw = dict(scale=0.5, initial_state=d["s0"], cu_seqlens_host=d["host"] if host else None)
+    want = (*kda.lin_chunk_fwd(*args, d["cu"], **kw), kda.lin_bwd(*args, d["dy"], d["cu"], **kw))
+    t = 200
+    d["g"][t, 1] = float("nan")
+    out, fin = kda.lin_chunk_fwd(*args, d["cu"], **kw)
+    got = kda.lin_bwd(*args, d["dy"], d["cu"], **kw)
+    nan = lambda x: torch.isnan(x).all()  # noqa: E731
+    assert nan(out[t:400, 1]) and nan(fin[0, 1]) and nan(got["dq"][t:400, 1])
+    assert nan(got["dk"][:t, 1]) and nan(got["dv"][:t, 1]) and nan(got["dg"][t, 1]) and nan(got["ds0"][0, 1])
+    out[t:400, 1], fin[0, 1] = want[0][t:400, 1], want[1][0, 1]
+    assert torch.equal(out, want[0]) and torch.equal(fin, want[1])
+    for name in want[2]:
+        x, y = got[name], want[2][name]
+        assert torch.equal(x[1:, 1], y[1:, 1]) and torch.equal(x[:, 0], y[:, 0]) if name == "ds0" else (
+            torch.equal(x[400:], y[400:]) and torch.equal(x[:, 0], y[:, 0])), name
+    s = d["s0"].clone()
+    kda.lin_decode_step(*(x[:2].contiguous() for x in args[:3]), d["g"][t:t + 2].contiguous(), s)
+    assert nan(s[0, 1]) and torch.isfinite(s[:, 0]).all()
