@@ -350,7 +350,11 @@ int kda_lin_bwd(const void *q, const void *k, const void *v, const void *g, cons
     cudaStream_t st = (cudaStream_t)stream;
     int rc = check_sizes(num_seqs, total_tokens, H, Hk, dk, dv, dtype, flags);
     if (rc != KDA_OK) return rc;
-    if (num_seqs == 0) return total_tokens == 0 ? KDA_OK : KDA_ERR_INVALID_ARG;
+    if (num_seqs == 0) {
+        if (total_tokens != 0) return KDA_ERR_INVALID_ARG;
+        if (!(flags & KDA_LIN_DECAY_PER_HEAD) || !dg) return KDA_OK;
+        return ok(cudaMemsetAsync(dg, 0, (size_t)H * (dtype == KDA_DTYPE_BF16 ? 2 : 4), st)) ? KDA_OK : KDA_ERR_CUDA;
+    }
     if (total_tokens > 0 && (!q || !k || !v || !g || !dy || !dq || !dk_out || !dv_out || !dg)) return KDA_ERR_INVALID_ARG;
     const bool bf16 = dtype == KDA_DTYPE_BF16;
     const size_t esz = bf16 ? 2 : 4;

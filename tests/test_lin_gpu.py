@@ -620,3 +620,19 @@ def test_nan_decays_are_not_hidden(cuda_lib, dtype, host):
     s = d["s0"].clone()
     kda.lin_decode_step(*(x[:2].contiguous() for x in args[:3]), d["g"][t:t + 2].contiguous(), s)
     assert nan(s[0, 1]) and torch.isfinite(s[:, 0]).all()
+
+
+def test_no_sequences_at_all(cuda_lib):
+    """The gradient of a decay per head is a sum, which over nothing is zero."""
+    d = make((), 4, 2, 64, 128, "bf16", per_head=True, seed=36)
+    junk = torch.full((64, 4), float("nan"), device="cuda", dtype=torch.bfloat16)
+    del junk
+    out, fin = kda.lin_chunk_fwd(d["q"], d["k"], d["v"], d["g"], d["cu"], cu_seqlens_host=[0])
+    assert out.shape == (0, 4, 128) and fin.shape == (0, 4, 64, 128)
+    dg = torch.full((4,), 7.0, device="cuda", dtype=torch.bfloat16)
+    lib, P = kda.load(), torch.Tensor.data_ptr
+    ws = torch.empty(max(kda.lin_bwd_workspace_size(0, 0, 4, 2, 64, 128), 16), dtype=torch.uint8, device="cuda")
+    st = lib.kda_lin_bwd(*[None] * 5, P(d["cu"]), None, 0, 0, 4, 2, 64, 128, kda.KDA_DTYPE_BF16, 1.0, kda.LIN_DECAY_PER_HEAD,
+                         None, None, None, None, None, P(dg), None, P(ws), ws.numel(), torch.cuda.current_stream().cuda_stream)
+    assert st == 0 and (dg == 0).all()
+    assert (kda.lin_bwd(d["q"], d["k"], d["v"], d["g"], d["dy"], d["cu"], cu_seqlens_host=[0])["dg"] == 0).all()
