@@ -43,7 +43,7 @@ __global__ void __launch_bounds__(256, 2)
         sk[i] = ld(k + nk * DK + i);
         sq[i] = ld(q + nk * DK + i);
     }
-    const float a = __expf(ld(g + (g_per_head ? (size_t)h : (size_t)nh)));
+    const float a = expf(ld(g + (g_per_head ? (size_t)h : (size_t)nh)));
     float vv[4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) vv[c] = ld(v + (size_t)nh * dv + c0 + cg * 4 + c);

@@ -39,7 +39,7 @@
 // cancel are at most 64 tokens long.
 //
 // What bounds it: short calls (2345 tokens of 5 sequences x 8 heads, 64 x 128,
-// gradient 175 us; 256 tokens x 2 heads of 64 x 64 forward 26 us; the floors of
+// gradient 179 us; 256 tokens x 2 heads of 64 x 64 forward 26 us; the floors of
 // their bytes 7 and 0.1 us) the latency of a token group's chain: read, sum over
 // the lanes, store; long ones the FMAs, two per state element and token.
 #include "kda_common.cuh"
@@ -225,7 +225,7 @@ KDA_DEVICE void rec_body(const Params &p, unsigned char *smem_raw) {
 #pragma unroll
                             for (int c = 0; c < 4; ++c) d = fmaf(x[c], s[i][r][c], d);
                         }
-                    d = warp_sum(d) * __expf(clamp_g(sm.g[buf][rows - 1]));
+                    d = warp_sum(d) * expf(clamp_g(sm.g[buf][rows - 1]));
                     if (lane == 0) sm.fdot[warp] = d;
                     if (tid < chunk_len) sm.xq[tid] = p.xdot[(size_t)(a + chunk * kCkpt + tid) * H + h];
                 }
@@ -242,6 +242,8 @@ KDA_DEVICE void rec_body(const Params &p, unsigned char *smem_raw) {
                 const bool slow = G + ((gs[0] + gs[1]) + (gs[2] + gs[3])) < -40.f;  // the same in every thread
 #pragma unroll 1
                 for (int only = slow ? 0 : 3; only < 4; ++only) {  // slow: one token per round, renormalised at each
+                    // (expf: exp2 of a rounded G log2 e, up to 58, would be off by 1e-6, and a write and the
+                    // renormalisation behind it not by the same; 2345 tokens' gradient 176 -> 179 us)
                     float wf[4], rf[4];
                     if (slow) {
                         const float f = expf(G + (only == 0 ? gs[0] : only == 1 ? gs[1] : only == 2 ? gs[2] : gs[3]));
@@ -254,8 +256,8 @@ KDA_DEVICE void rec_body(const Params &p, unsigned char *smem_raw) {
                         const int j = MO::rev ? j0 + 3 - e : j0 + e;
                         const bool on = j < rows && (!slow || e == only);
                         if (!slow) G += gs[e];
-                        wf[e] = on ? (slow ? 1.f : __expf(-G)) * p.wr_scale : 0.f;
-                        rf[e] = (slow ? 1.f : __expf(G)) * p.rd_scale;
+                        wf[e] = on ? (slow ? 1.f : expf(-G)) * p.wr_scale : 0.f;
+                        rf[e] = (slow ? 1.f : expf(G)) * p.rd_scale;
                     }
                     float o[4][4], dd[4] = {0.f, 0.f, 0.f, 0.f};  // dd: rd . wr of the token (gradient passes)
 #pragma unroll

@@ -636,3 +636,29 @@ def test_no_sequences_at_all(cuda_lib):
                          None, None, None, None, None, P(dg), None, P(ws), ws.numel(), torch.cuda.current_stream().cuda_stream)
     assert st == 0 and (dg == 0).all()
     assert (kda.lin_bwd(d["q"], d["k"], d["v"], d["g"], d["dy"], d["cu"], cu_seqlens_host=[0])["dg"] == 0).all()
+
+
+def test_fp32_writes_behind_strong_decays(cuda_lib):
+    """A token at the end of a block of strong decays, the only one with a value:
+    the state is k v^T, written as k (v e^-G) and renormalised by e^G, two
+    exponentials within two half steps of 2^-24 and four products: 8 half steps."""
+    T, H = 16, 64
+    d = make((T,), H, H, 64, 64, "f32", s0=False, seed=37)
+    d["g"] = torch.linspace(-2.45, -1.0, H, device="cuda").expand(T, H).contiguous()
+    d["v"][:-1] = 0
+    _, fin = kda.lin_chunk_fwd(d["q"], d["k"], d["v"], d["g"], d["cu"])
+    want = d["k"][-1].double()[:, :, None] * d["v"][-1].double()[:, None]
+    assert ((fin[0].double() - want).abs() <= 8 * 2.0 ** -24 * want.abs()).all()
+
+
+def test_fp32_decay_of_a_single_step(cuda_lib):
+    """Nothing written: the state is S e^g, an exponential within two half steps of
+    2^-24 and a product: 3 half steps."""
+    N, H = 2, 64
+    d = make((1,) * N, H, H, 64, 64, "f32", seed=38)
+    d["g"] = torch.linspace(-80.0, 0.0, N * H, device="cuda").view(N, H).contiguous()
+    d["k"].zero_()
+    s = d["s0"].sign() * (d["s0"].abs() + 0.01)  # (so that e^-80 of it is a normal number)
+    want = s.double() * d["g"].double().exp()[:, :, None, None]
+    kda.lin_decode_step(d["q"], d["k"], d["v"], d["g"], s)
+    assert ((s.double() - want).abs() <= 3 * 2.0 ** -24 * want.abs()).all()
