@@ -156,14 +156,26 @@ KDA_DEVICE int gate_of(const Params &p) {
     if (!p.gate) return GATE_NONE;
     return (p.flags & KDA_NORM_GATE_SIGMOID) ? GATE_SIGMOID : (p.flags & KDA_NORM_GATE_SILU) ? GATE_SILU : GATE_GIVEN;
 }
-// 1 / (1 + exp(-z)) of a pair, with the approximate exponential and reciprocal
-// (each off by an ulp or two): IEEE division would be a third of the gated
-// kernels' instructions.
+// 1 / (1 + exp(-z)) of a pair, with the approximate reciprocal (an ulp; 0 below
+// 2^-126): IEEE division would be a third of the gated kernels' instructions.  The
+// exponential is that of the rounded z log2 e, off by up to 2^-18.  bf16 rows, whose
+// results keep 8 bits, take it as it is; fp32 rows multiply it by 2 to the power of
+// what was rounded away, 1 + lo ln 2, which costs them nothing (6553 rows of 5120,
+// norm, gate, residual and norm: 130 us; expf 165, and IEEE division too 145 with
+// rows of 2304 at 229 instead of 127).
+constexpr float kLog2e = 1.4426950408889634f, kLog2eLo = (float)(1.4426950408889634 - (double)kLog2e);
+template <typename T>
 KDA_DEVICE float2 logistic(float2 z) {
-    const float2 t = f2mul(z, pair(-1.4426950408889634f));
+    const float2 t = f2mul(z, pair(-kLog2e));
     float2 e, r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
+    if constexpr (std::is_same<T, float>::value) {
+        // (where z is so large that lo is no such rounding, e is 0 or infinity and has to stay that)
+        float2 lo = f2fma(z, pair(-kLog2eLo), f2fma(z, pair(-kLog2e), make_float2(-t.x, -t.y)));
+        lo = make_float2(fminf(fmaxf(lo.x, -1.f), 1.f), fminf(fmaxf(lo.y, -1.f), 1.f));
+        e = f2mul(e, f2fma(lo, pair(0.6931471805599453f), pair(1.f)));
+    }
     e = f2add(e, pair(1.f));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(e.x));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(e.y));
@@ -253,7 +265,7 @@ __global__ void __launch_bounds__(MT) fwd_kernel(const __grid_constant__ Params 
                     float2 a = wa[i][e];
                     if (g != GATE_NONE) {
                         const float2 zz = get<T, VEC>(z[i], e);
-                        a = f2mul(a, act_of(g, zz, g >= GATE_SIGMOID ? logistic(zz) : pair(0.f)));
+                        a = f2mul(a, act_of(g, zz, g >= GATE_SIGMOID ? logistic<T>(zz) : pair(0.f)));
                     }
                     a = f2mul(a, u[i][e]);
                     u[i][e] = RES ? f2fma(a, pair(f), get<T, VEC>(x[i], e)) : f2mul(a, pair(f));
@@ -365,7 +377,7 @@ __global__ void __launch_bounds__(MT, kBwdCtas<MT>) bwd_kernel(const __grid_cons
         for (int i = 0; i < NV; ++i)
             if (g >= GATE_SIGMOID && live && (i * tpr + t) * VEC < p.D)
 #pragma unroll
-                for (int e = 0; e < NP; ++e) sg[i][e] = logistic(get<T, VEC>(at(1, i), e));
+                for (int e = 0; e < NP; ++e) sg[i][e] = logistic<T>(get<T, VEC>(at(1, i), e));
         auto weighted_act = [&](int i, int e) {             // w_post act(gate)
             return g == GATE_NONE ? wa[i][e] : f2mul(wa[i][e], act_of(g, get<T, VEC>(at(1, i), e), sg[i][e]));
         };

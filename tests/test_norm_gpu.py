@@ -176,3 +176,37 @@ def test_bindings_refuse(cuda_lib):
         kda.block_norm_bwd(None, None, y)
     with pytest.raises(TypeError):
         kda.block_norm(y.half())
+
+
+@pytest.mark.parametrize("act", ["logits", "silu"])
+def test_gates_of_fp32_rows_are_fp32(cuda_lib, act):
+    """Element by element, without a norm: logistic(z) = 1 / (1 + exp(-z)) from an
+    exponential and a reciprocal within two half steps of 2^-24 each and a sum (one),
+    and up to two products: 7 half steps, 8 in the slope's sum."""
+    z = torch.linspace(-87.0, 87.0, 4096, device="cuda").view(2, 2048)
+    y = torch.linspace(0.5, 2.0, 4096, device="cuda").view(2, 2048)
+    kw = dict(post_norm=False, gate=z, gate_logits=act == "logits", gate_silu=act == "silu")
+    out, _ = kda.block_norm(y, **kw)
+    got = kda.block_norm_bwd(torch.ones_like(y), None, y, **kw)
+    zd, yd = z.double(), y.double()
+    s = zd.sigmoid()
+    rest = (-zd).sigmoid()  # 1 - s
+    value, slope = (s, s * rest) if act == "logits" else (zd * s, s * (1 + zd * rest))
+    near_each = lambda a, e, n, room=0.0: ((a.double() - e).abs() - room <= n * 2.0 ** -24 * e.abs()).all()  # noqa: E731
+    assert near_each(out, yd * value, 7)
+    assert near_each(got["dy"], value, 7)
+    # 1 - s cancels for large z: it is off by up to four half steps of s, and the silu's z (1 - s) by z of them
+    assert near_each(got["dgate"], yd * slope, 8, (yd * s * (4 * (zd.abs() + 1 if act == "silu" else 1)) * 2.0 ** -24))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_gates_at_the_ends(cuda_lib, dtype):
+    """Closed and open gates, beyond what an exponential holds, and NaN."""
+    ends = [-float("inf"), -3e38, -1e30, -200.0, 200.0, 1e30, 3e38, float("inf"), float("nan")]
+    z = torch.tensor(ends, device="cuda").to(DT[dtype]).repeat(16).view(2, 72)
+    y = torch.full_like(z, 2.0)
+    out, _ = kda.block_norm(y, post_norm=False, gate=z, gate_logits=True)
+    want = torch.tensor([0.0] * 4 + [2.0] * 4, device="cuda").to(DT[dtype])
+    assert torch.equal(out.view(-1, 9)[:, :8], want.expand(16, 8)) and torch.isnan(out.view(-1, 9)[:, 8]).all()
+    got = kda.block_norm_bwd(torch.ones_like(y), None, y, post_norm=False, gate=z, gate_logits=True)
+    assert (got["dgate"].view(-1, 9)[:, :8] == 0).all() and torch.equal(got["dy"].view(-1, 9)[:, :8], want.expand(16, 8) / 2)
