@@ -210,3 +210,17 @@ def test_gates_at_the_ends(cuda_lib, dtype):
     assert torch.equal(out.view(-1, 9)[:, :8], want.expand(16, 8)) and torch.isnan(out.view(-1, 9)[:, 8]).all()
     got = kda.block_norm_bwd(torch.ones_like(y), None, y, post_norm=False, gate=z, gate_logits=True)
     assert (got["dgate"].view(-1, 9)[:, :8] == 0).all() and torch.equal(got["dy"].view(-1, 9)[:, :8], want.expand(16, 8) / 2)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("R,D", [(15001, 256), (4001, 1000), (1003, 2304), (1000, 4096), (401, 2055), (1001, 5120), (910, 8192),
+                                 (330, 9000), (310, 16384), (950, 4097)])
+def test_several_rows_per_cta(cuda_lib, dtype, R, D):
+    """Two or more rows for each group of threads, in every split of a row, of one warp, of
+    several and with several vectors per thread: the loops over rows, with what
+    they request ahead."""
+    d, kw, dr, dh = make(R, D, dtype, "silu", True, True, True)
+    both(d, kw, "silu", dr, dh, dtype, eps=1e-3)
+    kw.update(pre_norm=False)
+    d.update(pre_weight=None, residual=None)
+    both(d, kw, "logits", dr, None, dtype, eps=1e-3)
