@@ -385,9 +385,14 @@ int kda_bwd(const void *q, const void *k, const void *v, const void *g, const vo
  *
  * Rounding (BF16): fp32 accumulation throughout; the products inside a
  * 128-token chunk and the state that q reads are rounded to bf16 once as
- * operands (outputs within about 2.6e-3 of exact in the 2-norm), the carried
- * and returned states are fp32 with products of two bf16 parts (about 4e-6).
- * F32 inputs are computed in fp32 throughout.
+ * operands (outputs within about 2.6e-3 of exact in the 2-norm, of which the
+ * output's own rounding is 1.7e-3), the carried and returned states are fp32
+ * with products of two bf16 parts (about 4e-6).  The tensor cores truncate where
+ * they accumulate, so a state that decays slowly loses up to 2.6e-6 of itself
+ * (measured 9e-7) for each 128-token chunk that it remembers inside a window:
+ * about 2e-5 where memories end after 20 chunks, 1e-3 after 131072 tokens of one
+ * sign without any decay.  F32 inputs are computed in fp32 throughout (1e-7 to
+ * 4e-7).
  */
 #define KDA_LIN_DECAY_PER_HEAD 1 /* g is [H] (and dg [H]): the same decay at every token */
 

@@ -662,3 +662,27 @@ def test_fp32_decay_of_a_single_step(cuda_lib):
     want = s.double() * d["g"].double().exp()[:, :, None, None]
     kda.lin_decode_step(d["q"], d["k"], d["v"], d["g"], s)
     assert ((s.double() - want).abs() <= 3 * 2.0 ** -24 * want.abs()).all()
+
+
+def test_slow_decays_over_many_chunks(cuda_lib):
+    """One window of 256 chunks per head, decays from forgetting at once to none,
+    values of one sign, so that no rounding averages out.  The tensor cores
+    truncate where they accumulate: a chunk's 16 products take up to 16 x 2^-23 of
+    the state, and the sum of its decays is rounded by up to 2^-20 (in powers of
+    two, under 32 in absolute value): 1.9e-6 + 2^-20 ln 2 = 2.6e-6 for each chunk
+    that is remembered, on top of the parts' 2e-5."""
+    T, H, D, block = 32768, 148, 64, 1024
+    gen = torch.Generator(device="cuda").manual_seed(39)
+    rand = lambda *s: torch.rand(*s, generator=gen, device="cuda").bfloat16()  # noqa: E731
+    k, v = rand(T, 1, D), rand(T, H, D)
+    g = -torch.logspace(0, -6, H, device="cuda").bfloat16()
+    g[-1] = 0
+    _, fin = kda.lin_chunk_fwd(k, k, v, g, torch.tensor([0, T], dtype=torch.int32, device="cuda"))
+    gd, want = g.double(), torch.zeros(H, D, D, dtype=torch.float64, device="cuda")
+    behind = (torch.arange(block - 1, -1, -1, device="cuda")[:, None] * gd).exp()
+    for t in range(0, T, block):
+        want *= (block * gd).exp()[:, None, None]
+        want += torch.einsum("tk,thv->hkv", k[t:t + block, 0].double(), behind[:, :, None] * v[t:t + block].double())
+    off = (fin[0].double() - want).norm(dim=(1, 2)) / want.norm(dim=(1, 2))
+    remembered = (-(128 * gd).expm1()).clamp_min(128 / T).reciprocal()  # chunks: the sum of exp(128 g i), T / 128 at most
+    assert (off <= 2e-5 + 2.6e-6 * remembered).all(), off.tolist()
