@@ -65,7 +65,8 @@ struct Params {
     const float *init;      // [num_seqs][H] states or null; transposed ([DB][DA]) when init_t
     float *final_state;     // same layout, or null
     int init_t;
-    float *win_state;       // [W][H] states [DA][DB]: Z out of the summary, incoming states after the scan
+    float *win_state;       // [W][H] states [DA][DB]: Z out of the summary, incoming states after the scan (with
+                            // by_seq not one per window, and not to be read whatever the offsets say)
     int win_t;              // the pass reads them transposed
     float *gamma;           // [W][H]
     float *start_copy;      // [W][H] states or null.  When final_state is init, the summary keeps here the

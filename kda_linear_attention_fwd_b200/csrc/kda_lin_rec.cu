@@ -423,7 +423,7 @@ KDA_DEVICE void rec_body(const Params &p, unsigned char *smem_raw) {
         for (int i = first; i < end; ++i) {
             const int n = MO::rev ? end - 1 - (i - first) : i;
             const int a = seg_a(n), b = seg_b(n, a);
-            const bool from_win = MO::rev ? p.cu[n + 1] > t1 : n < lo;
+            const bool from_win = !p.by_seq && (MO::rev ? p.cu[n + 1] > t1 : n < lo);
             const bool ends = MO::rev ? n >= lo : p.cu[n + 1] <= t1;
             if (from_win)
                 load_state(p.win_state + win_at, p.win_t);

@@ -525,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
         const bool mine = row < DA;
         float gamma = 1.f;
         segments([&](int n, int a, int b, int qa, int qb) {
-            const bool from_win = C::rev ? p.cu[n + 1] > t1 : n < lo;
+            const bool from_win = !p.by_seq && (C::rev ? p.cu[n + 1] > t1 : n < lo);
             const bool ends = C::rev ? n >= lo : p.cu[n + 1] <= t1;
             const size_t win_at = ((size_t)w * H + h) * (DA * DB), seq_at = ((size_t)n * H + h) * (DA * DB);
             const float *src;

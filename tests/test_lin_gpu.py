@@ -686,3 +686,30 @@ def test_slow_decays_over_many_chunks(cuda_lib):
     off = (fin[0].double() - want).norm(dim=(1, 2)) / want.norm(dim=(1, 2))
     remembered = (-(128 * gd).expm1()).clamp_min(128 / T).reciprocal()  # chunks: the sum of exp(128 g i), T / 128 at most
     assert (off <= 2e-5 + 2.6e-6 * remembered).all(), off.tolist()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_sequences_that_hold_none_of_the_tokens(cuda_lib, dtype):
+    """Tokens, but all of them behind the last sequence, and every sequence empty."""
+    d = make((70, 0, 130), 2, 1, 64, 128, dtype, per_head=True, seed=40)
+    cu = torch.zeros(4, dtype=torch.int32, device="cuda")
+    out = torch.full_like(d["v"], 7.0)
+    for x in ("q", "k", "v", "dy"):
+        d[x].fill_(float("nan"))
+    args = [d[x] for x in ("q", "k", "v", "g")]
+    _, fin = kda.lin_chunk_fwd(*args, cu, initial_state=d["s0"], out=out)
+    assert torch.equal(fin, d["s0"]) and (out == 7.0).all()
+    got = kda.lin_bwd(*args, d["dy"], cu, initial_state=d["s0"], d_final_state=d["dsf"])
+    assert torch.equal(got["ds0"], d["dsf"])
+    assert all((got[x] == 0).all() for x in ("dq", "dk", "dv", "dg"))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_state_in_place_of_whole_sequences(cuda_lib, dtype):
+    """final_state = initial_state where a CTA takes a whole sequence."""
+    d = make((257, 0, 64, 500, 1, 130, 128, 300, 90, 411, 2, 350), 48, 24, 64, 64, dtype, seed=41)
+    args = [d[x] for x in ("q", "k", "v", "g")]
+    want, fin = kda.lin_chunk_fwd(*args, d["cu"], initial_state=d["s0"], cu_seqlens_host=d["host"])
+    s = d["s0"].clone()
+    out, got = kda.lin_chunk_fwd(*args, d["cu"], initial_state=s, final_state=s, cu_seqlens_host=d["host"])
+    assert got is s and torch.equal(out, want) and torch.equal(s, fin)
