@@ -954,7 +954,11 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                 ++it;
             });
         });
-        if (*dead)  // loads in flight land before the CTA ends (bounded)
+        // nothing in flight arrives behind the CTA's end: the last products' arrivals, the last of which are
+        // their tiles' releases, and, when a wait gave up, the loads (bounded)
+        for (int x = max(0, it * C::tiles - C::slots); x < it * C::tiles; ++x)
+            wait(ctl.free[x % C::slots], (uint32_t)(x / C::slots) & 1u);
+        if (*dead)
             for (int x = max(0, it * C::tiles - C::slots); x < it * C::tiles; ++x) {
                 const int c = x / C::tiles;
                 if (x % C::tiles == C::tV) mbar_wait(smem_u32(&ctl.v_full[c % kVBars]), (uint32_t)(c / kVBars) & 1u);

@@ -2,7 +2,8 @@
 model: its warps as generators that wait on mbarriers by parity, its loads and
 products as events that end in any order the hardware allows, run under random
 schedules.  What is looked for: a tile read that is not (or no longer) in its
-slot, a load over a tile that somebody still has to read, and standstill.
+slot, a load over a tile that somebody still has to read, anything in flight
+when all warps have ended, and standstill.
 
 The roles, waits and arrivals are those of the kernel, line by line; a chunk is
 its number of 32-token quarters and whether its last one is cut short.
@@ -101,6 +102,8 @@ class Ring:
                     self.full[s].arrive()
                 self.readers[s] = 2 * self.chunks[c][0] if name == "V" else 0  # reads by the V groups
                 self.loads.append((bar, s, (c, name)))
+        for x in range(max(0, len(self.chunks) * self.tiles - self.slots), len(self.chunks) * self.tiles):
+            yield self.free[x % self.slots], x // self.slots & 1
 
     def v_warp(self, grp, w):
         quarters = 0
@@ -131,12 +134,13 @@ class Ring:
             self.p_full[ab].arrive()
 
     def s_role(self):
-        for c in range(len(self.chunks)):
+        for c in range(len(self.chunks) + 1):  # (the last time for the state behind the segment)
             if c > 0:
                 yield self.kv_done, (c - 1) & 1
                 if self.out:
                     yield self.qs_done, (c - 1) & 1
-            self.s_full.arrive()
+            if c < len(self.chunks):
+                self.s_full.arrive()
 
     def o_role(self):
         for c in range(len(self.chunks)):
@@ -262,6 +266,8 @@ class Ring:
                 self.step_pipe(who)
             else:
                 waits[who] = next(roles[who], None)
+            if not any(waits.values()):  # every warp is at the CTA's end
+                assert not self.loads and not any(self.pipes.values()), "in flight behind the CTA's end"
         assert all(w is None for w in waits.values()), f"standstill: {[i for i, w in waits.items() if w is not None]}"
 
 
