@@ -468,7 +468,8 @@ def lin_chunk_fwd(q, k, v, g, cu_seqlens, *, scale=1.0, initial_state=None, fina
     S <- exp(g) S + k v^T, o = S^T (scale q).  q, k [T, Hk, dk]; v [T, H, dv],
     H a multiple of Hk; g [T, H], or [H] for the same decay at every token;
     cu_seqlens int32 [N+1] (device).  Returns (out, final_state); final_state
-    may be initial_state itself."""
+    may be initial_state itself.  A device wait that gave up is recorded in the
+    workspace: pass one to ask chunk_fwd_check for it."""
     lib = load()
     dev, T, H, Hk, dk, dv, flags, code, ptrs = _lin_shapes(q, k, v, g)
     N = cu_seqlens.shape[0] - 1
@@ -510,7 +511,8 @@ def lin_bwd_workspace_size(total_tokens, num_seqs, H, Hk, dk, dv) -> int:
 def lin_bwd(q, k, v, g, dy, cu_seqlens, *, scale=1.0, initial_state=None, d_final_state=None,
             cu_seqlens_host=None, workspace=None, stream=None):
     """Gradients of lin_chunk_fwd: a dict of dq, dk [T, Hk, dk], dv [T, H, dv],
-    dg (the shape of g), all in the inputs' dtype, and ds0 [N, H, dk, dv] fp32."""
+    dg (the shape of g), all in the inputs' dtype, and ds0 [N, H, dk, dv] fp32.
+    Waits that gave up: as lin_chunk_fwd."""
     lib = load()
     dev, T, H, Hk, dk, dv, flags, code, ptrs = _lin_shapes(q, k, v, g)
     N = cu_seqlens.shape[0] - 1
@@ -542,10 +544,16 @@ def _norm_rows(name, t, shape, dtype, dev):
     D = shape[-1]
     if t.is_contiguous():
         return t.data_ptr(), D
-    rows = t.flatten(0, -2) if t.dim() != 2 else t
+    rows = t.unsqueeze(0) if t.dim() == 1 else t.flatten(0, -2) if t.dim() != 2 else t
     if rows.data_ptr() != t.data_ptr() or rows.stride(1) != 1 or (rows.shape[0] > 1 and rows.stride(0) < D):
         raise ValueError(f"{name}: rows must be contiguous and evenly spaced, got strides {t.stride()}")
     return t.data_ptr(), max(rows.stride(0), D)
+
+
+def _row_length(shape):
+    if not shape:
+        raise ValueError("y has no rows: want [..., D]")
+    return shape[-1]
 
 
 def _norm_flags(post_norm, post_weight, pre_norm, pre_weight, gate, gate_logits, gate_silu):
@@ -569,7 +577,7 @@ def block_norm(y, *, post_norm=True, post_weight=None, gate=None, gate_logits=Fa
     lib = load()
     dev = _device(y)
     shape = y.shape
-    D = shape[-1]
+    D = _row_length(shape)
     code, dt = _code(y), y.dtype
     flags = _norm_flags(post_norm, post_weight, pre_norm, pre_weight, gate, gate_logits, gate_silu)
     p_y, s_y = _norm_rows("y", y, shape, dt, dev)
@@ -596,7 +604,7 @@ def block_norm_bwd(dout, dnormed, y, *, post_norm=True, post_weight=None, gate=N
     lib = load()
     dev = _device(y)
     shape = y.shape
-    D = shape[-1]
+    D = _row_length(shape)
     code, dt = _code(y), y.dtype
     flags = _norm_flags(post_norm, post_weight, pre_norm, pre_weight, gate, gate_logits, gate_silu)
     if dout is None and dnormed is None:

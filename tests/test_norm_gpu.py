@@ -224,3 +224,16 @@ def test_several_rows_per_cta(cuda_lib, dtype, R, D):
     kw.update(pre_norm=False)
     d.update(pre_weight=None, residual=None)
     both(d, kw, "logits", dr, None, dtype, eps=1e-3)
+
+
+def test_single_rows_and_scalars(cuda_lib):
+    """A tensor of one dimension is one row; a strided one or a scalar is refused as such."""
+    y = torch.randn(64, device="cuda")
+    out, normed = kda.block_norm(y, pre_norm=True)
+    assert out.shape == normed.shape == (64,)
+    near(out[None], O.block_norm(np32(y)[None])[0], TOL["f32"], "out")
+    for bad in (y[::2], y[0]):
+        with pytest.raises(ValueError):
+            kda.block_norm(bad)
+        with pytest.raises(ValueError):
+            kda.block_norm_bwd(bad, None, bad)
