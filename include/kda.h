@@ -385,7 +385,7 @@ int kda_bwd(const void *q, const void *k, const void *v, const void *g, const vo
  *
  * Rounding (BF16): fp32 accumulation throughout; the products inside a
  * 128-token chunk and the state that q reads are rounded to bf16 once as
- * operands (outputs within about 2.6e-3 of exact in the 2-norm, of which the
+ * operands (outputs within about 2.4e-3 of exact in the 2-norm, of which the
  * output's own rounding is 1.7e-3), the carried and returned states are fp32
  * with products of two bf16 parts (about 4e-6).  The tensor cores truncate where
  * they accumulate, so a state that decays slowly loses up to 2.6e-6 of itself

@@ -11,7 +11,12 @@
 //   S   = exp(c_last) S + W^T (w V)      (the decay kept aside, see carried)
 // The state stays in TMEM in fp32 for the whole window.  w V is split into two
 // bf16 parts (hi + lo, 2^-16 of the value), so the state that is carried and
-// returned has fp32-like accuracy; only the copy that R reads is one bf16.
+// returned has fp32-like accuracy, but that the tensor core truncates where it
+// accumulates: up to 16 x 2^-23 of the state for every chunk that it remembers
+// (measured 9e-7).  P and the copy of the state that R reads are one bf16, as two
+// parts would double their products (R S and P V) and the copy's 32 KB; the
+// outputs, bf16 themselves, are 2.3e-3 from exact with it and 1.7e-3 by their own
+// rounding alone.
 // Reversed passes (the gradient) keep the tokens in their rows and flip the
 // triangle: c_t is then summed from the chunk's last token back to t.
 //
@@ -39,10 +44,11 @@
 // columns, A (P in its place) two buffers of 128, O 128.
 //
 // Measured on one B200 (6531 GB/s copied, 1653 TFLOP/s): 131072 x 32 heads of
-// 128 x 128 in 1570 us (floor 658; summary 345, scan 10, outputs 1000) at the
-// 1000 W cap (1.75 GHz); 30202 tokens in 8 ragged sequences x 32 heads 300 us
-// (floor 119).  A chunk of the outputs' pass takes 4.4 us (its products 1.4, its
-// bytes 3.0), one of a summary 2.4; the tensor pipe is active 22% of the time.  What is
+// 128 x 128 in 1450 to 1525 us (floor 658; summary 345, scan 10, outputs 970) at
+// the 1000 W cap (1.75 GHz); 30202 tokens in 8 ragged sequences x 32 heads 300 us
+// (floor 119).  A chunk of the outputs' pass takes 4.3 us (its products 1.4, its
+// bytes 3.0), one of a summary 2.4; on the ragged batch the tensor pipe is active
+// 27% of the time and DRAM 41%.  What is
 // left is the chain of a chunk: w V -> state -> its copy -> R S -> scaling ->
 // P V -> O, with the waits and the code of each step.
 //
