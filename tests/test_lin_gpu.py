@@ -713,3 +713,34 @@ def test_state_in_place_of_whole_sequences(cuda_lib, dtype):
     s = d["s0"].clone()
     out, got = kda.lin_chunk_fwd(*args, d["cu"], initial_state=s, final_state=s, cu_seqlens_host=d["host"])
     assert got is s and torch.equal(out, want) and torch.equal(s, fin)
+
+
+def test_two_streams_in_one_capture(cuda_lib):
+    """Calls on the capturing stream and on one that it forks, side by side in a
+    graph: the fills of the forked call are captured with it."""
+    d, e = (make((333, 50), 4, 2, 64, 64, "bf16", seed=s) for s in (42, 43))
+    args = lambda x: [x[n] for n in ("q", "k", "v", "g")]  # noqa: E731
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+
+    def work():
+        side.wait_stream(main)
+        got = kda.lin_bwd(*args(d), d["dy"], d["cu"], initial_state=d["s0"], stream=side)
+        out = kda.lin_chunk_fwd(*args(e), e["cu"], initial_state=e["s0"])
+        normed = kda.block_norm(d["v"], gate=d["dy"], gate_logits=True, stream=side)[0]
+        main.wait_stream(side)
+        return [*got.values(), *out, normed]
+
+    torch.cuda.synchronize()
+    with torch.cuda.stream(main):
+        want = [x.clone() for x in work()]
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=main):
+            got = work()
+    for _ in range(3):
+        for x in got:
+            x.fill_(float("nan"))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
